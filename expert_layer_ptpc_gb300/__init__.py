@@ -6,4 +6,4 @@ torch tensors into those calls. Importing the package loads nothing; the
 library is loaded on first use and a missing build raises.
 """
 
-__all__ = ["binding", "synthetic", "build"]
+__all__ = ["attention", "binding", "synthetic", "build"]

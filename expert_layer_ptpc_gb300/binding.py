@@ -17,6 +17,7 @@ from . import build as _build
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
+MOE_DTYPE_E4M3 = 2   # key-value caches only
 MOE_GEMM_GATEUP_SWIGLU = 0
 MOE_GEMM_DOWN = 1
 
@@ -37,6 +38,20 @@ class moe_dims(ctypes.Structure):
 class moe_prenorm(ctypes.Structure):
     _fields_ = [("residual", ctypes.c_void_p), ("gamma", ctypes.c_void_p),
                 ("eps", ctypes.c_float), ("residual_out", ctypes.c_void_p)]
+
+
+class moe_rotary_plan(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("neighbours", ctypes.c_int32)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -81,6 +96,15 @@ _SIGNATURES = {
     "moe_quant_blocks": (_I, [_P, _I64, _I, _I, _P, _P, _P]),
     "moe_quant_weight_blocks": (_I, [_P, _I64, _I, _P, _P, _P]),
     "moe_grouped_gemm_scaled": (_I, [_I, _P, _P, _I64, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_rotary": (_I, [_P, _P, _I, _I, _P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _I,
+                        _P]),
+    "moe_kv_write": (_I, [_P, _P, _I, _P, _I64, _P, _I64, _P]),
+    "moe_rotary_kv_write": (_I, [_P, _P, _P, _P, _I, _P, _I64, _I, _P, _I64, _P, _I64, _P,
+                                 _I64, _P]),
+    "moe_kv_read": (_I, [_P, _P, _I64, _I, _P, _I, _I64, _P, _P, _P]),
+    "moe_paged_attention_workspace_size": (_SZ, [_P, _I, _I]),
+    "moe_paged_attention": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _I, _P, ctypes.c_float, _I,
+                                 _P, _P, _P, _SZ, _P]),
 }
 
 MOE_SCALE_PTPC, MOE_SCALE_SUB512, MOE_SCALE_BLOCK128 = 0, 1, 2
@@ -587,3 +611,183 @@ def moe_workspace_status(ws, stream=None):
     st = load_library().moe_workspace_status(
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream), ctypes.byref(detail))
     return st, detail.value
+
+
+# ---------------------------------------------------------------------------
+# Attention operators. `plan` and `cache` are moe_rotary_plan and moe_kv_cache
+# structures (expert_layer_ptpc_gb300.attention builds them from tensors).
+# ---------------------------------------------------------------------------
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the kernel will run on, so that
+    its memory is reused in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _need_heads(t, heads, head_dim, name):
+    """A [T, heads, head_dim] bf16 tensor whose tokens may be strided (a slice
+    of a wider projection); returns the token stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    n, h, d = t.shape
+    if h != heads or d != head_dim:
+        raise ValueError(f"{name} must be [T, {heads}, {head_dim}], got {tuple(t.shape)}")
+    stride, sh, sd = t.stride()
+    if (sd != 1 and d != 1) or (sh != d and h != 1):
+        raise ValueError(f"{name}'s heads must be contiguous within a token")
+    # a dimension of size one can carry any stride
+    return stride if n > 1 else h * d
+
+
+def _need_slots(slots, T, cache):
+    _need(slots, torch.int32, "slots")
+    if slots.numel() != T:
+        raise ValueError(f"slots must have {T} entries, got {slots.numel()}")
+
+
+def _need_positions(positions, plan, T):
+    _need(positions, torch.int32, "positions")
+    if tuple(positions.shape) != (plan.axes, T):
+        raise ValueError(f"positions must be [{plan.axes}, {T}], got {tuple(positions.shape)}")
+
+
+def _need_table(table, batch):
+    """A [batch, max_pages] int32 block table; returns (row stride, max_pages)."""
+    if not table.is_cuda:
+        raise ValueError("block_table must be a CUDA tensor")
+    if table.dtype != torch.int32:
+        raise ValueError(f"block_table must be {torch.int32}, got {table.dtype}")
+    n, pages = table.shape
+    if n != batch:
+        raise ValueError(f"block_table must have {batch} rows, got {n}")
+    stride, inner = table.stride()
+    if inner != 1 and pages > 1:
+        raise ValueError("block_table's rows must be contiguous")
+    return (stride if n > 1 else pages), pages
+
+
+def moe_rotary(plan, positions, q, k=None, inverse=False, q_out=None, k_out=None, stream=None):
+    """q [T, heads, head_dim] bf16 (and k) rotated by positions [axes, T];
+    returns (q_out, k_out), k_out None without k."""
+    T, hq, d = q.shape
+    q_stride = _need_heads(q, hq, d, "q")
+    _need_positions(positions, plan, T)
+    if q_out is None:
+        q_out = _empty((T, hq, d), torch.bfloat16, q.device, stream)
+    qo_stride = _need_heads(q_out, hq, d, "q_out")
+    if q_out.shape[0] != T:
+        raise ValueError("q_out must have as many tokens as q")
+    hk = k_stride = ko_stride = 0
+    k_ptr = ko_ptr = None
+    if k is not None:
+        hk = k.shape[1]
+        k_stride = _need_heads(k, hk, d, "k")
+        if k_out is None:
+            k_out = _empty((T, hk, d), torch.bfloat16, q.device, stream)
+        ko_stride = _need_heads(k_out, hk, d, "k_out")
+        if k.shape[0] != T or k_out.shape[0] != T:
+            raise ValueError("k and k_out must have as many tokens as q")
+        k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _check("moe_rotary", load_library().moe_rotary(
+        ctypes.byref(plan), positions.data_ptr(), T, d, q.data_ptr(), q_stride, hq,
+        q_out.data_ptr(), qo_stride, k_ptr, k_stride, hk, ko_ptr, ko_stride,
+        int(bool(inverse)), _stream(stream)))
+    return q_out, k_out
+
+
+def moe_kv_write(cache, k, v, slots, stream=None):
+    """k, v [T, heads, head_dim] bf16 into the cache's slots [T] int32."""
+    T = k.shape[0]
+    k_stride = _need_heads(k, cache.heads, cache.head_dim, "k")
+    v_stride = _need_heads(v, cache.heads, cache.head_dim, "v")
+    if v.shape[0] != T:
+        raise ValueError("k and v must have as many tokens")
+    _need_slots(slots, T, cache)
+    _check("moe_kv_write", load_library().moe_kv_write(
+        ctypes.byref(cache), slots.data_ptr(), T, k.data_ptr(), k_stride, v.data_ptr(),
+        v_stride, _stream(stream)))
+
+
+def moe_rotary_kv_write(plan, positions, cache, q, k, v, slots, q_out=None, stream=None):
+    """q rotated (returned), k rotated and v as it is into the cache."""
+    T, hq, d = q.shape
+    q_stride = _need_heads(q, hq, cache.head_dim, "q")
+    k_stride = _need_heads(k, cache.heads, d, "k")
+    v_stride = _need_heads(v, cache.heads, d, "v")
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v must have as many tokens")
+    _need_positions(positions, plan, T)
+    _need_slots(slots, T, cache)
+    if q_out is None:
+        q_out = _empty((T, hq, d), torch.bfloat16, q.device, stream)
+    qo_stride = _need_heads(q_out, hq, d, "q_out")
+    if q_out.shape[0] != T:
+        raise ValueError("q_out must have as many tokens as q")
+    _check("moe_rotary_kv_write", load_library().moe_rotary_kv_write(
+        ctypes.byref(plan), positions.data_ptr(), ctypes.byref(cache), slots.data_ptr(), T,
+        q.data_ptr(), q_stride, hq, q_out.data_ptr(), qo_stride, k.data_ptr(), k_stride,
+        v.data_ptr(), v_stride, _stream(stream)))
+    return q_out
+
+
+def moe_kv_read(cache, block_table, offsets, rows, k_out=None, v_out=None, stream=None):
+    """Contexts offsets[b]..offsets[b + 1] of the cache as bf16 (k, v)
+    [rows, heads, head_dim]."""
+    _need(offsets, torch.int32, "offsets")
+    batch = offsets.numel() - 1
+    stride, pages = _need_table(block_table, batch)
+    shape = (rows, cache.heads, cache.head_dim)
+    outs = []
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = _empty(shape, torch.bfloat16, offsets.device, stream)
+        _need(t, torch.bfloat16, n)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
+        outs.append(t)
+    _check("moe_kv_read", load_library().moe_kv_read(
+        ctypes.byref(cache), block_table.data_ptr(), stride, pages, offsets.data_ptr(), batch,
+        rows, outs[0].data_ptr(), outs[1].data_ptr(), _stream(stream)))
+    return tuple(outs)
+
+
+def moe_paged_attention_workspace_size(cache, batch, q_heads):
+    """Workspace bytes of moe_paged_attention (0 for an unsupported shape)."""
+    return load_library().moe_paged_attention_workspace_size(ctypes.byref(cache), batch, q_heads)
+
+
+def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=None, lse=None,
+                        ws=None, stream=None):
+    """Attention of one new token per context: q [batch, q_heads, head_dim]
+    bf16 over the cached tokens; returns out, of q's shape. `lse`: optional
+    [batch, q_heads] fp32 tensor that receives the log of the sums."""
+    batch, hq, d = q.shape
+    q_stride = _need_heads(q, hq, cache.head_dim, "q")
+    stride, pages = _need_table(block_table, batch)
+    _need(lengths, torch.int32, "lengths")
+    if lengths.numel() != batch:
+        raise ValueError(f"lengths must have {batch} entries, got {lengths.numel()}")
+    if out is None:
+        out = _empty((batch, hq, d), torch.bfloat16, q.device, stream)
+    else:
+        _need(out, torch.bfloat16, "out")
+        if tuple(out.shape) != (batch, hq, d):
+            raise ValueError(f"out must be {(batch, hq, d)}, got {tuple(out.shape)}")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (batch, hq):
+            raise ValueError(f"lse must be {(batch, hq)}, got {tuple(lse.shape)}")
+    if ws is None:
+        need = moe_paged_attention_workspace_size(cache, batch, hq)
+        ws = _empty(max(need, 1), torch.uint8, q.device, stream)
+    _check("moe_paged_attention", load_library().moe_paged_attention(
+        ctypes.byref(cache), q.data_ptr(), q_stride, batch, hq, block_table.data_ptr(), stride,
+        pages, lengths.data_ptr(), float(scale), int(window), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return out

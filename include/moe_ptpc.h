@@ -60,7 +60,11 @@ typedef enum moe_status {
   MOE_ERR_TIMEOUT = -5      /* a kernel's bounded wait expired             */
 } moe_status;
 
-typedef enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
+typedef enum moe_dtype {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_F32 = 1,
+  MOE_DTYPE_E4M3 = 2 /* key-value caches only */
+} moe_dtype;
 
 typedef enum moe_gemm_kind {
   MOE_GEMM_GATEUP_SWIGLU = 0, /* h = silu(x Wg^T) * (x Wu^T), fp32 out      */
@@ -588,6 +592,151 @@ MOE_API int moe_grouped_gemm_scaled(int scale_kind, const uint8_t* A, const floa
                                     int64_t a_rows, const uint8_t* W, const float* w_scale,
                                     const int32_t* group_offsets, int groups, int N, int K,
                                     float* out, moe_stream_t stream);
+
+/*
+ * Attention beside the MoE block: rotary positions with several axes, a
+ * paged key-value cache and attention of one new token over it ("Ultimate
+ * Latency Optimization of Qwen3 and Qwen3-VL on AMD MI300X Series": fused
+ * MRoPE of q and k; the paged attention and FP8 cache types the pages name
+ * beside the MoE path). No formulas on the pages; the definitions are here.
+ *
+ * Rotation. A head's first rot_dim elements form rot_dim / 2 pairs: pair i is
+ * (x[i], x[i + rot_dim/2]), or (x[2i], x[2i + 1]) with `neighbours`. With
+ * p = positions[pair_axis[i], t] the pair turns by the angle
+ *   a = 2 pi * frac(p * turns[i] / 2^64),
+ *   y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a     (inverse: -a)
+ * in fp32, rounded once to bf16; elements from rot_dim on are copied. turns
+ * holds each frequency as a fraction of a turn per position, in units of
+ * 2^-64: turns[i] = round(inv_freq[i] / (2 pi) * 2^64) mod 2^64, so that the
+ * angle of any 32-bit position is exact to 2^-31 turns. The inverse is the
+ * transpose of the rotation, hence also its gradient.
+ */
+typedef struct moe_rotary_plan {
+  const uint64_t* turns;     /* [rot_dim / 2], device                        */
+  const uint8_t* pair_axis;  /* [rot_dim / 2], device; an axis outside
+                                [0, axes) leaves its pair unrotated          */
+  int32_t axes;              /* 1 .. 8                                       */
+  int32_t rot_dim;           /* a positive multiple of 16, <= head_dim       */
+  int32_t neighbours;        /* 0: pairs (i, i + rot_dim/2); 1: (2i, 2i + 1) */
+} moe_rotary_plan;
+
+/*
+ * moe_rotary - rotate the heads of q, and of k when it is not NULL.
+ *   positions [axes, T] int32. q [T, q_heads, head_dim] bf16 with q_stride
+ *   elements between tokens (heads contiguous), q_out alike with
+ *   q_out_stride; k, k_out likewise. An output may alias its input when the
+ *   strides agree; otherwise they must not overlap.
+ * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, strides smaller
+ *         than a token's heads or not multiples of 8, bad plan, T < 0, heads
+ *         < 1), MOE_ERR_UNSUPPORTED (head_dim not a multiple of 16 or > 512,
+ *         more than 65536 elements a token). T == 0 is a no-op.
+ */
+MOE_API int moe_rotary(const moe_rotary_plan* plan, const int32_t* positions, int T,
+                       int head_dim, const uint16_t* q, int64_t q_stride, int q_heads,
+                       uint16_t* q_out, int64_t q_out_stride, const uint16_t* k,
+                       int64_t k_stride, int k_heads, uint16_t* k_out,
+                       int64_t k_out_stride, int inverse, moe_stream_t stream);
+
+/*
+ * A paged key-value cache. Slot s is offset s % page_size of page
+ * s / page_size; a page holds its tokens head by head:
+ *   k, v [pages, heads, page_size, head_dim], e4m3 codes or bf16;
+ *   k_scale, v_scale [pages, heads, page_size] fp32 for e4m3, else NULL:
+ *   one scale per token and head (the PTPC quantiser of moe_quant_ptpc on the
+ *   head's row), value = code * scale.
+ * head_dim is 64, 128 or 256; page_size a power of two <= 1024; the whole
+ * cache has fewer than 2^31 slots and fewer than 2^32 - 1 rows (pages *
+ * heads * page_size). Entry points return MOE_ERR_INVALID_ARG for null,
+ * misaligned or non-positive fields and MOE_ERR_UNSUPPORTED for the rest.
+ */
+typedef struct moe_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t pages;
+  int32_t heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t dtype;             /* MOE_DTYPE_BF16 or MOE_DTYPE_E4M3             */
+} moe_kv_cache;
+
+/*
+ * moe_kv_write - store T tokens' keys and values, quantised on the way when
+ * the cache is e4m3. k, v [T, heads, head_dim] bf16 with k_stride and
+ * v_stride elements between tokens; slots [T] int32. A token whose slot lies
+ * outside [0, pages * page_size) is not read and not written. Two tokens of
+ * one call in the same slot are outside the contract.
+ * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
+ *         pointers, bad strides, T < 0). T == 0 is a no-op.
+ */
+MOE_API int moe_kv_write(const moe_kv_cache* cache, const int32_t* slots, int T,
+                         const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                         int64_t v_stride, moe_stream_t stream);
+
+/*
+ * moe_rotary_kv_write - moe_rotary of q and k and moe_kv_write of the rotated
+ * keys and the values in one launch: the keys go from fp32 to the cache with
+ * one rounding (to e4m3, or to bf16), without the bf16 rounding in between
+ * that the two calls would add for an e4m3 cache. Every token's q is rotated,
+ * whatever its slot.
+ * Errors: those of moe_rotary and moe_kv_write.
+ */
+MOE_API int moe_rotary_kv_write(const moe_rotary_plan* plan, const int32_t* positions,
+                                const moe_kv_cache* cache, const int32_t* slots, int T,
+                                const uint16_t* q, int64_t q_stride, int q_heads,
+                                uint16_t* q_out, int64_t q_out_stride, const uint16_t* k,
+                                int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                moe_stream_t stream);
+
+/*
+ * moe_kv_read - read contexts back in bf16: out row r of context b (offsets[b]
+ * <= r < offsets[b + 1]) is token r - offsets[b] of that context,
+ *   k_out[r], v_out[r] = bf16_rne(fp32(code * scale))   (bf16: as stored).
+ *   block_table: context b's pages in order, entries block_table[b *
+ *   table_stride + i] for i < max_pages; offsets [batch + 1] int32, ascending,
+ *   offsets[0] = 0; k_out, v_out [rows, heads, head_dim] bf16. Rows from
+ *   offsets[batch] on, tokens past max_pages and pages outside [0, pages)
+ *   read as zeros. Asynchronous on lengths: `rows` is the outputs' size.
+ * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
+ *         pointers, batch < 1, max_pages < 0, rows < 0). rows == 0 is a no-op.
+ */
+MOE_API int moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table,
+                        int64_t table_stride, int max_pages, const int32_t* offsets,
+                        int batch, int64_t rows, uint16_t* k_out, uint16_t* v_out,
+                        moe_stream_t stream);
+
+/*
+ * moe_paged_attention - attention of one new token per context over its cached
+ * keys and values. With kv head h / (q_heads / heads) for query head h and the
+ * tokens j that take part,
+ *   s_j = scale * q[b, h] . k_j,  out[b, h] = sum_j softmax(s)_j v_j,
+ *   lse[b, h] = ln sum_j exp(s_j).
+ * A token takes part if j < lengths[b], j < max_pages * page_size, its page
+ * entry lies in [0, pages), and, with window > 0, j >= lengths[b] - window.
+ * Where none does (or every s_j is -inf), out is 0 and lse is -inf. What
+ * other slots of the cache hold (NaN included) has no influence.
+ *   q [batch, q_heads, head_dim] bf16 with q_stride elements between contexts;
+ *   block_table as for moe_kv_read; lengths [batch] int32 (the new token's own
+ *   key and value are in the cache already and counted); out [batch, q_heads,
+ *   head_dim] bf16; lse [batch, q_heads] fp32 or NULL.
+ *   ws: device workspace of moe_paged_attention_workspace_size bytes, 16-byte
+ *   aligned, of any content; calls in flight at once need workspaces of their
+ *   own.
+ *   Sums, maxima and accumulators are fp32; results do not depend on timing.
+ * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
+ *         pointers, q_heads not a multiple of heads, scale not finite, batch
+ *         < 0, max_pages < 0), MOE_ERR_UNSUPPORTED (batch > 65535),
+ *         MOE_ERR_WORKSPACE. batch == 0 is a no-op.
+ */
+MOE_API size_t moe_paged_attention_workspace_size(const moe_kv_cache* cache, int batch,
+                                                  int q_heads);
+MOE_API int moe_paged_attention(const moe_kv_cache* cache, const uint16_t* q,
+                                int64_t q_stride, int batch, int q_heads,
+                                const int32_t* block_table, int64_t table_stride,
+                                int max_pages, const int32_t* lengths, float scale,
+                                int window, uint16_t* out, float* lse, void* ws,
+                                size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -13,3 +13,5 @@ from .blockscale_ref import (BLOCK_K, BLOCK_N, SUBCHANNEL_K,  # noqa: F401
                              blockscale_matmul_ref, grouped_blockscale_ref,
                              quant_blocks_ref, quant_weight_blocks_ref,
                              subchannel_matmul_ref)
+from .attention_ref import (cache_rows_ref, kv_write_ref, paged_attention_ref,  # noqa: F401
+                            rotary_ref)
