@@ -1,12 +1,44 @@
 // Attention of one new token per context over the paged key-value cache.
 //
-//   s_j = scale q . k_j,  m = max_j s_j,  l = sum_j exp(s_j - m),
-//   out = sum_j exp(s_j - m) v_j / l,  lse = m + ln l
+//   s_j = scale q . k_j,  p_j = exp(s_j) / sum_i exp(s_i),  out = sum_j p_j v_j,
+//   lse = ln sum_j exp(s_j)
 //
-// One pass over the tokens with a running maximum: when a new maximum
-// arrives, the sum and the accumulator are scaled by exp(old - new). One block
-// per (context, query head); its warps take tokens in turn, a lane holds
-// head_dim / 32 elements, and the warps' (m, l, acc) are joined at the end.
+// One pass over the cached tokens. In base 2, with x_j = s_j log2(e) and an
+// e4m3 value row v_j = a_j c_j (a_j its scale, c_j its codes), a warp keeps
+//   M (a bound of max_j x_j + log2 a_j),  w_j = 2^(x_j + log2 a_j - M),
+//   acc = sum_j w_j c_j,   l = sum_j w_j / a_j,
+// so that out = acc / l and lse = (M + log2 l) ln 2. The scale of a value row
+// goes into its weight's exponent: the weights stay in fp16's range whatever
+// the scales, and the codes go to the tensor cores unscaled. M moves only when
+// a tile's maximum passes it by 2^8 (fp16 weights reach 2^16), so that the
+// accumulators are rarely rescaled. Sums and accumulators are fp32.
+//
+// The work is bound by the cache's bytes: 4 D flops a token and query head
+// against 2 D + 8 bytes a token and kv head, 31 flop/byte with 16 query heads a
+// kv head. Hence:
+// * the length is split. The batch's contexts are cut into units of 64 tokens
+//   of one kv head, and every CTA gets an equal run of units, whatever the
+//   lengths (they are read on the device, so a captured graph follows them). A
+//   context that ends up on several CTAs leaves partial results, which a
+//   second kernel joins.
+// * the up to 16 query heads of a kv head are the rows of one m16n8k16 tensor
+//   core tile. More heads a kv head are further work items, which find the
+//   tokens in L2.
+// * each warp has tiles of 16 tokens of its own in flight, kStages deep, without
+//   a barrier: a lane copies (cp.async) to shared memory exactly the 16-byte
+//   pieces that it will need as operands, and reads them back itself. The
+//   order of the head's elements in the contraction is free (q is laid out to
+//   match), so a lane's piece of a key row is 16 neighbouring bytes: word w of
+//   it feeds contraction step w. The order of the output's elements is free
+//   too: a lane's piece of a value row is 16 neighbouring bytes, byte j of it
+//   belongs to output tile j.
+// e4m3 operands are converted to fp16, which holds every code. q goes from
+// bf16 to fp16 scaled by a power of two per head; only elements under 2^-24 of
+// the head's largest lose bits. The weights are rounded to fp16 (11 bits). With
+// a bf16 cache the operands are bf16, and the weights go in as the sum of two
+// bf16 numbers (16 bits).
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "attention.h"
@@ -19,117 +51,711 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kSms = 152;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;                  // tokens a warp takes at a time
+constexpr int kUnit = kWarps * kTile;      // tokens of a work unit
+constexpr int kRows = 16;                  // query heads of a work item
+constexpr int kMaxCtasPerSm = 4;
+constexpr int kMaxWorkers = kSms * kMaxCtasPerSm;
+constexpr uint32_t kAbsent = 0xffffffffu;
+constexpr float kSlack = 8.0f;             // log2 by which a weight may pass 1
 
-template <bool E4M3, int N>
-__device__ __forceinline__ void load_row(const void* base, int64_t row, int head_dim, int lane,
-                                         float (&x)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const int64_t at = row * head_dim + 64 * (i / 2) + 2 * lane;
-    if (E4M3) {
-      const uint16_t c = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(base) + at);
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    } else {
-      const uint32_t w =
-          *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + at);
-      x[i] = __uint_as_float(w << 16);
-      x[i + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-  }
+// Where a segment that several workers share left its pieces.
+struct Joint {
+  int32_t first;    // the first worker
+  int32_t pieces;   // number of workers; 1: nothing to join
+  int32_t slot;     // slot of the first piece; worker w's, w > first: 2 w
+  int32_t pad;
+};
+
+struct Args {
+  CacheView c;
+  const uint16_t* q;
+  int64_t q_stride;
+  int batch, q_heads, group;   // group: query heads of a kv head
+  int chunks;                  // items of at most kRows heads a group is cut into
+  const int32_t* lengths;
+  float scale;
+  int window;
+  uint16_t* out;
+  float* lse;
+  Joint* joints;               // [batch][heads * chunks]
+  float2* stats;               // [slots][kRows] (M, l)
+  float* parts;                // [slots][kRows][D]
+};
+
+// First and last tokens that take part, and the units they cover (units start
+// at a multiple of kTile).
+struct Span {
+  uint32_t begin, end, start, units;
+};
+
+__device__ __forceinline__ Span span_of(const Args& a, int b) {
+  const int length = a.lengths[b];
+  const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
+  Span s;
+  s.end = (uint32_t)min((int64_t)max(length, 0), room);
+  s.begin = a.window > 0 ? (uint32_t)max(length - a.window, 0) : 0u;
+  s.start = s.begin & ~(uint32_t)(kTile - 1);
+  s.units = s.end > s.begin ? (s.end - s.start + kUnit - 1) / kUnit : 0u;
+  return s;
 }
 
 template <bool E4M3, int D>
-__global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(
-    const CacheView c, const uint16_t* __restrict__ q, int64_t q_stride, int q_heads,
-    const int32_t* __restrict__ lengths, float scale, int window, uint16_t* __restrict__ out,
-    float* __restrict__ lse) {
-  constexpr int N = D / 32;
-  __shared__ float sm[kWarps], sl[kWarps], sacc[kWarps][D];
-  const int b = blockIdx.x, h = blockIdx.y;
+struct Shape {
+  static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
+  static constexpr int kKeyPieces = kRowBytes / 64;        // 16-byte pieces a lane holds of a key
+  static constexpr int kChunk = E4M3 && D >= 128 ? 16 : 8; // elements of a value piece
+  static constexpr int kPieceBytes = kChunk * (E4M3 ? 1 : 2);
+  static constexpr int kValuePieces = D / 8 / kChunk;      // pieces a lane holds of a value
+  static constexpr int kTileBytes = 2 * kTile * kRowBytes;
+  static constexpr int kSideBytes = 2 * kTile * 4 + 16;    // scales, and which tokens take part
+  static constexpr int kCtas = E4M3 ? (D == 256 ? 2 : 3) : (D == 64 ? 3 : D == 128 ? 2 : 1);
+  static constexpr int kStages =
+      kTileBytes <= 2048 ? 6 : kTileBytes <= 4096 ? 4 : 3;
+  static constexpr int kWarpBytes = kStages * (kTileBytes + kSideBytes);
+  static constexpr int kSmemBytes = kWarps * kWarpBytes;
+  static_assert(kStages * kTileBytes >= kRows * D * 4, "the join reuses the stages");
+  static_assert(kCtas * (kSmemBytes + 1536) <= 227 * 1024, "shared memory");
+  static_assert(kCtas <= kMaxCtasPerSm, "workspace slots");
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four e4m3 codes of a word as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// acc (+)= A B, 16 x 8 x 16: A's rows are query heads.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Largest over the four lanes that share a row of the accumulator tile.
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+__device__ __forceinline__ float weight(float m, float top) {   // 2^(m - top), 0 for no tokens
+  return m == -INFINITY ? 0.f : exp2_approx(m - top);
+}
+
+// Place of float4 f of a row of D floats in the join's shared memory: lanes
+// that hold neighbouring pieces of the same or the next row fall into
+// different banks.
+template <int CHUNK>
+__device__ __forceinline__ int join_place(int row, int f) {
+  return CHUNK == 16 ? f ^ ((((f >> 3) & 3) << 1) | (row & 1))
+                     : f ^ (((f >> 3) & 1) | ((row & 1) << 1));
+}
+
+template <bool E4M3, int D>
+__global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
+    paged_attention_kernel(const Args a) {
+  using S = Shape<E4M3, D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 stats[kWarps][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int kv = h / (q_heads / c.heads);
-  const int64_t top = (int64_t)c.max_pages << c.page_shift;
-  const int length = lengths[b];
-  const int end = (int)min((int64_t)max(length, 0), top);
-  const int begin = window > 0 ? max(length - window, 0) : 0;
-  float qv[N], acc[N];
-  load_row<false>(q + b * q_stride, h, D, lane, qv);
+  const int g = lane >> 2, t = lane & 3;    // row (or column) and place in a tile's fragments
+  uint8_t* const stage0 = smem + warp * S::kWarpBytes;
+  uint8_t* const side0 = stage0 + S::kStages * S::kTileBytes;
+  const uint32_t stage_u32 = smem_u32(stage0), side_u32 = smem_u32(side0);
+  pdl_launch_dependents();
+
+  // ---- this worker's units: [lo, hi) of the batch's total ----
+  const int items = a.c.heads * a.chunks;
+  int64_t total = 0;
+  for (int b = lane; b < a.batch; b += 32) total += span_of(a, b).units;
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = begin + warp; j < end; j += kWarps) {
-    const int32_t entry = c.table[b * c.table_stride + (j >> c.page_shift)];
-    if ((uint32_t)entry >= (uint32_t)c.pages) continue;
-    const int64_t row = (((int64_t)entry * c.heads + kv) << c.page_shift) +
-                        (j & ((1 << c.page_shift) - 1));
-    float k[N], v[N];
-    load_row<E4M3>(c.k, row, D, lane, k);
-    load_row<E4M3>(c.v, row, D, lane, v);
-    float s = 0.f;
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= items;
+  const int64_t workers = min((int64_t)gridDim.x, total);
+  const int64_t worker = blockIdx.x;
+  if (worker >= workers) return;
+  const int64_t lo = total * worker / workers, hi = total * (worker + 1) / workers;
+  // the context that unit lo falls into
+  int b = 0;
+  int64_t before = 0;    // units of the contexts before b
+  for (int b0 = 0;; b0 += 32) {
+    if (b0 >= a.batch) return;   // (lengths changed under the kernel)
+    const int64_t mine = b0 + lane < a.batch ? (int64_t)span_of(a, b0 + lane).units * items : 0;
+    int64_t up = mine;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(qv[i], k[i], s);
-    s = warp_sum(s) * scale * (E4M3 ? c.k_scale[row] : 1.f);
-    const float next = fmaxf(m, s);
-    const float old = m == -INFINITY ? 0.f : expf(m - next);
-    const float p = s == -INFINITY ? 0.f : expf(s - next);
-    const float pv = p * (E4M3 ? c.v_scale[row] : 1.f);
-    l = l * old + p;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + up > lo);
+    if (past != 0) {
+      const int at = __ffs(past) - 1;
+      b = b0 + at;
+      before += __shfl_sync(0xffffffffu, up - mine, at);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, up, 31);
+  }
+
+  Span span = span_of(a, b);
+  for (int64_t unit = lo; unit < hi;) {
+    // ---- the segment: units [u0, u1) of item `item` of context b ----
+    while (unit - before >= (int64_t)span.units * items) {
+      before += (int64_t)span.units * items;
+      if (++b >= a.batch) return;
+      span = span_of(a, b);
+    }
+    const int item = (int)((unit - before) / span.units);
+    const int64_t first = before + (int64_t)item * span.units;   // the item's first unit
+    const uint32_t u0 = (uint32_t)(unit - first);
+    const uint32_t u1 = (uint32_t)min((int64_t)span.units, hi - first);
+    const int kv = item / a.chunks;
+    const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;
+    const int rows = min(kRows, (kv + 1) * a.group - head0);
+    const int32_t* const table = a.c.table + (int64_t)b * a.c.table_stride;
+
+    // ---- q, in the order in which the lanes hold the keys ----
+    uint32_t qf[D / 16][4];
+    float row_scale[2];
+    {
+      const uint16_t* const q0 = a.q + (int64_t)b * a.q_stride + (int64_t)head0 * D;
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = fmaf(pv, v[i], acc[i] * old);
-    m = next;
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
+      for (int step = 0; step < D / 16; ++step) {
+        const int d = E4M3 ? 64 * (step >> 2) + 16 * t + 4 * (step & 3)
+                           : 32 * (step >> 1) + 8 * t + 4 * (step & 1);
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    sacc[warp][64 * (i / 2) + 2 * lane] = acc[i];
-    sacc[warp][64 * (i / 2) + 2 * lane + 1] = acc[i + 1];
+        for (int r = 0; r < 2; ++r) {
+          uint2 w = make_uint2(0u, 0u);
+          if (g + 8 * r < rows) w = *reinterpret_cast<const uint2*>(q0 + (g + 8 * r) * D + d);
+          qf[step][r] = w.x;
+          qf[step][2 + r] = w.y;
+        }
+      }
+      const float log2e = 1.4426950408889634f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) row_scale[r] = a.scale * log2e;
+      if (E4M3) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float top = 0.f;
+#pragma unroll
+          for (int step = 0; step < D / 16; ++step)
+#pragma unroll
+            for (int i = r; i < 4; i += 2)
+              top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[step][i])), fabsf(bf16_hi(qf[step][i]))));
+          top = quad_max(top);
+          // scale the head's largest element into [1, 2)
+          const uint32_t e = min(max((__float_as_uint(top) >> 23) & 255u, 1u), 253u);
+          const float down = __uint_as_float((254u - e) << 23);
+          row_scale[r] *= __uint_as_float(e << 23);
+#pragma unroll
+          for (int step = 0; step < D / 16; ++step)
+#pragma unroll
+            for (int i = r; i < 4; i += 2)
+              qf[step][i] = pack_f16(bf16_lo(qf[step][i]) * down, bf16_hi(qf[step][i]) * down);
+        }
+      }
+    }
+
+    // ---- this warp's tiles: tokens from + 64 i ----
+    const uint32_t from = span.start + u0 * kUnit + warp * kTile;
+    const uint32_t stop = min(span.end, span.start + u1 * kUnit);
+    const int tiles = from < stop ? (int)((stop - from + kUnit - 1) / kUnit) : 0;
+    // cache row of token lane % 16 of tile i
+    auto row_of = [&](int i) -> uint32_t {
+      const uint32_t token = from + (uint32_t)i * kUnit + (lane & 15);
+      if (i >= tiles || token >= stop || token < span.begin) return kAbsent;
+      const int32_t entry = table[token >> a.c.page_shift];
+      if ((uint32_t)entry >= (uint32_t)a.c.pages) return kAbsent;
+      return (((uint32_t)entry * a.c.heads + kv) << a.c.page_shift) +
+             (token & ((1u << a.c.page_shift) - 1u));
+    };
+    auto copy_tile = [&](int i, uint32_t row) {
+      const uint32_t at = stage_u32 + (i % S::kStages) * S::kTileBytes;
+      const uint32_t side = side_u32 + (i % S::kStages) * S::kSideBytes;
+      const unsigned here = __ballot_sync(0xffffffffu, row != kAbsent);
+      auto source = [&](const void* base, int token, uint32_t& bytes) {
+        const uint32_t r = __shfl_sync(0xffffffffu, row, token);
+        bytes = r != kAbsent ? 16u : 0u;
+        return static_cast<const uint8_t*>(base) +
+               (uint64_t)(r != kAbsent ? r : 0u) * S::kRowBytes;
+      };
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t bytes;
+        const uint8_t* src = source(a.c.k, 8 * n + g, bytes) + 16 * t;
+#pragma unroll
+        for (int p = 0; p < S::kKeyPieces; ++p)
+          cp_async_16(at + (n * S::kKeyPieces + p) * 512 + lane * 16, src + 64 * p, bytes);
+      }
+      const uint32_t values = at + 2 * S::kKeyPieces * 512;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t bytes;
+        const uint8_t* src =
+            source(a.c.v, 8 * (n >> 1) + 2 * t + (n & 1), bytes) + S::kPieceBytes * g;
+#pragma unroll
+        for (int p = 0; p < S::kValuePieces; ++p) {
+          if (S::kPieceBytes == 16)
+            cp_async_16(values + (n * S::kValuePieces + p) * 512 + lane * 16, src + 128 * p,
+                        bytes);
+          else
+            cp_async_8(values + n * 256 + lane * 8, src, bytes >> 1);
+        }
+      }
+      if (E4M3)
+        cp_async_4(side + lane * 4,
+                   (lane < 16 ? a.c.k_scale : a.c.v_scale) + (row != kAbsent ? row : 0u),
+                   row != kAbsent ? 4u : 0u);
+      if (lane == 0)
+        *reinterpret_cast<uint32_t*>(side0 + (i % S::kStages) * S::kSideBytes + 128) =
+            here & 0xffffu;
+      cp_commit();
+    };
+
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+
+    uint32_t next_row = row_of(0);
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      const uint32_t row = next_row;
+      next_row = row_of(i + 1);
+      if (i < tiles) copy_tile(i, row); else cp_commit();
+    }
+    for (int i = 0; i < tiles; ++i) {
+      cp_wait<S::kStages - 2>();
+      __syncwarp();
+      // the stage of tile i - 1, which every lane has read, takes a new tile
+      {
+        const uint32_t row = next_row;
+        next_row = row_of(i + S::kStages);
+        if (i + S::kStages - 1 < tiles) copy_tile(i + S::kStages - 1, row); else cp_commit();
+      }
+      const uint8_t* const tile = stage0 + (i % S::kStages) * S::kTileBytes;
+      const uint8_t* const side = side0 + (i % S::kStages) * S::kSideBytes;
+
+      // scores: [heads g, g + 8] x [tokens 8 n + 2 t, + 1]
+      float x[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
+#pragma unroll
+        for (int p = 0; p < S::kKeyPieces; ++p) {
+          const uint4 raw = *reinterpret_cast<const uint4*>(
+              tile + (n * S::kKeyPieces + p) * 512 + lane * 16);
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+          if (E4M3) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16(w[j], b0, b1);
+              mma16816<true>(x[n], qf[4 * p + j], b0, b1);
+            }
+          } else {
+            mma16816<false>(x[n], qf[2 * p], w[0], w[1]);
+            mma16816<false>(x[n], qf[2 * p + 1], w[2], w[3]);
+          }
+        }
+      }
+      // to base 2, with the value rows' scales in the exponent
+      float inverse[2][2];
+      const uint32_t here = *reinterpret_cast<const uint32_t*>(side + 128);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float2 ks = make_float2(1.f, 1.f);
+        float2 lv = make_float2(0.f, 0.f);
+        if (E4M3) {
+          ks = *reinterpret_cast<const float2*>(side + 4 * (8 * n + 2 * t));
+          const float2 vs = *reinterpret_cast<const float2*>(side + 64 + 4 * (8 * n + 2 * t));
+          // a scale of 0 (nothing to add but its weight) stays finite
+          lv = make_float2(log2_approx(fmaxf(vs.x, 0x1p-100f)),
+                           log2_approx(fmaxf(vs.y, 0x1p-100f)));
+          inverse[n][0] = exp2_approx(-lv.x);
+          inverse[n][1] = exp2_approx(-lv.y);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          x[n][2 * r] = fmaf(x[n][2 * r], row_scale[r] * ks.x, lv.x);
+          x[n][2 * r + 1] = fmaf(x[n][2 * r + 1], row_scale[r] * ks.y, lv.y);
+        }
+      }
+      if (here != 0xffffu) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((here >> (8 * n + 2 * t + (j & 1))) & 1u)) x[n][j] = -INFINITY;
+      }
+      // a tile that passes the bound moves it
+      float high[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        high[r] = quad_max(fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]),
+                                 fmaxf(x[1][2 * r], x[1][2 * r + 1])));
+      const bool moves = high[0] > top[0] + kSlack || high[1] > top[1] + kSlack;
+      if (__any_sync(0xffffffffu, moves)) {
+        float f[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float was = top[r];
+          top[r] = fmaxf(was, high[r]);
+          f[r] = weight(was, top[r]);
+          sum[r] *= f[r];
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          acc[n][0] *= f[0];
+          acc[n][1] *= f[0];
+          acc[n][2] *= f[1];
+          acc[n][3] *= f[1];
+        }
+      }
+      // weights
+      uint32_t wf[4], wr[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float bound = top[r] == -INFINITY ? 0.f : top[r];
+          const float w0 = exp2_approx(x[n][2 * r] - bound);
+          const float w1 = exp2_approx(x[n][2 * r + 1] - bound);
+          if (E4M3) {
+            sum[r] = fmaf(w0, inverse[n][0], fmaf(w1, inverse[n][1], sum[r]));
+            wf[2 * n + r] = pack_f16(w0, w1);
+          } else {
+            sum[r] += w0 + w1;
+            wf[2 * n + r] = pack_bf16(w0, w1);
+            wr[2 * n + r] = pack_bf16(w0 - bf16_lo(wf[2 * n + r]), w1 - bf16_hi(wf[2 * n + r]));
+          }
+        }
+      // acc += weights x values, tile (p, j): element j of the lanes' pieces p
+      const uint8_t* const values = tile + 2 * S::kKeyPieces * 512;
+#pragma unroll
+      for (int p = 0; p < S::kValuePieces; ++p) {
+        uint32_t w[4][S::kPieceBytes / 4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          if (S::kPieceBytes == 16) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(
+                values + (n * S::kValuePieces + p) * 512 + lane * 16);
+            w[n][0] = raw.x;
+            w[n][1] = raw.y;
+            w[n][S::kPieceBytes / 4 - 2] = raw.z;
+            w[n][S::kPieceBytes / 4 - 1] = raw.w;
+          } else {
+            const uint2 raw = *reinterpret_cast<const uint2*>(values + n * 256 + lane * 8);
+            w[n][0] = raw.x;
+            w[n][1] = raw.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < S::kPieceBytes / 4; ++j) {
+          if (E4M3) {
+            // bytes 4j .. 4j+3 of tokens (2t, 2t+1) and (2t+8, 2t+9), paired
+            uint32_t b[4][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              e4m3x4_to_f16(__byte_perm(w[2 * h][j], w[2 * h + 1][j], 0x5140), b[0][h], b[1][h]);
+              e4m3x4_to_f16(__byte_perm(w[2 * h][j], w[2 * h + 1][j], 0x7362), b[2][h], b[3][h]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma16816<true>(acc[p * S::kChunk + 4 * j + k], wf, b[k][0], b[k][1]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t pick = k == 0 ? 0x5410 : 0x7632;
+              const uint32_t b0 = __byte_perm(w[0][j], w[1][j], pick);
+              const uint32_t b1 = __byte_perm(w[2][j], w[3][j], pick);
+              mma16816<false>(acc[p * S::kChunk + 2 * j + k], wf, b0, b1);
+              mma16816<false>(acc[p * S::kChunk + 2 * j + k], wr, b0, b1);
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();   // (only empty groups can be left)
+
+    // ---- join the warps, each through its own stages ----
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float l = quad_sum(sum[r]);
+      if (t == 0) stats[warp][g + 8 * r] = make_float2(top[r], l);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float4* const to = reinterpret_cast<float4*>(stage0) + (g + 8 * r) * (D / 4);
+#pragma unroll
+      for (int p = 0; p < S::kValuePieces; ++p)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int j = 0; j < S::kChunk / 4; ++j) {
+            const int n = p * S::kChunk + 4 * j, e = 2 * r + half;
+            const int f = ((p * 8 + 2 * t + half) * S::kChunk) / 4 + j;
+            to[join_place<S::kChunk>(g, f)] =
+                make_float4(acc[n][e], acc[n + 1][e], acc[n + 2][e], acc[n + 3][e]);
+          }
+    }
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == span.units;
+    const int64_t slot = 2 * worker + (unit == lo ? 0 : 1);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), f = i % (D / 4);
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stats[w][row].x);
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 st = stats[w][row];
+        const float k = weight(st.x, m);
+        const float4 v = reinterpret_cast<const float4*>(
+            smem + w * S::kWarpBytes)[row * (D / 4) + join_place<S::kChunk>(row, f)];
+        l = fmaf(st.y, k, l);
+        o.x = fmaf(v.x, k, o.x);
+        o.y = fmaf(v.y, k, o.y);
+        o.z = fmaf(v.z, k, o.z);
+        o.w = fmaf(v.w, k, o.w);
+      }
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = (int64_t)b * a.q_heads + head0 + row;
+        *reinterpret_cast<uint2*>(a.out + at * D + 4 * f) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (f == 0 && a.lse != nullptr) a.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+      } else {
+        reinterpret_cast<float4*>(a.parts)[(slot * kRows + row) * (D / 4) + f] = o;
+        if (f == 0) a.stats[slot * kRows + row] = make_float2(m, l);
+      }
+    }
+    if (u0 == 0 && threadIdx.x == 0) {
+      // unit s belongs to the largest worker w with floor(total w / workers) <= s
+      const int64_t end = first + span.units;
+      const int64_t last = min((end * workers + total - 1) / total, workers) - 1;
+      Joint j;
+      j.first = (int32_t)worker;
+      j.pieces = (int32_t)(last - worker + 1);
+      j.slot = (int32_t)slot;
+      j.pad = 0;
+      a.joints[(int64_t)b * items + item] = j;
+    }
+    unit = first + u1;
+    __syncthreads();   // the stages are free again
   }
-  __syncthreads();
-  float top_m = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) top_m = fmaxf(top_m, sm[w]);
-  for (int w = 0; w < kWarps; ++w)
-    total += sm[w] == -INFINITY ? 0.f : sl[w] * expf(sm[w] - top_m);
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float sum = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (sm[w] != -INFINITY) sum += sacc[w][d] * expf(sm[w] - top_m);
-    const __nv_bfloat16 y = __float2bfloat16_rn(total == 0.f ? 0.f : sum / total);
-    out[((int64_t)b * q_heads + h) * D + d] = *reinterpret_cast<const uint16_t*>(&y);
+}
+
+// Joins the pieces of the segments that several workers share, and writes the
+// rows of contexts without tokens. One block per segment and share of its
+// rows; each warp takes every eighth piece, with a running bound.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a) {
+  constexpr int N = D / 32;
+  __shared__ float2 stats[kJoinWarps];
+  __shared__ float sacc[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int items = a.c.heads * a.chunks;
+  const int b = blockIdx.x / items, item = blockIdx.x - b * items;
+  const int kv = item / a.chunks;
+  const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;
+  const int rows = min(kRows, (kv + 1) * a.group - head0);
+  const bool empty = span_of(a, b).units == 0;
+  pdl_wait();
+  Joint j = {0, 0, 0, 0};
+  if (!empty) {
+    j = a.joints[blockIdx.x];
+    if (j.pieces == 1) return;
   }
-  if (lse != nullptr && threadIdx.x == 0)
-    lse[(int64_t)b * q_heads + h] = top_m + logf(total);
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    float m = -INFINITY, l = 0.f, acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int p = warp; p < j.pieces; p += kJoinWarps) {
+      const int64_t slot = p == 0 ? j.slot : 2 * (int64_t)(j.first + p);
+      const float2 st = a.stats[slot * kRows + row];
+      const float* from = a.parts + (slot * kRows + row) * D + lane * N;
+      float v[N];
+#pragma unroll
+      for (int i = 0; i < N; i += 2)
+        *reinterpret_cast<float2*>(v + i) = *reinterpret_cast<const float2*>(from + i);
+      const float top = fmaxf(m, st.x);
+      const float was = weight(m, top), now = weight(st.x, top);
+      m = top;
+      l = l * was + st.y * now;
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = acc[i] * was + v[i] * now;
+    }
+    if (lane == 0) stats[warp] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sacc[warp][lane * N + i] = acc[i];
+    __syncthreads();
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, stats[w].x);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l = fmaf(stats[w].y, weight(stats[w].x, m), l);
+    const int64_t at = (int64_t)b * a.q_heads + head0 + row;
+    for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) o = fmaf(sacc[w][d], weight(stats[w].x, m), o);
+      const __nv_bfloat16 y = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+      a.out[at * D + d] = *reinterpret_cast<const uint16_t*>(&y);
+    }
+    if (threadIdx.x == 0 && a.lse != nullptr)
+      a.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+    __syncthreads();
+  }
+}
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+int chunks_of(int group) { return (group + kRows - 1) / kRows; }
+
+template <bool E4M3, int D>
+int launch(const Args& a, cudaStream_t stream) {
+  using S = Shape<E4M3, D>;
+  const int64_t items = (int64_t)a.batch * a.c.heads * a.chunks;
+  if (items > 0x7fffffff) return -2;
+  // the opt-in to more than 48 KB of shared memory, once per device
+  static std::atomic<uint64_t> opted{0};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return -3;
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if ((opted.load(std::memory_order_relaxed) & bit) == 0 || device >= 64) {
+    if (cudaFuncSetAttribute(paged_attention_kernel<E4M3, D>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::kSmemBytes) != cudaSuccess)
+      return -3;
+    opted.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
+  // no more workers than units (a window's units can start before it by a tile)
+  const int64_t most = items * ((room + kTile + kUnit - 1) / kUnit);
+  const int grid = (int)std::min<int64_t>(kSms * S::kCtas, std::max<int64_t>(most, 1));
+  cudaError_t e = launch_kernel(false, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
+                                paged_attention_kernel<E4M3, D>, a);
+  if (e != cudaSuccess) return -3;
+  const int rows = std::min(a.group, kRows);
+  const int split = (int)std::min<int64_t>(std::max<int64_t>(8 * kSms / items, 1), rows);
+  e = launch_kernel(true, dim3((unsigned)items, split), dim3(kJoinWarps * 32), 0, stream,
+                    join_kernel<D>, a);
+  return e == cudaSuccess ? 0 : -3;
 }
 
 }  // namespace
 
-size_t paged_attention_ws_bytes(int, int, int, int) { return 256; }
+size_t paged_attention_ws_bytes(int heads, int head_dim, int batch, int q_heads) {
+  const size_t items = (size_t)batch * heads * chunks_of(q_heads / heads);
+  const size_t slots = 2 * kMaxWorkers;
+  return align256(items * sizeof(Joint)) + align256(slots * kRows * sizeof(float2)) +
+         slots * kRows * head_dim * sizeof(float);
+}
 
 int launch_paged_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int batch,
                            int q_heads, const int32_t* lengths, float scale, int window,
-                           uint16_t* out, float* lse, void*, cudaStream_t stream) {
-  const dim3 grid(batch, q_heads);
-  auto go = [&](auto kernel) {
-    kernel<<<grid, kWarps * 32, 0, stream>>>(c, q, q_stride, q_heads, lengths, scale, window, out,
-                                             lse);
-  };
+                           uint16_t* out, float* lse, void* ws, cudaStream_t stream) {
+  Args a{};
+  a.c = c;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.batch = batch;
+  a.q_heads = q_heads;
+  a.group = q_heads / c.heads;
+  a.chunks = chunks_of(a.group);
+  a.lengths = lengths;
+  a.scale = scale;
+  a.window = window;
+  a.out = out;
+  a.lse = lse;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  a.joints = reinterpret_cast<Joint*>(p);
+  p += align256((size_t)batch * c.heads * a.chunks * sizeof(Joint));
+  a.stats = reinterpret_cast<float2*>(p);
+  p += align256(2 * kMaxWorkers * kRows * sizeof(float2));
+  a.parts = reinterpret_cast<float*>(p);
   if (c.e4m3) {
-    if (c.head_dim == 64) go(paged_attention_kernel<true, 64>);
-    else if (c.head_dim == 128) go(paged_attention_kernel<true, 128>);
-    else go(paged_attention_kernel<true, 256>);
-  } else {
-    if (c.head_dim == 64) go(paged_attention_kernel<false, 64>);
-    else if (c.head_dim == 128) go(paged_attention_kernel<false, 128>);
-    else go(paged_attention_kernel<false, 256>);
+    if (c.head_dim == 64) return launch<true, 64>(a, stream);
+    if (c.head_dim == 128) return launch<true, 128>(a, stream);
+    return launch<true, 256>(a, stream);
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : -3;
+  if (c.head_dim == 64) return launch<false, 64>(a, stream);
+  if (c.head_dim == 128) return launch<false, 128>(a, stream);
+  return launch<false, 256>(a, stream);
 }
 
 }  // namespace moe
