@@ -111,7 +111,7 @@ class PagedKVCache:
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if coded else None,
             v_scale.data_ptr() if coded else None, self.pages, self.heads, self.page_size,
             self.head_dim, dtypes[k.dtype])
-        self._ws = {}
+        self._ws, self._need_ws = {}, {}
 
     @classmethod
     def empty(cls, pages, heads, page_size, head_dim, dtype="e4m3", device="cuda"):
@@ -151,14 +151,17 @@ class PagedKVCache:
     def workspace(self, batch, q_heads, stream=None):
         """The attention workspace of one stream, kept for the next step (calls
         on different streams may overlap, so each stream has its own)."""
-        on = torch.cuda.current_stream(self.k.device) if stream is None else stream
-        need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
-        ws = self._ws.get(on.cuda_stream)
+        need = self._need_ws.get((batch, q_heads))
+        if need is None:
+            need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
+            self._need_ws[batch, q_heads] = need
+        on = binding._raw_stream(stream, self.k)
+        ws = self._ws.get(on)
         if ws is None or ws.numel() < need:
             ws = binding._empty(max(need, 1), torch.uint8, self.k.device, stream)
             # memory of a graph under capture belongs to that graph
             if not torch.cuda.is_current_stream_capturing():
-                self._ws[on.cuda_stream] = ws
+                self._ws[on] = ws
         return ws
 
     def attend(self, q, block_table, lengths, scale=None, window=0, out=None, lse=None,

@@ -617,6 +617,15 @@ def moe_workspace_status(ws, stream=None):
 # Attention operators. `plan` and `cache` are moe_rotary_plan and moe_kv_cache
 # structures (expert_layer_ptpc_gb300.attention builds them from tensors).
 # ---------------------------------------------------------------------------
+def _raw_stream(stream, t):
+    """The handle of `stream`, or of the current stream of t's device (asked
+    for without making a Stream object: a small call costs about 10 us, and
+    that object would be 3 of them)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to the stream the kernel will run on, so that
     its memory is reused in that stream's order."""
@@ -677,18 +686,20 @@ def moe_rotary(plan, positions, q, k=None, inverse=False, q_out=None, k_out=None
     q_stride = _need_heads(q, hq, d, "q")
     _need_positions(positions, plan, T)
     if q_out is None:
-        q_out = _empty((T, hq, d), torch.bfloat16, q.device, stream)
-    qo_stride = _need_heads(q_out, hq, d, "q_out")
-    if q_out.shape[0] != T:
-        raise ValueError("q_out must have as many tokens as q")
+        q_out, qo_stride = _empty((T, hq, d), torch.bfloat16, q.device, stream), hq * d
+    else:
+        qo_stride = _need_heads(q_out, hq, d, "q_out")
+        if q_out.shape[0] != T:
+            raise ValueError("q_out must have as many tokens as q")
     hk = k_stride = ko_stride = 0
     k_ptr = ko_ptr = None
     if k is not None:
         hk = k.shape[1]
         k_stride = _need_heads(k, hk, d, "k")
         if k_out is None:
-            k_out = _empty((T, hk, d), torch.bfloat16, q.device, stream)
-        ko_stride = _need_heads(k_out, hk, d, "k_out")
+            k_out, ko_stride = _empty((T, hk, d), torch.bfloat16, q.device, stream), hk * d
+        else:
+            ko_stride = _need_heads(k_out, hk, d, "k_out")
         if k.shape[0] != T or k_out.shape[0] != T:
             raise ValueError("k and k_out must have as many tokens as q")
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
@@ -697,7 +708,7 @@ def moe_rotary(plan, positions, q, k=None, inverse=False, q_out=None, k_out=None
     _check("moe_rotary", load_library().moe_rotary(
         ctypes.byref(plan), positions.data_ptr(), T, d, q.data_ptr(), q_stride, hq,
         q_out.data_ptr(), qo_stride, k_ptr, k_stride, hk, ko_ptr, ko_stride,
-        int(bool(inverse)), _stream(stream)))
+        int(bool(inverse)), _raw_stream(stream, q)))
     return q_out, k_out
 
 
@@ -711,7 +722,7 @@ def moe_kv_write(cache, k, v, slots, stream=None):
     _need_slots(slots, T, cache)
     _check("moe_kv_write", load_library().moe_kv_write(
         ctypes.byref(cache), slots.data_ptr(), T, k.data_ptr(), k_stride, v.data_ptr(),
-        v_stride, _stream(stream)))
+        v_stride, _raw_stream(stream, k)))
 
 
 def moe_rotary_kv_write(plan, positions, cache, q, k, v, slots, q_out=None, stream=None):
@@ -725,14 +736,15 @@ def moe_rotary_kv_write(plan, positions, cache, q, k, v, slots, q_out=None, stre
     _need_positions(positions, plan, T)
     _need_slots(slots, T, cache)
     if q_out is None:
-        q_out = _empty((T, hq, d), torch.bfloat16, q.device, stream)
-    qo_stride = _need_heads(q_out, hq, d, "q_out")
-    if q_out.shape[0] != T:
-        raise ValueError("q_out must have as many tokens as q")
+        q_out, qo_stride = _empty((T, hq, d), torch.bfloat16, q.device, stream), hq * d
+    else:
+        qo_stride = _need_heads(q_out, hq, d, "q_out")
+        if q_out.shape[0] != T:
+            raise ValueError("q_out must have as many tokens as q")
     _check("moe_rotary_kv_write", load_library().moe_rotary_kv_write(
         ctypes.byref(plan), positions.data_ptr(), ctypes.byref(cache), slots.data_ptr(), T,
         q.data_ptr(), q_stride, hq, q_out.data_ptr(), qo_stride, k.data_ptr(), k_stride,
-        v.data_ptr(), v_stride, _stream(stream)))
+        v.data_ptr(), v_stride, _raw_stream(stream, q)))
     return q_out
 
 
@@ -747,13 +759,14 @@ def moe_kv_read(cache, block_table, offsets, rows, k_out=None, v_out=None, strea
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
             t = _empty(shape, torch.bfloat16, offsets.device, stream)
-        _need(t, torch.bfloat16, n)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
+        else:
+            _need(t, torch.bfloat16, n)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
         outs.append(t)
     _check("moe_kv_read", load_library().moe_kv_read(
         ctypes.byref(cache), block_table.data_ptr(), stride, pages, offsets.data_ptr(), batch,
-        rows, outs[0].data_ptr(), outs[1].data_ptr(), _stream(stream)))
+        rows, outs[0].data_ptr(), outs[1].data_ptr(), _raw_stream(stream, offsets)))
     return tuple(outs)
 
 
@@ -789,5 +802,6 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
     _check("moe_paged_attention", load_library().moe_paged_attention(
         ctypes.byref(cache), q.data_ptr(), q_stride, batch, hq, block_table.data_ptr(), stride,
         pages, lengths.data_ptr(), float(scale), int(window), out.data_ptr(),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, q)))
     return out
