@@ -16,22 +16,21 @@
 // The work is bound by the cache's bytes: 4 D flops a token and query head
 // against 2 D + 8 bytes a token and kv head, 31 flop/byte with 16 query heads a
 // kv head. Hence:
-// * the length is split. The batch's contexts are cut into units of 64 tokens
-//   of one kv head, and every CTA gets an equal run of units, whatever the
+// * the length is split. The batch's contexts are cut into units of 64 or 128
+//   tokens of one kv head, and every CTA gets an equal run of units, whatever the
 //   lengths (they are read on the device, so a captured graph follows them). A
 //   context that ends up on several CTAs leaves partial results, which a
 //   second kernel joins.
 // * the up to 16 query heads of a kv head are the rows of one m16n8k16 tensor
 //   core tile. More heads a kv head are further work items, which find the
 //   tokens in L2.
-// * each warp has tiles of 16 tokens of its own in flight, kStages deep, without
-//   a barrier: a lane copies (cp.async) to shared memory exactly the 16-byte
-//   pieces that it will need as operands, and reads them back itself. The
-//   order of the head's elements in the contraction is free (q is laid out to
-//   match), so a lane's piece of a key row is 16 neighbouring bytes: word w of
-//   it feeds contraction step w. The order of the output's elements is free
-//   too: a lane's piece of a value row is 16 neighbouring bytes, byte j of it
-//   belongs to output tile j.
+// * each warp has tiles of 16 or 32 tokens of its own in flight (cp.async),
+//   kStages deep, with barriers of the warp only.
+// * the order of the head's elements in the contraction is free (q is laid out
+//   to match), so that a lane's operands of a key row are 16 neighbouring bytes:
+//   word w of them feeds contraction step w. The order of the output's elements
+//   is free too: a lane's operands of a value row are 16 neighbouring bytes,
+//   byte j of them belongs to output tile j.
 // e4m3 operands are converted to fp16, which holds every code. q goes from
 // bf16 to fp16 scaled by a power of two per head; only elements under 2^-24 of
 // the head's largest lose bits. The weights are rounded to fp16 (11 bits). With
@@ -54,12 +53,10 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;                  // tokens a warp takes at a time
-constexpr int kUnit = kWarps * kTile;      // tokens of a work unit
+constexpr int kGroup = 16;                 // tokens of one tensor core contraction
 constexpr int kRows = 16;                  // query heads of a work item
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kMaxWorkers = kSms * kMaxCtasPerSm;
-constexpr uint32_t kAbsent = 0xffffffffu;
 constexpr float kSlack = 8.0f;             // log2 by which a weight may pass 1
 
 // Where a segment that several workers share left its pieces.
@@ -86,52 +83,63 @@ struct Args {
   float* parts;                // [slots][kRows][D]
 };
 
-// First and last tokens that take part, and the units they cover (units start
-// at a multiple of kTile).
+// First and last tokens that take part, and the units (of `unit` tokens) they
+// cover; the first unit starts at a multiple of kGroup.
 struct Span {
   uint32_t begin, end, start, units;
 };
 
-__device__ __forceinline__ Span span_of(const Args& a, int b) {
+__device__ __forceinline__ Span span_of(const Args& a, int b, int unit) {
   const int length = a.lengths[b];
   const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
   Span s;
   s.end = (uint32_t)min((int64_t)max(length, 0), room);
   s.begin = a.window > 0 ? (uint32_t)max(length - a.window, 0) : 0u;
-  s.start = s.begin & ~(uint32_t)(kTile - 1);
-  s.units = s.end > s.begin ? (s.end - s.start + kUnit - 1) / kUnit : 0u;
+  s.start = s.begin & ~(uint32_t)(kGroup - 1);
+  s.units = s.end > s.begin ? (s.end - s.start + unit - 1) / unit : 0u;
   return s;
 }
 
 template <bool E4M3, int D>
 struct Shape {
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
+  static constexpr int kTile = kRowBytes <= 128 ? 32 : 16;  // tokens a warp takes at a time
+  static constexpr int kUnit = kWarps * kTile;              // tokens of a work unit
+  static constexpr int kGroups = kTile / kGroup;
   static constexpr int kKeyPieces = kRowBytes / 64;        // 16-byte pieces a lane holds of a key
   static constexpr int kChunk = E4M3 && D >= 128 ? 16 : 8; // elements of a value piece
   static constexpr int kPieceBytes = kChunk * (E4M3 ? 1 : 2);
   static constexpr int kValuePieces = D / 8 / kChunk;      // pieces a lane holds of a value
-  static constexpr int kTileBytes = 2 * kTile * kRowBytes;
-  static constexpr int kSideBytes = 2 * kTile * 4 + 16;    // scales, and which tokens take part
+  static constexpr int kKeyBytes = kTile * kRowBytes;      // of a stage, and as much of values
   static constexpr int kCtas = E4M3 ? (D == 256 ? 2 : 3) : (D == 64 ? 3 : D == 128 ? 2 : 1);
-  static constexpr int kStages =
-      kTileBytes <= 2048 ? 6 : kTileBytes <= 4096 ? 4 : 3;
-  static constexpr int kWarpBytes = kStages * (kTileBytes + kSideBytes);
+  static constexpr int kStages = kRowBytes == 128 ? 2 : 3;
+  static constexpr int kSides = 4;                         // at least kStages + 1
+  static constexpr int kScaleBytes = E4M3 ? kSides * kTile * 12 : 0;
+  static constexpr int kStageBytes = 2 * kKeyBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes + kScaleBytes;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
-  static_assert(kStages * kTileBytes >= kRows * D * 4, "the join reuses the stages");
+  // Byte at which 16-byte piece `piece` of a tile lies in shared memory. Keys
+  // are read by 8 lanes at a time, 4 pieces of two neighbouring rows; values,
+  // 2 pieces (of 64-byte rows 2 halves each of 2) of 4 rows two apart.
+  static __device__ __forceinline__ int key_place(int piece) {
+    const int row = piece / (kRowBytes / 16);
+    return (piece ^ (kRowBytes == 64 ? 0 : (row & 1) << 2)) * 16;
+  }
+  static __device__ __forceinline__ int value_place(int piece) {
+    const int row = piece / (kRowBytes / 16);
+    return (piece ^ (row & 6)) * 16;
+  }
+  static_assert(kWarpBytes >= kRows * D * 4, "the join reuses the stages");
   static_assert(kCtas * (kSmemBytes + 1536) <= 227 * 1024, "shared memory");
   static_assert(kCtas <= kMaxCtasPerSm, "workspace slots");
 };
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Copies `bytes` bytes and fills the rest of the piece with zeros.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -161,7 +169,7 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
       : "r"(w));
 }
 
-// acc (+)= A B, 16 x 8 x 16: A's rows are query heads.
+// acc += A B, 16 x 8 x 16.
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -222,14 +230,14 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;    // row (or column) and place in a tile's fragments
   uint8_t* const stage0 = smem + warp * S::kWarpBytes;
-  uint8_t* const side0 = stage0 + S::kStages * S::kTileBytes;
-  const uint32_t stage_u32 = smem_u32(stage0), side_u32 = smem_u32(side0);
+  const uint32_t stage_u32 = smem_u32(stage0);
+  float* const side0 = reinterpret_cast<float*>(stage0 + S::kStages * S::kStageBytes);
   pdl_launch_dependents();
 
   // ---- this worker's units: [lo, hi) of the batch's total ----
   const int items = a.c.heads * a.chunks;
   int64_t total = 0;
-  for (int b = lane; b < a.batch; b += 32) total += span_of(a, b).units;
+  for (int b = lane; b < a.batch; b += 32) total += span_of(a, b, S::kUnit).units;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= items;
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   int64_t before = 0;    // units of the contexts before b
   for (int b0 = 0;; b0 += 32) {
     if (b0 >= a.batch) return;   // (lengths changed under the kernel)
-    const int64_t mine = b0 + lane < a.batch ? (int64_t)span_of(a, b0 + lane).units * items : 0;
+    const int64_t mine = b0 + lane < a.batch ? (int64_t)span_of(a, b0 + lane, S::kUnit).units * items : 0;
     int64_t up = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -259,13 +267,13 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     before += __shfl_sync(0xffffffffu, up, 31);
   }
 
-  Span span = span_of(a, b);
+  Span span = span_of(a, b, S::kUnit);
   for (int64_t unit = lo; unit < hi;) {
     // ---- the segment: units [u0, u1) of item `item` of context b ----
     while (unit - before >= (int64_t)span.units * items) {
       before += (int64_t)span.units * items;
       if (++b >= a.batch) return;
-      span = span_of(a, b);
+      span = span_of(a, b, S::kUnit);
     }
     const int item = (int)((unit - before) / span.units);
     const int64_t first = before + (int64_t)item * span.units;   // the item's first unit
@@ -293,9 +301,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
           qf[step][2 + r] = w.y;
         }
       }
-      const float log2e = 1.4426950408889634f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) row_scale[r] = a.scale * log2e;
+      for (int r = 0; r < 2; ++r) row_scale[r] = a.scale * 1.4426950408889634f;
       if (E4M3) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
             for (int i = r; i < 4; i += 2)
               top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[step][i])), fabsf(bf16_hi(qf[step][i]))));
           top = quad_max(top);
-          // scale the head's largest element into [1, 2)
+          // a power of two brings the head's largest element into [1, 2)
           const uint32_t e = min(max((__float_as_uint(top) >> 23) & 255u, 1u), 253u);
           const float down = __uint_as_float((254u - e) << 23);
           row_scale[r] *= __uint_as_float(e << 23);
@@ -319,60 +326,68 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       }
     }
 
-    // ---- this warp's tiles: tokens from + 64 i ----
-    const uint32_t from = span.start + u0 * kUnit + warp * kTile;
-    const uint32_t stop = min(span.end, span.start + u1 * kUnit);
-    const int tiles = from < stop ? (int)((stop - from + kUnit - 1) / kUnit) : 0;
-    // cache row of token lane % 16 of tile i
-    auto row_of = [&](int i) -> uint32_t {
-      const uint32_t token = from + (uint32_t)i * kUnit + (lane & 15);
-      if (i >= tiles || token >= stop || token < span.begin) return kAbsent;
-      const int32_t entry = table[token >> a.c.page_shift];
-      if ((uint32_t)entry >= (uint32_t)a.c.pages) return kAbsent;
-      return (((uint32_t)entry * a.c.heads + kv) << a.c.page_shift) +
-             (token & ((1u << a.c.page_shift) - 1u));
+    // ---- this warp's tiles: tokens from + kUnit i ----
+    const uint32_t from = span.start + u0 * S::kUnit + warp * S::kTile;
+    const uint32_t stop = min(span.end, span.start + u1 * S::kUnit);
+    const int tiles = from < stop ? (int)((stop - from + S::kUnit - 1) / S::kUnit) : 0;
+    // page entry of token lane % kTile of tile i
+    auto entry_of = [&](int i) -> int32_t {
+      const uint32_t token = from + (uint32_t)i * S::kUnit + (lane & (S::kTile - 1));
+      return i < tiles && token < stop ? table[token >> a.c.page_shift] : -1;
     };
-    auto copy_tile = [&](int i, uint32_t row) {
-      const uint32_t at = stage_u32 + (i % S::kStages) * S::kTileBytes;
-      const uint32_t side = side_u32 + (i % S::kStages) * S::kSideBytes;
-      const unsigned here = __ballot_sync(0xffffffffu, row != kAbsent);
-      auto source = [&](const void* base, int token, uint32_t& bytes) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, token);
-        bytes = r != kAbsent ? 16u : 0u;
-        return static_cast<const uint8_t*>(base) +
-               (uint64_t)(r != kAbsent ? r : 0u) * S::kRowBytes;
-      };
+    // A tile's tokens: lane's cache row, and which tokens take part.
+    struct Tokens {
+      uint32_t row, here;
+    };
+    constexpr uint32_t kAll = S::kTile == 32 ? 0xffffffffu : 0xffffu;
+    auto tokens_of = [&](int i, int32_t entry) -> Tokens {
+      const uint32_t token = from + (uint32_t)i * S::kUnit + (lane & (S::kTile - 1));
+      const bool paged = (uint32_t)entry < (uint32_t)a.c.pages;
+      Tokens k;
+      k.row = paged ? (((uint32_t)entry * a.c.heads + kv) << a.c.page_shift) +
+                          (token & ((1u << a.c.page_shift) - 1u))
+                    : 0u;
+      k.here = __ballot_sync(0xffffffffu, paged && token >= span.begin) & kAll;
+      return k;
+    };
+    // Rows lie in shared memory as in the cache, with their 16-byte pieces
+    // permuted within 128-byte lines so that the lanes' reads meet no bank twice.
+    // Eight lanes copy a line: whole lines leave L2 at once. A group of 16
+    // tokens of a full tile is one run of memory when pages have at least 16;
+    // otherwise every row's place comes from the lane that looked it up.
+    const bool runs = a.c.page_shift >= 4;
+    auto copy_tile = [&](uint32_t at, const void* cache, const Tokens k, auto place) {
+      if (runs && k.here == kAll) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        uint32_t bytes;
-        const uint8_t* src = source(a.c.k, 8 * n + g, bytes) + 16 * t;
+        for (int h = 0; h < S::kGroups; ++h) {
+          const uint8_t* const src =
+              static_cast<const uint8_t*>(cache) +
+              (uint64_t)__shfl_sync(0xffffffffu, k.row, kGroup * h) * S::kRowBytes + lane * 16;
 #pragma unroll
-        for (int p = 0; p < S::kKeyPieces; ++p)
-          cp_async_16(at + (n * S::kKeyPieces + p) * 512 + lane * 16, src + 64 * p, bytes);
-      }
-      const uint32_t values = at + 2 * S::kKeyPieces * 512;
+          for (int j = 0; j < kGroup * S::kRowBytes / 512; ++j) {
+            const int piece = h * (kGroup * S::kRowBytes / 16) + 32 * j + lane;
+            cp_async_16(at + place(piece), src + 512 * j);
+          }
+        }
+      } else {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        uint32_t bytes;
-        const uint8_t* src =
-            source(a.c.v, 8 * (n >> 1) + 2 * t + (n & 1), bytes) + S::kPieceBytes * g;
-#pragma unroll
-        for (int p = 0; p < S::kValuePieces; ++p) {
-          if (S::kPieceBytes == 16)
-            cp_async_16(values + (n * S::kValuePieces + p) * 512 + lane * 16, src + 128 * p,
-                        bytes);
-          else
-            cp_async_8(values + n * 256 + lane * 8, src, bytes >> 1);
+        for (int j = 0; j < S::kKeyBytes / 512; ++j) {
+          const int piece = 32 * j + lane, token = piece / (S::kRowBytes / 16);
+          const uint8_t* const src =
+              static_cast<const uint8_t*>(cache) +
+              (uint64_t)__shfl_sync(0xffffffffu, k.row, token) * S::kRowBytes +
+              piece % (S::kRowBytes / 16) * 16;
+          cp_async_16(at + place(piece), src, ((k.here >> token) & 1u) * 16u);
         }
       }
-      if (E4M3)
-        cp_async_4(side + lane * 4,
-                   (lane < 16 ? a.c.k_scale : a.c.v_scale) + (row != kAbsent ? row : 0u),
-                   row != kAbsent ? 4u : 0u);
-      if (lane == 0)
-        *reinterpret_cast<uint32_t*>(side0 + (i % S::kStages) * S::kSideBytes + 128) =
-            here & 0xffffu;
-      cp_commit();
+    };
+    auto copy_keys = [&](int i, const Tokens k) {
+      copy_tile(stage_u32 + (i % S::kStages) * S::kStageBytes, a.c.k, k,
+                [](int piece) { return S::key_place(piece); });
+    };
+    auto copy_values = [&](int i, const Tokens k) {
+      copy_tile(stage_u32 + (i % S::kStages) * S::kStageBytes + S::kKeyBytes, a.c.v, k,
+                [](int piece) { return S::value_place(piece); });
     };
 
     float acc[D / 8][4];
@@ -382,91 +397,130 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 
-    uint32_t next_row = row_of(0);
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-      const uint32_t row = next_row;
-      next_row = row_of(i + 1);
-      if (i < tiles) copy_tile(i, row); else cp_commit();
-    }
-    for (int i = 0; i < tiles; ++i) {
-      cp_wait<S::kStages - 2>();
-      __syncwarp();
-      // the stage of tile i - 1, which every lane has read, takes a new tile
-      {
-        const uint32_t row = next_row;
-        next_row = row_of(i + S::kStages);
-        if (i + S::kStages - 1 < tiles) copy_tile(i + S::kStages - 1, row); else cp_commit();
+    // The keys of a tile are one group of copies and its values the next, so
+    // that a stage's keys make room for a later tile's while its values are
+    // still to be used. Every wait leaves all but the group it needs pending.
+    uint32_t here[S::kStages];                      // of tiles i, i + 1, ...
+    // What the tokens of a tile bring to the scores: (scale of the key, log2 of
+    // the value's scale a) and 1 / a, a token a lane. They are asked for with the
+    // tile and put down an iteration later; with a place more than there are
+    // stages, the one barrier of the warp a tile orders this too.
+    float key_scale = 1.f, value_scale = 1.f;
+    auto ask_scales = [&](const Tokens k) {
+      if (E4M3 && ((k.here >> (lane & (S::kTile - 1))) & 1u)) {
+        key_scale = a.c.k_scale[k.row];
+        value_scale = a.c.v_scale[k.row];
       }
-      const uint8_t* const tile = stage0 + (i % S::kStages) * S::kTileBytes;
-      const uint8_t* const side = side0 + (i % S::kStages) * S::kSideBytes;
+    };
+    auto put_scales = [&](int i) {
+      if (E4M3 && lane < S::kTile) {
+        float* const side = side0 + (i & (S::kSides - 1)) * (3 * S::kTile);
+        // a scale of 0 (nothing to add but its weight) stays finite
+        const float l = log2_approx(fmaxf(value_scale, 0x1p-100f));
+        reinterpret_cast<float2*>(side)[lane] = make_float2(key_scale, l);
+        side[2 * S::kTile + lane] = exp2_approx(-l);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) {
+      const Tokens k = tokens_of(i, entry_of(i));
+      here[i] = k.here;
+      if (i < tiles) copy_keys(i, k);
+      cp_commit();
+      if (i < tiles) copy_values(i, k);
+      cp_commit();
+      ask_scales(k);
+      if (i + 1 < S::kStages) put_scales(i);
+    }
+    int32_t entry = entry_of(S::kStages);
+    for (int i = 0; i < tiles; ++i) {
+      const uint8_t* const tile = stage0 + (i % S::kStages) * S::kStageBytes;
+      const float* const side = side0 + (i & (S::kSides - 1)) * (3 * S::kTile);
+      put_scales(i + S::kStages - 1);
+      cp_wait<2 * S::kStages - 1>();   // this tile's keys
+      __syncwarp();
 
       // scores: [heads g, g + 8] x [tokens 8 n + 2 t, + 1]
-      float x[2][4];
+      float x[2 * S::kGroups][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
-#pragma unroll
-        for (int p = 0; p < S::kKeyPieces; ++p) {
-          const uint4 raw = *reinterpret_cast<const uint4*>(
-              tile + (n * S::kKeyPieces + p) * 512 + lane * 16);
-          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-          if (E4M3) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16(w[j], b0, b1);
-              mma16816<true>(x[n], qf[4 * p + j], b0, b1);
-            }
-          } else {
-            mma16816<false>(x[n], qf[2 * p], w[0], w[1]);
-            mma16816<false>(x[n], qf[2 * p + 1], w[2], w[3]);
-          }
-        }
-      }
-      // to base 2, with the value rows' scales in the exponent
-      float inverse[2][2];
-      const uint32_t here = *reinterpret_cast<const uint32_t*>(side + 128);
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        float2 ks = make_float2(1.f, 1.f);
-        float2 lv = make_float2(0.f, 0.f);
-        if (E4M3) {
-          ks = *reinterpret_cast<const float2*>(side + 4 * (8 * n + 2 * t));
-          const float2 vs = *reinterpret_cast<const float2*>(side + 64 + 4 * (8 * n + 2 * t));
-          // a scale of 0 (nothing to add but its weight) stays finite
-          lv = make_float2(log2_approx(fmaxf(vs.x, 0x1p-100f)),
-                           log2_approx(fmaxf(vs.y, 0x1p-100f)));
-          inverse[n][0] = exp2_approx(-lv.x);
-          inverse[n][1] = exp2_approx(-lv.y);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          x[n][2 * r] = fmaf(x[n][2 * r], row_scale[r] * ks.x, lv.x);
-          x[n][2 * r + 1] = fmaf(x[n][2 * r + 1], row_scale[r] * ks.y, lv.y);
-        }
-      }
-      if (here != 0xffffu) {
+      for (int h = 0; h < S::kGroups; ++h) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!((here >> (8 * n + 2 * t + (j & 1))) & 1u)) x[n][j] = -INFINITY;
+          for (int j = 0; j < 4; ++j) x[2 * h + n][j] = 0.f;
+#pragma unroll
+        for (int p = 0; p < S::kKeyPieces; ++p)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                tile + S::key_place((8 * (2 * h + n) + g) * (S::kRowBytes / 16) + 4 * p + t));
+            if (E4M3) {
+              const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16(v[j], b0, b1);
+                mma16816<true>(x[2 * h + n], qf[4 * p + j], b0, b1);
+              }
+            } else {
+              mma16816<false>(x[2 * h + n], qf[2 * p], w.x, w.y);
+              mma16816<false>(x[2 * h + n], qf[2 * p + 1], w.z, w.w);
+            }
+          }
+        // base 2, with the value rows' scales in the exponent
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float (&y)[4] = x[2 * h + n];
+          if (E4M3) {
+            const float4 sc = *reinterpret_cast<const float4*>(side + 2 * (8 * (2 * h + n) + 2 * t));
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              y[2 * r] = fmaf(y[2 * r] * sc.x, row_scale[r], sc.y);
+              y[2 * r + 1] = fmaf(y[2 * r + 1] * sc.z, row_scale[r], sc.w);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] *= row_scale[j >> 1];
+          }
+        }
       }
+      // the tile after the stages' takes the place of these keys
+      __syncwarp();
+      const Tokens next = tokens_of(i + S::kStages, entry);
+      entry = entry_of(i + S::kStages + 1);
+      if (i + S::kStages < tiles) copy_keys(i + S::kStages, next);
+      cp_commit();
+
+      if (here[0] != kAll) {
+#pragma unroll
+        for (int n = 0; n < 2 * S::kGroups; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((here[0] >> (8 * n + 2 * t + (j & 1))) & 1u)) x[n][j] = -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j + 1 < S::kStages; ++j) {
+        here[j] = here[j + 1];
+      }
+      here[S::kStages - 1] = next.here;
+      ask_scales(next);
+
       // a tile that passes the bound moves it
       float high[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        high[r] = quad_max(fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]),
-                                 fmaxf(x[1][2 * r], x[1][2 * r + 1])));
+      for (int r = 0; r < 2; ++r) {
+        high[r] = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
+#pragma unroll
+        for (int n = 1; n < 2 * S::kGroups; ++n)
+          high[r] = fmaxf(high[r], fmaxf(x[n][2 * r], x[n][2 * r + 1]));
+      }
       const bool moves = high[0] > top[0] + kSlack || high[1] > top[1] + kSlack;
       if (__any_sync(0xffffffffu, moves)) {
         float f[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float was = top[r];
-          top[r] = fmaxf(was, high[r]);
+          top[r] = fmaxf(was, quad_max(high[r]));
           f[r] = weight(was, top[r]);
           sum[r] *= f[r];
         }
@@ -479,68 +533,87 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
         }
       }
       // weights
-      uint32_t wf[4], wr[4];
+      const float bound[2] = {top[0] == -INFINITY ? 0.f : top[0],
+                              top[1] == -INFINITY ? 0.f : top[1]};
+      uint32_t wf[S::kGroups][4], wr[S::kGroups][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2 * S::kGroups; ++n) {
+        float2 inverse = make_float2(1.f, 1.f);
+        if (E4M3)
+          inverse = *reinterpret_cast<const float2*>(side + 2 * S::kTile + 8 * n + 2 * t);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float bound = top[r] == -INFINITY ? 0.f : top[r];
-          const float w0 = exp2_approx(x[n][2 * r] - bound);
-          const float w1 = exp2_approx(x[n][2 * r + 1] - bound);
+          const float w0 = exp2_approx(x[n][2 * r] - bound[r]);
+          const float w1 = exp2_approx(x[n][2 * r + 1] - bound[r]);
+          uint32_t& to = wf[n >> 1][2 * (n & 1) + r];
           if (E4M3) {
-            sum[r] = fmaf(w0, inverse[n][0], fmaf(w1, inverse[n][1], sum[r]));
-            wf[2 * n + r] = pack_f16(w0, w1);
+            sum[r] = fmaf(w0, inverse.x, fmaf(w1, inverse.y, sum[r]));
+            to = pack_f16(w0, w1);
           } else {
             sum[r] += w0 + w1;
-            wf[2 * n + r] = pack_bf16(w0, w1);
-            wr[2 * n + r] = pack_bf16(w0 - bf16_lo(wf[2 * n + r]), w1 - bf16_hi(wf[2 * n + r]));
-          }
-        }
-      // acc += weights x values, tile (p, j): element j of the lanes' pieces p
-      const uint8_t* const values = tile + 2 * S::kKeyPieces * 512;
-#pragma unroll
-      for (int p = 0; p < S::kValuePieces; ++p) {
-        uint32_t w[4][S::kPieceBytes / 4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          if (S::kPieceBytes == 16) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(
-                values + (n * S::kValuePieces + p) * 512 + lane * 16);
-            w[n][0] = raw.x;
-            w[n][1] = raw.y;
-            w[n][S::kPieceBytes / 4 - 2] = raw.z;
-            w[n][S::kPieceBytes / 4 - 1] = raw.w;
-          } else {
-            const uint2 raw = *reinterpret_cast<const uint2*>(values + n * 256 + lane * 8);
-            w[n][0] = raw.x;
-            w[n][1] = raw.y;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < S::kPieceBytes / 4; ++j) {
-          if (E4M3) {
-            // bytes 4j .. 4j+3 of tokens (2t, 2t+1) and (2t+8, 2t+9), paired
-            uint32_t b[4][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              e4m3x4_to_f16(__byte_perm(w[2 * h][j], w[2 * h + 1][j], 0x5140), b[0][h], b[1][h]);
-              e4m3x4_to_f16(__byte_perm(w[2 * h][j], w[2 * h + 1][j], 0x7362), b[2][h], b[3][h]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma16816<true>(acc[p * S::kChunk + 4 * j + k], wf, b[k][0], b[k][1]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t pick = k == 0 ? 0x5410 : 0x7632;
-              const uint32_t b0 = __byte_perm(w[0][j], w[1][j], pick);
-              const uint32_t b1 = __byte_perm(w[2][j], w[3][j], pick);
-              mma16816<false>(acc[p * S::kChunk + 2 * j + k], wf, b0, b1);
-              mma16816<false>(acc[p * S::kChunk + 2 * j + k], wr, b0, b1);
-            }
+            to = pack_bf16(w0, w1);
+            wr[n >> 1][2 * (n & 1) + r] = pack_bf16(w0 - bf16_lo(to), w1 - bf16_hi(to));
           }
         }
       }
+      cp_wait<2 * S::kStages - 1>();   // this tile's values
+      __syncwarp();
+      // acc += weights x values, tile (p, j): element j of the lanes' pieces p
+      const uint8_t* const values = tile + S::kKeyBytes;
+#pragma unroll
+      for (int h = 0; h < S::kGroups; ++h)
+#pragma unroll
+        for (int p = 0; p < S::kValuePieces; ++p) {
+          uint32_t w[4][S::kPieceBytes / 4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const int row = kGroup * h + 8 * (n >> 1) + 2 * t + (n & 1);
+            const uint8_t* const piece =
+                values + (S::kPieceBytes == 16
+                              ? S::value_place(row * (S::kRowBytes / 16) + 8 * p + g)
+                              : S::value_place(row * (S::kRowBytes / 16) + (g >> 1)) + (g & 1) * 8);
+            if (S::kPieceBytes == 16) {
+              const uint4 raw = *reinterpret_cast<const uint4*>(piece);
+              w[n][0] = raw.x;
+              w[n][1] = raw.y;
+              w[n][S::kPieceBytes / 4 - 2] = raw.z;
+              w[n][S::kPieceBytes / 4 - 1] = raw.w;
+            } else {
+              const uint2 raw = *reinterpret_cast<const uint2*>(piece);
+              w[n][0] = raw.x;
+              w[n][1] = raw.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < S::kPieceBytes / 4; ++j) {
+            if (E4M3) {
+              // bytes 4j .. 4j+3 of tokens (2t, 2t+1) and (2t+8, 2t+9), paired
+              uint32_t b[4][2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                e4m3x4_to_f16(__byte_perm(w[2 * e][j], w[2 * e + 1][j], 0x5140), b[0][e],
+                              b[1][e]);
+                e4m3x4_to_f16(__byte_perm(w[2 * e][j], w[2 * e + 1][j], 0x7362), b[2][e],
+                              b[3][e]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma16816<true>(acc[p * S::kChunk + 4 * j + k], wf[h], b[k][0], b[k][1]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t pick = k == 0 ? 0x5410 : 0x7632;
+                const uint32_t b0 = __byte_perm(w[0][j], w[1][j], pick);
+                const uint32_t b1 = __byte_perm(w[2][j], w[3][j], pick);
+                mma16816<false>(acc[p * S::kChunk + 2 * j + k], wf[h], b0, b1);
+                mma16816<false>(acc[p * S::kChunk + 2 * j + k], wr[h], b0, b1);
+              }
+            }
+          }
+        }
+      __syncwarp();
+      if (i + S::kStages < tiles) copy_values(i + S::kStages, next);
+      cp_commit();
     }
     cp_wait<0>();   // (only empty groups can be left)
 
@@ -621,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
 constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int unit) {
   constexpr int N = D / 32;
   __shared__ float2 stats[kJoinWarps];
   __shared__ float sacc[kJoinWarps][D];
@@ -631,7 +704,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a) {
   const int kv = item / a.chunks;
   const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;
   const int rows = min(kRows, (kv + 1) * a.group - head0);
-  const bool empty = span_of(a, b).units == 0;
+  const bool empty = span_of(a, b, unit).units == 0;
   pdl_wait();
   Joint j = {0, 0, 0, 0};
   if (!empty) {
@@ -704,8 +777,8 @@ int launch(const Args& a, cudaStream_t stream) {
     opted.fetch_or(bit, std::memory_order_relaxed);
   }
   const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
-  // no more workers than units (a window's units can start before it by a tile)
-  const int64_t most = items * ((room + kTile + kUnit - 1) / kUnit);
+  // no more workers than units (a window's can start before it by a group)
+  const int64_t most = items * ((room + kGroup + S::kUnit - 1) / S::kUnit);
   const int grid = (int)std::min<int64_t>(kSms * S::kCtas, std::max<int64_t>(most, 1));
   cudaError_t e = launch_kernel(false, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
                                 paged_attention_kernel<E4M3, D>, a);
@@ -713,7 +786,7 @@ int launch(const Args& a, cudaStream_t stream) {
   const int rows = std::min(a.group, kRows);
   const int split = (int)std::min<int64_t>(std::max<int64_t>(8 * kSms / items, 1), rows);
   e = launch_kernel(true, dim3((unsigned)items, split), dim3(kJoinWarps * 32), 0, stream,
-                    join_kernel<D>, a);
+                    join_kernel<D>, a, S::kUnit);
   return e == cudaSuccess ? 0 : -3;
 }
 
