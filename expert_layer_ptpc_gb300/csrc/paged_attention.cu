@@ -58,13 +58,17 @@ constexpr int kRows = 16;                  // query heads of a work item
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kMaxWorkers = kSms * kMaxCtasPerSm;
 constexpr float kSlack = 8.0f;             // log2 by which a weight may pass 1
+// What an item of a context costs beside its units, in units: fetching q, and
+// joining the warps. The work is cut with this included, or the workers that
+// get many short contexts would be the last to finish.
+constexpr uint32_t kItemCost = 2;
+constexpr int kLengths = 256;              // contexts whose lengths a worker keeps at hand
 
-// Where a segment that several workers share left its pieces.
+// Where a segment that several workers share left its pieces: the first
+// worker's in slot 2 first + 1, worker w's after it in slot 2 w.
 struct Joint {
   int32_t first;    // the first worker
   int32_t pieces;   // number of workers; 1: nothing to join
-  int32_t slot;     // slot of the first piece; worker w's, w > first: 2 w
-  int32_t pad;
 };
 
 struct Args {
@@ -89,8 +93,7 @@ struct Span {
   uint32_t begin, end, start, units;
 };
 
-__device__ __forceinline__ Span span_of(const Args& a, int b, int unit) {
-  const int length = a.lengths[b];
+__device__ __forceinline__ Span span_of(const Args& a, int length, int unit) {
   const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
   Span s;
   s.end = (uint32_t)min((int64_t)max(length, 0), room);
@@ -111,13 +114,14 @@ struct Shape {
   static constexpr int kPieceBytes = kChunk * (E4M3 ? 1 : 2);
   static constexpr int kValuePieces = D / 8 / kChunk;      // pieces a lane holds of a value
   static constexpr int kKeyBytes = kTile * kRowBytes;      // of a stage, and as much of values
-  static constexpr int kCtas = E4M3 ? (D == 256 ? 2 : 3) : (D == 64 ? 3 : D == 128 ? 2 : 1);
-  static constexpr int kStages = kRowBytes == 128 ? 2 : 3;
+  static constexpr int kCtas = kRowBytes == 64 ? 3 : kRowBytes == 512 ? 1 : 2;
+  static constexpr int kStages = kRowBytes == 64 || kRowBytes == 512 ? 3 : 2;
   static constexpr int kSides = 4;                         // at least kStages + 1
   static constexpr int kScaleBytes = E4M3 ? kSides * kTile * 12 : 0;
   static constexpr int kStageBytes = 2 * kKeyBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes + kScaleBytes;
-  static constexpr int kSmemBytes = kWarps * kWarpBytes;
+  static constexpr int kJoinBytes = kRows * D * 4;         // an accumulator tile
+  static constexpr int kSmemBytes = kWarps * kWarpBytes + 2 * kJoinBytes;
   // Byte at which 16-byte piece `piece` of a tile lies in shared memory. Keys
   // are read by 8 lanes at a time, 4 pieces of two neighbouring rows; values,
   // 2 pieces (of 64-byte rows 2 halves each of 2) of 4 rows two apart.
@@ -129,7 +133,6 @@ struct Shape {
     const int row = piece / (kRowBytes / 16);
     return (piece ^ (row & 6)) * 16;
   }
-  static_assert(kWarpBytes >= kRows * D * 4, "the join reuses the stages");
   static_assert(kCtas * (kSmemBytes + 1536) <= 227 * 1024, "shared memory");
   static_assert(kCtas <= kMaxCtasPerSm, "workspace slots");
 };
@@ -221,36 +224,95 @@ __device__ __forceinline__ int join_place(int row, int f) {
                      : f ^ (((f >> 3) & 1) | ((row & 1) << 1));
 }
 
+// A worker's part of one item of one context: units [u0, u1) of the item, which
+// ends at place `end` of the batch's work.
+struct Segment {
+  int b, kv, chunk;
+  uint32_t u0, u1;
+  Span span;
+  int64_t end;
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == span.units; }
+};
+
+// Hands out a worker's run of the batch's work, segment by segment. An item
+// takes kItemCost + units places; a run that ends within the first of them
+// gets nothing of it.
+struct Walker {
+  int64_t place, stop;     // next place, and the run's end
+  int b, kv, chunk;        // of the next place
+  uint32_t in;             // places of the item before it
+  Span span;
+
+  __device__ __forceinline__ bool next(const Args& a, const int* lengths, int first, int unit,
+                                       Segment& s) {
+    while (place < stop) {
+      const uint32_t size = kItemCost + span.units;
+      const uint32_t to = (uint32_t)min((int64_t)size, in + (stop - place));
+      s.b = b;
+      s.kv = kv;
+      s.chunk = chunk;
+      s.span = span;
+      s.u0 = max(in, kItemCost) - kItemCost;
+      s.u1 = max(to, kItemCost) - kItemCost;
+      s.end = place + (size - in);
+      place += to - in;
+      in = 0;
+      if (place < stop && ++chunk == a.chunks) {
+        chunk = 0;
+        if (++kv == a.c.heads) {
+          kv = 0;
+          do {
+            if (++b >= a.batch) {   // (lengths changed under the kernel)
+              place = stop;
+              break;
+            }
+            const int at = b - first;
+            span = span_of(a, at < kLengths ? lengths[at] : a.lengths[b], unit);
+          } while (span.units == 0);
+        }
+      }
+      if (s.u1 > s.u0) return true;
+    }
+    return false;
+  }
+};
+
 template <bool E4M3, int D>
 __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     paged_attention_kernel(const Args a) {
   using S = Shape<E4M3, D>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 stats[kWarps][kRows];
+  __shared__ float2 stats[2][kRows];
+  __shared__ int lengths[kLengths];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;    // row (or column) and place in a tile's fragments
   uint8_t* const stage0 = smem + warp * S::kWarpBytes;
   const uint32_t stage_u32 = smem_u32(stage0);
   float* const side0 = reinterpret_cast<float*>(stage0 + S::kStages * S::kStageBytes);
+  uint8_t* const join0 = smem + kWarps * S::kWarpBytes;
   pdl_launch_dependents();
 
-  // ---- this worker's units: [lo, hi) of the batch's total ----
+  // ---- this worker's run of the batch's work: places [lo, hi) ----
   const int items = a.c.heads * a.chunks;
+  auto places_of = [&](int b) -> int64_t {
+    const uint32_t units = b < a.batch ? span_of(a, a.lengths[b], S::kUnit).units : 0u;
+    return units == 0 ? 0 : (int64_t)(units + kItemCost) * items;
+  };
   int64_t total = 0;
-  for (int b = lane; b < a.batch; b += 32) total += span_of(a, b, S::kUnit).units;
+  for (int b = lane; b < a.batch; b += 32) total += places_of(b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= items;
   const int64_t workers = min((int64_t)gridDim.x, total);
   const int64_t worker = blockIdx.x;
   if (worker >= workers) return;
-  const int64_t lo = total * worker / workers, hi = total * (worker + 1) / workers;
-  // the context that unit lo falls into
-  int b = 0;
-  int64_t before = 0;    // units of the contexts before b
+  const int64_t cut = total * (worker + (lane & 1)) / workers;
+  const int64_t lo = __shfl_sync(0xffffffffu, cut, 0), hi = __shfl_sync(0xffffffffu, cut, 1);
+  // the context that place lo falls into
+  int first = 0;
+  int64_t before = 0;    // places of the contexts before it
   for (int b0 = 0;; b0 += 32) {
     if (b0 >= a.batch) return;   // (lengths changed under the kernel)
-    const int64_t mine = b0 + lane < a.batch ? (int64_t)span_of(a, b0 + lane, S::kUnit).units * items : 0;
+    const int64_t mine = places_of(b0 + lane);
     int64_t up = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -259,136 +321,220 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     }
     const unsigned past = __ballot_sync(0xffffffffu, before + up > lo);
     if (past != 0) {
-      const int at = __ffs(past) - 1;
-      b = b0 + at;
-      before += __shfl_sync(0xffffffffu, up - mine, at);
+      const int in = __ffs(past) - 1;
+      first = b0 + in;
+      before += __shfl_sync(0xffffffffu, up - mine, in);
       break;
     }
     before += __shfl_sync(0xffffffffu, up, 31);
   }
+  for (int i = threadIdx.x; i < kLengths; i += kThreads)
+    lengths[i] = first + i < a.batch ? a.lengths[first + i] : 0;
+  __syncthreads();
+  Walker walker;
+  walker.place = lo;
+  walker.stop = hi;
+  walker.b = first;
+  walker.span = span_of(a, lengths[0], S::kUnit);
+  {
+    const int64_t past = lo - before;
+    const uint32_t size = kItemCost + walker.span.units;
+    const int item = (int)(past / size);
+    walker.kv = item / a.chunks;
+    walker.chunk = item - walker.kv * a.chunks;
+    walker.in = (uint32_t)(past - (int64_t)item * size);
+    if (walker.kv >= a.c.heads) walker.stop = lo;   // (as above)
+  }
 
-  Span span = span_of(a, b, S::kUnit);
-  for (int64_t unit = lo; unit < hi;) {
-    // ---- the segment: units [u0, u1) of item `item` of context b ----
-    while (unit - before >= (int64_t)span.units * items) {
-      before += (int64_t)span.units * items;
-      if (++b >= a.batch) return;
-      span = span_of(a, b, S::kUnit);
+  // ---- copies: the tiles of all segments, one after the other ----
+  // Tile i of a segment holds the tokens from first_token + i kUnit on; the
+  // warps' tiles of a unit follow each other.
+  auto first_token = [&](const Segment& s) -> uint32_t {
+    return s.span.start + s.u0 * S::kUnit + warp * S::kTile;
+  };
+  auto end_token = [&](const Segment& s) -> uint32_t {
+    return min(s.span.end, s.span.start + s.u1 * S::kUnit);
+  };
+  auto tiles_of = [&](const Segment& s) -> int {
+    const uint32_t from = first_token(s), stop = end_token(s);
+    return from < stop ? (int)((stop - from + S::kUnit - 1) / S::kUnit) : 0;
+  };
+  // The next tile to copy: its lane's token, page entry (asked for a tile
+  // ahead) and segment.
+  Walker ahead = walker;
+  Segment source;
+  int source_left = 0;          // its tiles still to copy, the next one included
+  uint32_t token = 0;
+  int32_t entry = -1;
+  bool more = true;             // whether there is a next tile
+  auto ask = [&]() {
+    while (source_left == 0) {
+      if (!ahead.next(a, lengths, first, S::kUnit, source)) {
+        more = false;
+        return;
+      }
+      source_left = tiles_of(source);
+      token = first_token(source) + (lane & (S::kTile - 1));
     }
-    const int item = (int)((unit - before) / span.units);
-    const int64_t first = before + (int64_t)item * span.units;   // the item's first unit
-    const uint32_t u0 = (uint32_t)(unit - first);
-    const uint32_t u1 = (uint32_t)min((int64_t)span.units, hi - first);
-    const int kv = item / a.chunks;
-    const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;
-    const int rows = min(kRows, (kv + 1) * a.group - head0);
-    const int32_t* const table = a.c.table + (int64_t)b * a.c.table_stride;
-
-    // ---- q, in the order in which the lanes hold the keys ----
-    uint32_t qf[D / 16][4];
-    float row_scale[2];
-    {
-      const uint16_t* const q0 = a.q + (int64_t)b * a.q_stride + (int64_t)head0 * D;
+    entry = token < end_token(source)
+                ? a.c.table[(int64_t)source.b * a.c.table_stride + (token >> a.c.page_shift)]
+                : -1;
+  };
+  // A tile's tokens: the lane's cache row, and which tokens take part.
+  struct Tokens {
+    uint32_t row, here;
+  };
+  constexpr uint32_t kAll = S::kTile == 32 ? 0xffffffffu : 0xffffu;
+  auto tokens = [&]() -> Tokens {
+    const bool paged = more && (uint32_t)entry < (uint32_t)a.c.pages;
+    Tokens k;
+    k.row = paged ? (((uint32_t)entry * a.c.heads + source.kv) << a.c.page_shift) +
+                        (token & ((1u << a.c.page_shift) - 1u))
+                  : 0u;
+    k.here = __ballot_sync(0xffffffffu, paged && token >= source.span.begin) & kAll;
+    return k;
+  };
+  auto step = [&]() {   // past the tile just copied
+    if (!more) return;
+    --source_left;
+    token += S::kUnit;
+    entry = -1;
+    ask();
+  };
+  // Rows lie in shared memory as in the cache, with their 16-byte pieces
+  // permuted within 128-byte lines so that the lanes' reads meet no bank twice.
+  // Eight lanes copy a line: whole lines leave L2 at once. A group of 16
+  // tokens of a full tile is one run of memory when pages have at least 16;
+  // otherwise every row's place comes from the lane that looked it up.
+  const bool runs = a.c.page_shift >= 4;
+  auto copy_tile = [&](uint32_t to, const void* cache, const Tokens k, auto place) {
+    if (runs && k.here == kAll) {
 #pragma unroll
-      for (int step = 0; step < D / 16; ++step) {
-        const int d = E4M3 ? 64 * (step >> 2) + 16 * t + 4 * (step & 3)
-                           : 32 * (step >> 1) + 8 * t + 4 * (step & 1);
+      for (int h = 0; h < S::kGroups; ++h) {
+        const uint8_t* const src =
+            static_cast<const uint8_t*>(cache) +
+            (uint64_t)__shfl_sync(0xffffffffu, k.row, kGroup * h) * S::kRowBytes + lane * 16;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint2 w = make_uint2(0u, 0u);
-          if (g + 8 * r < rows) w = *reinterpret_cast<const uint2*>(q0 + (g + 8 * r) * D + d);
-          qf[step][r] = w.x;
-          qf[step][2 + r] = w.y;
+        for (int j = 0; j < kGroup * S::kRowBytes / 512; ++j) {
+          const int piece = h * (kGroup * S::kRowBytes / 16) + 32 * j + lane;
+          cp_async_16(to + place(piece), src + 512 * j);
         }
       }
+    } else {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) row_scale[r] = a.scale * 1.4426950408889634f;
-      if (E4M3) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float top = 0.f;
-#pragma unroll
-          for (int step = 0; step < D / 16; ++step)
-#pragma unroll
-            for (int i = r; i < 4; i += 2)
-              top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[step][i])), fabsf(bf16_hi(qf[step][i]))));
-          top = quad_max(top);
-          // a power of two brings the head's largest element into [1, 2)
-          const uint32_t e = min(max((__float_as_uint(top) >> 23) & 255u, 1u), 253u);
-          const float down = __uint_as_float((254u - e) << 23);
-          row_scale[r] *= __uint_as_float(e << 23);
-#pragma unroll
-          for (int step = 0; step < D / 16; ++step)
-#pragma unroll
-            for (int i = r; i < 4; i += 2)
-              qf[step][i] = pack_f16(bf16_lo(qf[step][i]) * down, bf16_hi(qf[step][i]) * down);
-        }
+      for (int j = 0; j < S::kKeyBytes / 512; ++j) {
+        const int piece = 32 * j + lane, row = piece / (S::kRowBytes / 16);
+        const uint8_t* const src =
+            static_cast<const uint8_t*>(cache) +
+            (uint64_t)__shfl_sync(0xffffffffu, k.row, row) * S::kRowBytes +
+            piece % (S::kRowBytes / 16) * 16;
+        cp_async_16(to + place(piece), src, ((k.here >> row) & 1u) * 16u);
       }
     }
+  };
+  auto copy_keys = [&](int stage, const Tokens k) {
+    copy_tile(stage_u32 + stage * S::kStageBytes, a.c.k, k,
+              [](int piece) { return S::key_place(piece); });
+  };
+  auto copy_values = [&](int stage, const Tokens k) {
+    copy_tile(stage_u32 + stage * S::kStageBytes + S::kKeyBytes, a.c.v, k,
+              [](int piece) { return S::value_place(piece); });
+  };
+  // What the tokens of a tile bring to the scores: (scale of the key, log2 of
+  // the value's scale a) and 1 / a, a token a lane. They are asked for with the
+  // tile and put down an iteration later; with a place more than there are
+  // stages, the one barrier of the warp a tile orders this too.
+  float key_scale = 1.f, value_scale = 1.f;
+  auto ask_scales = [&](const Tokens k) {
+    if (E4M3 && ((k.here >> (lane & (S::kTile - 1))) & 1u)) {
+      key_scale = a.c.k_scale[k.row];
+      value_scale = a.c.v_scale[k.row];
+    }
+  };
+  auto put_scales = [&](int n) {
+    if (E4M3 && lane < S::kTile) {
+      float* const side = side0 + (n & (S::kSides - 1)) * (3 * S::kTile);
+      // a scale of 0 (nothing to add but its weight) stays finite
+      const float l = log2_approx(fmaxf(value_scale, 0x1p-100f));
+      reinterpret_cast<float2*>(side)[lane] = make_float2(key_scale, l);
+      side[2 * S::kTile + lane] = exp2_approx(-l);
+    }
+  };
+  // The keys of a tile are one group of copies and its values the next, so
+  // that a stage's keys make room for a later tile's while its values are
+  // still to be used. Every wait leaves all but the group it needs pending.
+  uint32_t here[S::kStages];   // of the next tiles
+  ask();
+#pragma unroll
+  for (int i = 0; i < S::kStages; ++i) {
+    const Tokens k = tokens();
+    here[i] = k.here;
+    if (more) copy_keys(i, k);
+    cp_commit();
+    if (more) copy_values(i, k);
+    cp_commit();
+    ask_scales(k);
+    if (i + 1 < S::kStages) put_scales(i);
+    step();
+  }
 
-    // ---- this warp's tiles: tokens from + kUnit i ----
-    const uint32_t from = span.start + u0 * S::kUnit + warp * S::kTile;
-    const uint32_t stop = min(span.end, span.start + u1 * S::kUnit);
-    const int tiles = from < stop ? (int)((stop - from + S::kUnit - 1) / S::kUnit) : 0;
-    // page entry of token lane % kTile of tile i
-    auto entry_of = [&](int i) -> int32_t {
-      const uint32_t token = from + (uint32_t)i * S::kUnit + (lane & (S::kTile - 1));
-      return i < tiles && token < stop ? table[token >> a.c.page_shift] : -1;
-    };
-    // A tile's tokens: lane's cache row, and which tokens take part.
-    struct Tokens {
-      uint32_t row, here;
-    };
-    constexpr uint32_t kAll = S::kTile == 32 ? 0xffffffffu : 0xffffu;
-    auto tokens_of = [&](int i, int32_t entry) -> Tokens {
-      const uint32_t token = from + (uint32_t)i * S::kUnit + (lane & (S::kTile - 1));
-      const bool paged = (uint32_t)entry < (uint32_t)a.c.pages;
-      Tokens k;
-      k.row = paged ? (((uint32_t)entry * a.c.heads + kv) << a.c.page_shift) +
-                          (token & ((1u << a.c.page_shift) - 1u))
-                    : 0u;
-      k.here = __ballot_sync(0xffffffffu, paged && token >= span.begin) & kAll;
-      return k;
-    };
-    // Rows lie in shared memory as in the cache, with their 16-byte pieces
-    // permuted within 128-byte lines so that the lanes' reads meet no bank twice.
-    // Eight lanes copy a line: whole lines leave L2 at once. A group of 16
-    // tokens of a full tile is one run of memory when pages have at least 16;
-    // otherwise every row's place comes from the lane that looked it up.
-    const bool runs = a.c.page_shift >= 4;
-    auto copy_tile = [&](uint32_t at, const void* cache, const Tokens k, auto place) {
-      if (runs && k.here == kAll) {
+  // ---- q, in the order in which the lanes hold the keys ----
+  uint32_t qf[D / 16][4];
+  float row_scale[2];
+  auto heads_of = [&](const Segment& s, int& head0, int& rows) {
+    head0 = s.kv * a.group + s.chunk * kRows;
+    rows = min(kRows, (s.kv + 1) * a.group - head0);
+  };
+  auto ask_q = [&](const Segment& s) {
+    int head0, rows;
+    heads_of(s, head0, rows);
+    const uint16_t* const q0 = a.q + (int64_t)s.b * a.q_stride + (int64_t)head0 * D;
 #pragma unroll
-        for (int h = 0; h < S::kGroups; ++h) {
-          const uint8_t* const src =
-              static_cast<const uint8_t*>(cache) +
-              (uint64_t)__shfl_sync(0xffffffffu, k.row, kGroup * h) * S::kRowBytes + lane * 16;
+    for (int step = 0; step < D / 16; ++step) {
+      const int d = E4M3 ? 64 * (step >> 2) + 16 * t + 4 * (step & 3)
+                         : 32 * (step >> 1) + 8 * t + 4 * (step & 1);
 #pragma unroll
-          for (int j = 0; j < kGroup * S::kRowBytes / 512; ++j) {
-            const int piece = h * (kGroup * S::kRowBytes / 16) + 32 * j + lane;
-            cp_async_16(at + place(piece), src + 512 * j);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < S::kKeyBytes / 512; ++j) {
-          const int piece = 32 * j + lane, token = piece / (S::kRowBytes / 16);
-          const uint8_t* const src =
-              static_cast<const uint8_t*>(cache) +
-              (uint64_t)__shfl_sync(0xffffffffu, k.row, token) * S::kRowBytes +
-              piece % (S::kRowBytes / 16) * 16;
-          cp_async_16(at + place(piece), src, ((k.here >> token) & 1u) * 16u);
-        }
+      for (int r = 0; r < 2; ++r) {
+        uint2 w = make_uint2(0u, 0u);
+        if (g + 8 * r < rows) w = *reinterpret_cast<const uint2*>(q0 + (g + 8 * r) * D + d);
+        qf[step][r] = w.x;
+        qf[step][2 + r] = w.y;
       }
-    };
-    auto copy_keys = [&](int i, const Tokens k) {
-      copy_tile(stage_u32 + (i % S::kStages) * S::kStageBytes, a.c.k, k,
-                [](int piece) { return S::key_place(piece); });
-    };
-    auto copy_values = [&](int i, const Tokens k) {
-      copy_tile(stage_u32 + (i % S::kStages) * S::kStageBytes + S::kKeyBytes, a.c.v, k,
-                [](int piece) { return S::value_place(piece); });
-    };
+    }
+  };
+  auto convert_q = [&]() {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) row_scale[r] = a.scale * 1.4426950408889634f;
+    if (E4M3) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float top = 0.f;
+#pragma unroll
+        for (int step = 0; step < D / 16; ++step)
+#pragma unroll
+          for (int i = r; i < 4; i += 2)
+            top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[step][i])), fabsf(bf16_hi(qf[step][i]))));
+        top = quad_max(top);
+        // a power of two brings the head's largest element into [1, 2)
+        const uint32_t e = min(max((__float_as_uint(top) >> 23) & 255u, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23);
+        row_scale[r] *= __uint_as_float(e << 23);
+#pragma unroll
+        for (int step = 0; step < D / 16; ++step)
+#pragma unroll
+          for (int i = r; i < 4; i += 2)
+            qf[step][i] = pack_f16(bf16_lo(qf[step][i]) * down, bf16_hi(qf[step][i]) * down);
+      }
+    }
+  };
+
+  Segment seg;
+  int stage = 0, n = 0;   // of the next tile: its stage, and its number (for put_scales)
+  bool running = walker.next(a, lengths, first, S::kUnit, seg);
+  if (running) ask_q(seg);
+  while (running) {
+    convert_q();
+    const int tiles = tiles_of(seg);
 
     float acc[D / 8][4];
 #pragma unroll
@@ -397,46 +543,10 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 
-    // The keys of a tile are one group of copies and its values the next, so
-    // that a stage's keys make room for a later tile's while its values are
-    // still to be used. Every wait leaves all but the group it needs pending.
-    uint32_t here[S::kStages];                      // of tiles i, i + 1, ...
-    // What the tokens of a tile bring to the scores: (scale of the key, log2 of
-    // the value's scale a) and 1 / a, a token a lane. They are asked for with the
-    // tile and put down an iteration later; with a place more than there are
-    // stages, the one barrier of the warp a tile orders this too.
-    float key_scale = 1.f, value_scale = 1.f;
-    auto ask_scales = [&](const Tokens k) {
-      if (E4M3 && ((k.here >> (lane & (S::kTile - 1))) & 1u)) {
-        key_scale = a.c.k_scale[k.row];
-        value_scale = a.c.v_scale[k.row];
-      }
-    };
-    auto put_scales = [&](int i) {
-      if (E4M3 && lane < S::kTile) {
-        float* const side = side0 + (i & (S::kSides - 1)) * (3 * S::kTile);
-        // a scale of 0 (nothing to add but its weight) stays finite
-        const float l = log2_approx(fmaxf(value_scale, 0x1p-100f));
-        reinterpret_cast<float2*>(side)[lane] = make_float2(key_scale, l);
-        side[2 * S::kTile + lane] = exp2_approx(-l);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < S::kStages; ++i) {
-      const Tokens k = tokens_of(i, entry_of(i));
-      here[i] = k.here;
-      if (i < tiles) copy_keys(i, k);
-      cp_commit();
-      if (i < tiles) copy_values(i, k);
-      cp_commit();
-      ask_scales(k);
-      if (i + 1 < S::kStages) put_scales(i);
-    }
-    int32_t entry = entry_of(S::kStages);
-    for (int i = 0; i < tiles; ++i) {
-      const uint8_t* const tile = stage0 + (i % S::kStages) * S::kStageBytes;
-      const float* const side = side0 + (i & (S::kSides - 1)) * (3 * S::kTile);
-      put_scales(i + S::kStages - 1);
+    for (int i = 0; i < tiles; ++i, ++n) {
+      const uint8_t* const tile = stage0 + stage * S::kStageBytes;
+      const float* const side = side0 + (n & (S::kSides - 1)) * (3 * S::kTile);
+      put_scales(n + S::kStages - 1);
       cp_wait<2 * S::kStages - 1>();   // this tile's keys
       __syncwarp();
 
@@ -486,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       }
       // the tile after the stages' takes the place of these keys
       __syncwarp();
-      const Tokens next = tokens_of(i + S::kStages, entry);
-      entry = entry_of(i + S::kStages + 1);
-      if (i + S::kStages < tiles) copy_keys(i + S::kStages, next);
+      const bool copies = more;
+      const Tokens next = tokens();
+      if (copies) copy_keys(stage, next);
       cp_commit();
 
       if (here[0] != kAll) {
@@ -504,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       }
       here[S::kStages - 1] = next.here;
       ask_scales(next);
+      step();
 
       // a tile that passes the bound moves it
       float high[2];
@@ -612,86 +723,117 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
           }
         }
       __syncwarp();
-      if (i + S::kStages < tiles) copy_values(i + S::kStages, next);
+      if (copies) copy_values(stage, next);
       cp_commit();
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
-    cp_wait<0>();   // (only empty groups can be left)
 
-    // ---- join the warps, each through its own stages ----
+    // ---- join the warps ----
+    const Segment done = seg;
+    running = walker.next(a, lengths, first, S::kUnit, seg);
+    if (running) ask_q(seg);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float l = quad_sum(sum[r]);
-      if (t == 0) stats[warp][g + 8 * r] = make_float2(top[r], l);
-    }
-    __syncwarp();
+    for (int r = 0; r < 2; ++r) sum[r] = quad_sum(sum[r]);
+    auto put_acc = [&](int to) {
+      if (t == 0) {
+        stats[to][g] = make_float2(top[0], sum[0]);
+        stats[to][g + 8] = make_float2(top[1], sum[1]);
+      }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float4* const to = reinterpret_cast<float4*>(stage0) + (g + 8 * r) * (D / 4);
+      for (int r = 0; r < 2; ++r) {
+        float4* const row = reinterpret_cast<float4*>(join0 + to * S::kJoinBytes) +
+                            (g + 8 * r) * (D / 4);
 #pragma unroll
-      for (int p = 0; p < S::kValuePieces; ++p)
+        for (int p = 0; p < S::kValuePieces; ++p)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int j = 0; j < S::kChunk / 4; ++j) {
-            const int n = p * S::kChunk + 4 * j, e = 2 * r + half;
-            const int f = ((p * 8 + 2 * t + half) * S::kChunk) / 4 + j;
-            to[join_place<S::kChunk>(g, f)] =
-                make_float4(acc[n][e], acc[n + 1][e], acc[n + 2][e], acc[n + 3][e]);
-          }
+            for (int j = 0; j < S::kChunk / 4; ++j) {
+              const int i = p * S::kChunk + 4 * j, e = 2 * r + half;
+              const int f = ((p * 8 + 2 * t + half) * S::kChunk) / 4 + j;
+              row[join_place<S::kChunk>(g, f)] =
+                  make_float4(acc[i][e], acc[i + 1][e], acc[i + 2][e], acc[i + 3][e]);
+            }
+      }
+    };
+    __syncthreads();   // the last segment's has been read
+    if (warp >= 2) put_acc(warp - 2);
+    __syncthreads();
+    if (warp < 2) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 other = stats[warp][g + 8 * r];
+        const float m = fmaxf(top[r], other.x);
+        const float mine = weight(top[r], m), its = weight(other.x, m);
+        top[r] = m;
+        sum[r] = sum[r] * mine + other.y * its;
+        const float4* const row = reinterpret_cast<const float4*>(join0 + warp * S::kJoinBytes) +
+                                  (g + 8 * r) * (D / 4);
+#pragma unroll
+        for (int p = 0; p < S::kValuePieces; ++p)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int j = 0; j < S::kChunk / 4; ++j) {
+              const int i = p * S::kChunk + 4 * j, e = 2 * r + half;
+              const int f = ((p * 8 + 2 * t + half) * S::kChunk) / 4 + j;
+              const float4 v = row[join_place<S::kChunk>(g, f)];
+              acc[i][e] = acc[i][e] * mine + v.x * its;
+              acc[i + 1][e] = acc[i + 1][e] * mine + v.y * its;
+              acc[i + 2][e] = acc[i + 2][e] * mine + v.z * its;
+              acc[i + 3][e] = acc[i + 3][e] * mine + v.w * its;
+            }
+      }
+      __syncwarp();   // every lane has read the statistics it replaces
+      put_acc(warp);
     }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == span.units;
-    const int64_t slot = 2 * worker + (unit == lo ? 0 : 1);
+    int head0, rows;
+    heads_of(done, head0, rows);
+    const bool whole = done.whole();
+    const int64_t slot = 2 * worker + (done.u0 == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
       const int row = i / (D / 4), f = i % (D / 4);
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stats[w][row].x);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 st = stats[w][row];
-        const float k = weight(st.x, m);
-        const float4 v = reinterpret_cast<const float4*>(
-            smem + w * S::kWarpBytes)[row * (D / 4) + join_place<S::kChunk>(row, f)];
-        l = fmaf(st.y, k, l);
-        o.x = fmaf(v.x, k, o.x);
-        o.y = fmaf(v.y, k, o.y);
-        o.z = fmaf(v.z, k, o.z);
-        o.w = fmaf(v.w, k, o.w);
-      }
+      const float2 s0 = stats[0][row], s1 = stats[1][row];
+      const float m = fmaxf(s0.x, s1.x);
+      const float k0 = weight(s0.x, m), k1 = weight(s1.x, m);
+      const int at = row * (D / 4) + join_place<S::kChunk>(row, f);
+      const float4 v0 = reinterpret_cast<const float4*>(join0)[at];
+      const float4 v1 = reinterpret_cast<const float4*>(join0 + S::kJoinBytes)[at];
+      const float l = s0.y * k0 + s1.y * k1;
+      const float4 o = make_float4(v0.x * k0 + v1.x * k1, v0.y * k0 + v1.y * k1,
+                                   v0.z * k0 + v1.z * k1, v0.w * k0 + v1.w * k1);
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t at = (int64_t)b * a.q_heads + head0 + row;
-        *reinterpret_cast<uint2*>(a.out + at * D + 4 * f) =
+        const int64_t to = (int64_t)done.b * a.q_heads + head0 + row;
+        *reinterpret_cast<uint2*>(a.out + to * D + 4 * f) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (f == 0 && a.lse != nullptr) a.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+        if (f == 0 && a.lse != nullptr) a.lse[to] = (m + log2f(l)) * 0.6931471805599453f;
       } else {
         reinterpret_cast<float4*>(a.parts)[(slot * kRows + row) * (D / 4) + f] = o;
         if (f == 0) a.stats[slot * kRows + row] = make_float2(m, l);
       }
     }
-    if (u0 == 0 && threadIdx.x == 0) {
-      // unit s belongs to the largest worker w with floor(total w / workers) <= s
-      const int64_t end = first + span.units;
-      const int64_t last = min((end * workers + total - 1) / total, workers) - 1;
+    if (done.u0 == 0 && threadIdx.x == 0) {
       Joint j;
       j.first = (int32_t)worker;
-      j.pieces = (int32_t)(last - worker + 1);
-      j.slot = (int32_t)slot;
-      j.pad = 0;
-      a.joints[(int64_t)b * items + item] = j;
+      j.pieces = 1;
+      if (!whole) {
+        // place p belongs to the largest worker w with floor(total w / workers) <= p
+        const int64_t last = min((done.end * workers + total - 1) / total, workers) - 1;
+        j.pieces = (int32_t)(last - worker + 1);
+      }
+      a.joints[((int64_t)done.b * a.c.heads + done.kv) * a.chunks + done.chunk] = j;
     }
-    unit = first + u1;
-    __syncthreads();   // the stages are free again
   }
+  cp_wait<0>();   // (only empty groups are left)
 }
 
-// Joins the pieces of the segments that several workers share, and writes the
-// rows of contexts without tokens. One block per segment and share of its
-// rows; each warp takes every eighth piece, with a running bound.
-constexpr int kJoinWarps = 8;
+// Joins the pieces of the items that several workers share, and writes the
+// rows of contexts without tokens. A block takes one item's rows, or a share of
+// them when there are few items; a row gets kJoinWarps / rows-a-block warps, each
+// of which takes every so many-th piece with a running bound.
+constexpr int kJoinWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int unit) {
@@ -704,20 +846,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int
   const int kv = item / a.chunks;
   const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;
   const int rows = min(kRows, (kv + 1) * a.group - head0);
-  const bool empty = span_of(a, b, unit).units == 0;
+  const int share = gridDim.y;                 // warps of a row: a power of two
+  const int row = blockIdx.y * (kJoinWarps / share) + warp / share;
+  const bool empty = span_of(a, a.lengths[b], unit).units == 0;
   pdl_wait();
-  Joint j = {0, 0, 0, 0};
+  Joint j = {0, 0};
   if (!empty) {
     j = a.joints[blockIdx.x];
     if (j.pieces == 1) return;
   }
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    float m = -INFINITY, l = 0.f, acc[N];
+  float m = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int p = warp; p < j.pieces; p += kJoinWarps) {
-      const int64_t slot = p == 0 ? j.slot : 2 * (int64_t)(j.first + p);
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  if (row < rows) {
+#pragma unroll 8
+    for (int p = warp & (share - 1); p < j.pieces; p += share) {
+      const int64_t slot = 2 * (int64_t)(j.first + p) + (p == 0 ? 1 : 0);
       const float2 st = a.stats[slot * kRows + row];
       const float* from = a.parts + (slot * kRows + row) * D + lane * N;
       float v[N];
@@ -731,28 +875,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] = acc[i] * was + v[i] * now;
     }
+  }
+  if (share > 1) {   // join the row's warps, in its first one
     if (lane == 0) stats[warp] = make_float2(m, l);
 #pragma unroll
-    for (int i = 0; i < N; ++i) sacc[warp][lane * N + i] = acc[i];
+    for (int i = 0; i < N; ++i) sacc[warp][i * 32 + lane] = acc[i];
     __syncthreads();
-    m = -INFINITY;
+    if ((warp & (share - 1)) != 0) return;
+    for (int w = warp; w < warp + share; ++w) m = fmaxf(m, stats[w].x);
     l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, stats[w].x);
+    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+    for (int w = warp; w < warp + share; ++w) {
+      const float k = weight(stats[w].x, m);
+      l = fmaf(stats[w].y, k, l);
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) l = fmaf(stats[w].y, weight(stats[w].x, m), l);
-    const int64_t at = (int64_t)b * a.q_heads + head0 + row;
-    for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
-      float o = 0.f;
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) o = fmaf(sacc[w][d], weight(stats[w].x, m), o);
-      const __nv_bfloat16 y = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-      a.out[at * D + d] = *reinterpret_cast<const uint16_t*>(&y);
+      for (int i = 0; i < N; ++i) acc[i] = fmaf(sacc[w][i * 32 + lane], k, acc[i]);
     }
-    if (threadIdx.x == 0 && a.lse != nullptr)
-      a.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
-    __syncthreads();
   }
+  if (row >= rows) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = (int64_t)b * a.q_heads + head0 + row;
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    *reinterpret_cast<uint32_t*>(a.out + at * D + lane * N + i) =
+        pack_bf16(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0 && a.lse != nullptr) a.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -777,15 +925,16 @@ int launch(const Args& a, cudaStream_t stream) {
     opted.fetch_or(bit, std::memory_order_relaxed);
   }
   const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
-  // no more workers than units (a window's can start before it by a group)
-  const int64_t most = items * ((room + kGroup + S::kUnit - 1) / S::kUnit);
-  const int grid = (int)std::min<int64_t>(kSms * S::kCtas, std::max<int64_t>(most, 1));
+  // no more workers than places (a window's units can start before it by a group)
+  const int64_t most = items * ((room + kGroup + S::kUnit - 1) / S::kUnit + kItemCost);
+  const int grid = (int)std::min<int64_t>(kSms * S::kCtas, most);
   cudaError_t e = launch_kernel(false, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
                                 paged_attention_kernel<E4M3, D>, a);
   if (e != cudaSuccess) return -3;
-  const int rows = std::min(a.group, kRows);
-  const int split = (int)std::min<int64_t>(std::max<int64_t>(8 * kSms / items, 1), rows);
-  e = launch_kernel(true, dim3((unsigned)items, split), dim3(kJoinWarps * 32), 0, stream,
+  // few items: a row's pieces go to several warps (2 blocks an SM hold 16 each)
+  int share = 1;
+  while (share < kJoinWarps && 2 * share * items <= 2 * kSms) share *= 2;
+  e = launch_kernel(true, dim3((unsigned)items, share), dim3(kJoinWarps * 32), 0, stream,
                     join_kernel<D>, a, S::kUnit);
   return e == cudaSuccess ? 0 : -3;
 }
