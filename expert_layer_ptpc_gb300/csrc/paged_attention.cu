@@ -224,6 +224,13 @@ __device__ __forceinline__ int join_place(int row, int f) {
                      : f ^ (((f >> 3) & 1) | ((row & 1) << 1));
 }
 
+// a / b for non-negative a and positive b; the 64-bit quotient, of many more
+// instructions, only where it is needed.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // A worker's part of one item of one context: units [u0, u1) of the item, which
 // ends at place `end` of the batch's work.
 struct Segment {
@@ -290,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   const uint32_t stage_u32 = smem_u32(stage0);
   float* const side0 = reinterpret_cast<float*>(stage0 + S::kStages * S::kStageBytes);
   uint8_t* const join0 = smem + kWarps * S::kWarpBytes;
+  pdl_wait();
   pdl_launch_dependents();
 
   // ---- this worker's run of the batch's work: places [lo, hi) ----
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   const int64_t workers = min((int64_t)gridDim.x, total);
   const int64_t worker = blockIdx.x;
   if (worker >= workers) return;
-  const int64_t cut = total * (worker + (lane & 1)) / workers;
+  const int64_t cut = quotient(total * (worker + (lane & 1)), workers);
   const int64_t lo = __shfl_sync(0xffffffffu, cut, 0), hi = __shfl_sync(0xffffffffu, cut, 1);
   // the context that place lo falls into
   int first = 0;
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   {
     const int64_t past = lo - before;
     const uint32_t size = kItemCost + walker.span.units;
-    const int item = (int)(past / size);
+    const int item = (int)quotient(past, size);
     walker.kv = item / a.chunks;
     walker.chunk = item - walker.kv * a.chunks;
     walker.in = (uint32_t)(past - (int64_t)item * size);
@@ -359,47 +367,54 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     const uint32_t from = first_token(s), stop = end_token(s);
     return from < stop ? (int)((stop - from + S::kUnit - 1) / S::kUnit) : 0;
   };
-  // The next tile to copy: its lane's token, page entry (asked for a tile
-  // ahead) and segment.
+  // The next tile to copy: whether there is one, its lane's token and page
+  // entry (asked for a tile ahead), and its segment's kv head and begin.
+  struct Pending {
+    bool more;
+    uint32_t token;
+    int32_t entry;
+    int kv;
+    uint32_t begin;
+  };
   Walker ahead = walker;
   Segment source;
   int source_left = 0;          // its tiles still to copy, the next one included
-  uint32_t token = 0;
-  int32_t entry = -1;
-  bool more = true;             // whether there is a next tile
+  Pending next_tile = {true, 0u, -1, 0, 0u};
   auto ask = [&]() {
     while (source_left == 0) {
       if (!ahead.next(a, lengths, first, S::kUnit, source)) {
-        more = false;
+        next_tile.more = false;
         return;
       }
       source_left = tiles_of(source);
-      token = first_token(source) + (lane & (S::kTile - 1));
+      next_tile.token = first_token(source) + (lane & (S::kTile - 1));
+      next_tile.kv = source.kv;
+      next_tile.begin = source.span.begin;
     }
-    entry = token < end_token(source)
-                ? a.c.table[(int64_t)source.b * a.c.table_stride + (token >> a.c.page_shift)]
-                : -1;
+    next_tile.entry = next_tile.token < end_token(source)
+                          ? a.c.table[(int64_t)source.b * a.c.table_stride +
+                                      (next_tile.token >> a.c.page_shift)]
+                          : -1;
+  };
+  auto step = [&]() {   // past a tile
+    if (!next_tile.more) return;
+    --source_left;
+    next_tile.token += S::kUnit;
+    ask();
   };
   // A tile's tokens: the lane's cache row, and which tokens take part.
   struct Tokens {
     uint32_t row, here;
   };
   constexpr uint32_t kAll = S::kTile == 32 ? 0xffffffffu : 0xffffu;
-  auto tokens = [&]() -> Tokens {
-    const bool paged = more && (uint32_t)entry < (uint32_t)a.c.pages;
+  auto tokens = [&](const Pending& p) -> Tokens {
+    const bool paged = p.more && (uint32_t)p.entry < (uint32_t)a.c.pages;
     Tokens k;
-    k.row = paged ? (((uint32_t)entry * a.c.heads + source.kv) << a.c.page_shift) +
-                        (token & ((1u << a.c.page_shift) - 1u))
+    k.row = paged ? (((uint32_t)p.entry * a.c.heads + p.kv) << a.c.page_shift) +
+                        (p.token & ((1u << a.c.page_shift) - 1u))
                   : 0u;
-    k.here = __ballot_sync(0xffffffffu, paged && token >= source.span.begin) & kAll;
+    k.here = __ballot_sync(0xffffffffu, paged && p.token >= p.begin) & kAll;
     return k;
-  };
-  auto step = [&]() {   // past the tile just copied
-    if (!more) return;
-    --source_left;
-    token += S::kUnit;
-    entry = -1;
-    ask();
   };
   // Rows lie in shared memory as in the cache, with their 16-byte pieces
   // permuted within 128-byte lines so that the lanes' reads meet no bank twice.
@@ -463,21 +478,6 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   // The keys of a tile are one group of copies and its values the next, so
   // that a stage's keys make room for a later tile's while its values are
   // still to be used. Every wait leaves all but the group it needs pending.
-  uint32_t here[S::kStages];   // of the next tiles
-  ask();
-#pragma unroll
-  for (int i = 0; i < S::kStages; ++i) {
-    const Tokens k = tokens();
-    here[i] = k.here;
-    if (more) copy_keys(i, k);
-    cp_commit();
-    if (more) copy_values(i, k);
-    cp_commit();
-    ask_scales(k);
-    if (i + 1 < S::kStages) put_scales(i);
-    step();
-  }
-
   // ---- q, in the order in which the lanes hold the keys ----
   uint32_t qf[D / 16][4];
   float row_scale[2];
@@ -528,10 +528,40 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     }
   };
 
+  // ---- the first tiles and the first q, all asked for before any is used ----
+  uint32_t here[S::kStages];   // of the next tiles
+  Pending firsts[S::kStages];
+  ask();
+#pragma unroll
+  for (int i = 0; i < S::kStages; ++i) {
+    firsts[i] = next_tile;
+    step();
+  }
   Segment seg;
   int stage = 0, n = 0;   // of the next tile: its stage, and its number (for put_scales)
   bool running = walker.next(a, lengths, first, S::kUnit, seg);
   if (running) ask_q(seg);
+  {
+    float ks[S::kStages], vs[S::kStages];
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) {
+      const Tokens k = tokens(firsts[i]);
+      here[i] = k.here;
+      if (firsts[i].more) copy_keys(i, k);
+      cp_commit();
+      if (firsts[i].more) copy_values(i, k);
+      cp_commit();
+      ask_scales(k);
+      ks[i] = key_scale;
+      vs[i] = value_scale;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) {
+      key_scale = ks[i];
+      value_scale = vs[i];
+      if (i + 1 < S::kStages) put_scales(i);
+    }
+  }
   while (running) {
     convert_q();
     const int tiles = tiles_of(seg);
@@ -596,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       }
       // the tile after the stages' takes the place of these keys
       __syncwarp();
-      const bool copies = more;
-      const Tokens next = tokens();
+      const bool copies = next_tile.more;
+      const Tokens next = tokens(next_tile);
       if (copies) copy_keys(stage, next);
       cp_commit();
 
@@ -820,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       j.pieces = 1;
       if (!whole) {
         // place p belongs to the largest worker w with floor(total w / workers) <= p
-        const int64_t last = min((done.end * workers + total - 1) / total, workers) - 1;
+        const int64_t last = min(quotient(done.end * workers + total - 1, total), workers) - 1;
         j.pieces = (int32_t)(last - worker + 1);
       }
       a.joints[((int64_t)done.b * a.c.heads + done.kv) * a.chunks + done.chunk] = j;
@@ -928,7 +958,7 @@ int launch(const Args& a, cudaStream_t stream) {
   // no more workers than places (a window's units can start before it by a group)
   const int64_t most = items * ((room + kGroup + S::kUnit - 1) / S::kUnit + kItemCost);
   const int grid = (int)std::min<int64_t>(kSms * S::kCtas, most);
-  cudaError_t e = launch_kernel(false, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
+  cudaError_t e = launch_kernel(true, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
                                 paged_attention_kernel<E4M3, D>, a);
   if (e != cudaSuccess) return -3;
   // few items: a row's pieces go to several warps (2 blocks an SM hold 16 each)
