@@ -2,8 +2,10 @@
 // b is the cache row of token r - offsets[b], as bf16(fp32(code) * scale).
 //
 // Bound by memory: an e4m3 row is read once (1 byte an element and its scale)
-// and written once (2 bytes). A thread owns 16 elements of one row: one
-// 16-byte load of codes, two 16-byte stores.
+// and written once (2 bytes). A block takes 16 rows: 16 lanes look their cache rows
+// up (context, then page), then all threads stream the rows' runs of 8 elements,
+// 8-byte loads of codes against 16-byte stores, both contiguous over the lanes, with
+// 8 loads in flight a thread.
 #include "attention.h"
 #include "common.cuh"
 #include "internal.h"
@@ -15,7 +17,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 16;
+constexpr int kRows = 16;    // out rows of a block
+constexpr int kRun = 8;      // elements of one access
+constexpr int kAhead = 4;    // runs loaded before the first is used
 
 // Two e4m3 codes (low byte first) as fp32.
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t c) {
@@ -28,56 +32,82 @@ template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(
     const CacheView c, const int32_t* __restrict__ offsets, int batch, int64_t rows,
     uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out) {
-  const int per_row = c.heads * (c.head_dim / kUnit);   // units of one token
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t r = i / per_row;
-  if (r >= rows) return;
-  const int unit = (int)(i - r * per_row);
-  const int head = unit / (c.head_dim / kUnit);
-  const int d = (unit - head * (c.head_dim / kUnit)) * kUnit;
-  // the context of row r: the last b with offsets[b] <= r
-  int lo = 0, hi = batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (offsets[mid] <= r) lo = mid; else hi = mid;
-  }
-  const int64_t token = r - offsets[lo];
-  const int64_t page = token >> c.page_shift;
-  int32_t entry = -1;
-  if (token >= 0 && r < offsets[lo + 1] && page < c.max_pages)
-    entry = c.table[lo * c.table_stride + page];
-  const bool here = (uint32_t)entry < (uint32_t)c.pages;
-  const int64_t row = (((int64_t)entry * c.heads + head) << c.page_shift) +
-                      (token & ((1 << c.page_shift) - 1));
-  const int64_t out = (r * c.heads + head) * c.head_dim + d;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    uint4 y[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (here) {
-      if (E4M3) {
-        const uint8_t* base = static_cast<const uint8_t*>(which ? c.v : c.k);
-        const uint4 raw = *reinterpret_cast<const uint4*>(base + row * c.head_dim + d);
-        const float s = (which ? c.v_scale : c.k_scale)[row];
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t p[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 f = e4m3x2_to_f32((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
-          p[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        y[0] = make_uint4(p[0], p[1], p[2], p[3]);
-        y[1] = make_uint4(p[4], p[5], p[6], p[7]);
-      } else {
-        const uint16_t* base = static_cast<const uint16_t*>(which ? c.v : c.k);
-        const uint4* from = reinterpret_cast<const uint4*>(base + row * c.head_dim + d);
-        y[0] = from[0];
-        y[1] = from[1];
+  __shared__ int64_t place[kRows];   // cache row of (token, head 0), -1: none
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t r0 = (int64_t)blockIdx.x * kRows;
+  if (threadIdx.x < kRows) {
+    const int64_t r = r0 + threadIdx.x;
+    int64_t at = -1;
+    if (r < rows) {
+      // the last context with offsets[b] <= r
+      int lo = 0, hi = batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (offsets[mid] <= r) lo = mid; else hi = mid;
+      }
+      const int64_t token = r - offsets[lo], page = token >> c.page_shift;
+      if (token >= 0 && r < offsets[lo + 1] && page < c.max_pages) {
+        const int32_t entry = c.table[lo * c.table_stride + page];
+        if ((uint32_t)entry < (uint32_t)c.pages)
+          at = ((int64_t)entry * c.heads << c.page_shift) + (token & ((1 << c.page_shift) - 1));
       }
     }
-    uint4* to = reinterpret_cast<uint4*>((which ? v_out : k_out) + out);
-    to[0] = y[0];
-    to[1] = y[1];
+    place[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const int in_head = c.head_dim / kRun, in_row = c.heads * in_head;   // runs
+  const int total = (int)min((int64_t)kRows, rows - r0) * in_row;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kAhead * kThreads) {
+    uint4 raw[kAhead][2];
+    float scale[kAhead][2];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j * kThreads;
+      raw[j][0] = raw[j][1] = make_uint4(0u, 0u, 0u, 0u);
+      scale[j][0] = scale[j][1] = 0.f;
+      if (i >= total) continue;
+      const int r = i / in_row, run = i - r * in_row, head = run / in_head;
+      if (place[r] < 0) continue;
+      const int64_t row = place[r] + ((int64_t)head << c.page_shift);
+      const int64_t at = row * c.head_dim + (run - head * in_head) * kRun;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (E4M3) {
+          const uint2 w = *reinterpret_cast<const uint2*>(
+              static_cast<const uint8_t*>(which ? c.v : c.k) + at);
+          raw[j][which].x = w.x;
+          raw[j][which].y = w.y;
+          scale[j][which] = (which ? c.v_scale : c.k_scale)[row];
+        } else {
+          raw[j][which] = *reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(which ? c.v : c.k) + at);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i >= total) continue;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        uint4 y = raw[j][which];
+        if (E4M3) {
+          const uint32_t w[2] = {y.x, y.y};
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = e4m3x2_to_f32((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+            const float s = scale[j][which];
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
+            p[k] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          y = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+        // out rows follow each other: run i of the block's is run i of the outputs'
+        *reinterpret_cast<uint4*>((which ? v_out : k_out) + (r0 * in_row + i) * kRun) = y;
+      }
+    }
   }
 }
 
@@ -85,16 +115,13 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(
 
 int launch_kv_read(const CacheView& c, const int32_t* offsets, int batch, int64_t rows,
                    uint16_t* k_out, uint16_t* v_out, cudaStream_t stream) {
-  const int64_t units = rows * c.heads * (c.head_dim / kUnit);
-  const int64_t blocks = (units + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffff) return -2;
-  if (c.e4m3)
-    kv_read_kernel<true><<<(unsigned)blocks, kThreads, 0, stream>>>(c, offsets, batch, rows,
-                                                                     k_out, v_out);
-  else
-    kv_read_kernel<false><<<(unsigned)blocks, kThreads, 0, stream>>>(c, offsets, batch, rows,
-                                                                      k_out, v_out);
-  return cudaGetLastError() == cudaSuccess ? 0 : -3;
+  const int64_t blocks = (rows + kRows - 1) / kRows;
+  if (blocks > 0x7fffffff || (int64_t)kRows * c.heads * (c.head_dim / kRun) > 0x3fffffff) return -2;
+  const cudaError_t e =
+      launch_kernel(true, dim3((unsigned)blocks), dim3(kThreads), 0, stream,
+                    c.e4m3 ? kv_read_kernel<true> : kv_read_kernel<false>, c, offsets, batch,
+                    rows, k_out, v_out);
+  return e == cudaSuccess ? 0 : -3;
 }
 
 }  // namespace moe

@@ -12,11 +12,13 @@
 // argument reduction. Its upper 32 bits, as a signed fraction, go to sincospif.
 //
 // Every element is read once and written once: the kernel is bound by memory
-// (4 bytes moved per element of q against 3 flops). A thread owns a unit of
-// 16 elements (8 pairs): two 16-byte loads, in flight before the block works
-// out the token's cosines, which all heads of the token share through shared
-// memory. A cache head is 4, 8 or 16 units, hence that many neighbouring
-// lanes of one warp, and its row maximum is a shuffle.
+// (4 bytes moved per element of q against 3 flops). A warp takes one token and
+// a run of its heads. It works out the token's cosines together, two pairs a lane
+// for 128 elements, and every lane keeps the 8 that its elements need in
+// registers over all the heads. A lane's unit of a head is two runs of 8 elements,
+// half a region apart, so that the lanes' 16-byte accesses are contiguous; four
+// units are loaded before the first is used. A cache head is 4, 8 or 16 units,
+// hence that many neighbouring lanes, and its row maximum is a shuffle.
 #include <algorithm>
 
 #include "attention.h"
@@ -27,8 +29,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnit = 16;   // elements per thread
+constexpr int kWarps = 8;
+constexpr int kUnit = 16;     // elements of a lane
+constexpr int kAhead = 4;     // units loaded before the first is used
 
 __device__ __forceinline__ void unpack8(const uint4& raw, float* v) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -49,14 +52,24 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint2 codes8(const float* v, float s) {
+// v / s rounded to nearest, for many v and one s: with y = 1 / s rounded to
+// nearest and q = v y within a unit in the last place of v / s, q + y (v - s q)
+// with fused products is v / s rounded to nearest (Markstein 1990), where nothing
+// under- or overflows. Here s >= 2^-49 and y is normal, and quotients below
+// 2^-10 become the code 0 whatever their last bits.
+__device__ __forceinline__ float quotient(float v, float s, float y) {
+  const float q = v * y;
+  return fmaf(-fmaf(s, q, -v), y, q);   // (this order keeps the sign of a zero)
+}
+
+__device__ __forceinline__ uint2 codes8(const float* v, float s, float y) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint16_t lo =
-        f32x2_to_e4m3x2(__fdiv_rn(v[4 * i], s), __fdiv_rn(v[4 * i + 1], s));
+        f32x2_to_e4m3x2(quotient(v[4 * i], s, y), quotient(v[4 * i + 1], s, y));
     const uint16_t hi =
-        f32x2_to_e4m3x2(__fdiv_rn(v[4 * i + 2], s), __fdiv_rn(v[4 * i + 3], s));
+        f32x2_to_e4m3x2(quotient(v[4 * i + 2], s, y), quotient(v[4 * i + 3], s, y));
     w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
   }
   return make_uint2(w[0], w[1]);
@@ -64,106 +77,132 @@ __device__ __forceinline__ uint2 codes8(const float* v, float s) {
 
 enum Sink { kSinkTensors = 0, kSinkE4m3 = 1, kSinkBf16 = 2 };
 
-// One block: one token's units [chunk * kThreads, ...). A token's units are
-// q's heads, then k's, then (with a cache) v's.
+// A token's heads are q's, then k's, then (with a cache) v's. Warp w of the grid
+// takes heads [part * per_warp, ...) of token w / parts, part = w % parts.
 template <int SINK, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, int chunks) {
-  __shared__ float2 turn[256];   // (cos, sin) of pair 8 u + j at j * (rot / 16) + u
-  const int t = blockIdx.x / chunks;
-  const int unit = (blockIdx.x - t * chunks) * kThreads + threadIdx.x;
-  const int per_head = a.head_dim / kUnit;
+__global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a, int parts,
+                                                             int per_warp) {
+  extern __shared__ float2 turns[];   // (cos, sin) of the warp's token, [kWarps][rot / 2]
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = (int)(w / parts);
+  if (t >= a.T) return;
+  const int units = a.head_dim / kUnit;              // of a head: lanes
+  const int at_once = 32 / units;                    // heads
+  const int u = lane % units;
+  const int heads = a.q_heads + (SINK == kSinkTensors ? a.k_heads : 2 * a.k_heads);
+  const int begin = (int)(w - (int64_t)t * parts) * per_warp;
+  const int end = min(heads, begin + per_warp);
+  const int mine = lane < at_once * units ? begin + lane / units : end;   // first head
   const int rot_units = a.rot / kUnit;
-  const int head = unit / per_head, u = unit - head * per_head;
+  const int32_t slot = SINK == kSinkTensors ? -1 : a.slots[t];
+  const bool kept = SINK != kSinkTensors && (uint32_t)slot < a.cache_slots;
 
-  // what this thread's unit belongs to
-  const uint16_t* src = nullptr;
-  uint16_t* dst = nullptr;       // kSinkTensors and q
-  bool rotated = u < rot_units;
-  int kv_head = -1;              // cache head, when the unit goes to the cache
-  bool is_v = false;
-  int32_t slot = -1;
-  if (head < a.q_heads) {
-    src = a.q + t * a.q_stride + head * a.head_dim;
-    dst = a.q_out + t * a.q_out_stride + head * a.head_dim;
-  } else if (SINK == kSinkTensors) {
-    if (head < a.q_heads + a.k_heads) {
-      const int h = head - a.q_heads;
-      src = a.k + t * a.k_stride + h * a.head_dim;
-      dst = a.k_out + t * a.k_out_stride + h * a.head_dim;
-    }
-  } else if (head < a.q_heads + 2 * a.k_heads) {
-    slot = a.slots[t];
-    if ((uint32_t)slot < a.cache_slots) {
-      kv_head = head - a.q_heads;
-      is_v = kv_head >= a.k_heads;
-      if (is_v) kv_head -= a.k_heads;
-      src = is_v ? a.v + t * a.v_stride + kv_head * a.head_dim
-                 : a.k + t * a.k_stride + kv_head * a.head_dim;
-      if (is_v) rotated = false;
-    }
-  }
-  // the unit's two runs of 8 elements
-  const bool split = rotated && !NEIGHBOURS;
-  const int o0 = split ? 8 * u : kUnit * u;
-  const int o1 = split ? a.rot / 2 + 8 * u : kUnit * u + 8;
-  uint4 raw0 = make_uint4(0, 0, 0, 0), raw1 = raw0;
-  if (src != nullptr) {
-    raw0 = *reinterpret_cast<const uint4*>(src + o0);
-    raw1 = *reinterpret_cast<const uint4*>(src + o1);
-  }
-  for (int p = threadIdx.x; p < a.rot / 2; p += kThreads) {
-    const int axis = a.pair_axis[p];
-    const int32_t pos = axis < a.axes ? a.positions[(int64_t)axis * a.T + t] : 0;
-    const uint64_t f = (uint64_t)(int64_t)pos * a.turns[p];
-    float s, c;
-    sincospif((float)(int32_t)(f >> 32) * 0x1p-31f, &s, &c);
-    turn[(p & 7) * rot_units + (p >> 3)] = make_float2(c, a.inverse ? -s : s);
-  }
-  __syncthreads();
+  // the lane's two runs of 8 elements in a rotated head, and in one of v
+  const bool rotates = u < rot_units;
+  const int from = rotates ? 0 : a.rot, region = rotates ? a.rot : a.head_dim - a.rot;
+  const int run0 = from + 8 * (rotates ? u : u - rot_units), run1 = run0 + region / 2;
+  const int v_run0 = 8 * u, v_run1 = v_run0 + a.head_dim / 2;
+  const int q_end = a.q_heads, k_end = q_end + a.k_heads;
 
-  float x[kUnit];
-  unpack8(raw0, x);
-  unpack8(raw1, x + 8);
-  if (rotated) {
+  auto source = [&](int head) -> const uint16_t* {
+    if (head < q_end) return a.q + t * a.q_stride + head * a.head_dim;
+    if (SINK != kSinkTensors && !kept) return nullptr;
+    if (head < k_end) return a.k + t * a.k_stride + (head - q_end) * a.head_dim;
+    return a.v + t * a.v_stride + (head - k_end) * a.head_dim;
+  };
+  uint4 raw[kAhead][2];
+  auto load = [&](int head, uint4 (&r)[2]) {
+    r[0] = r[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (head >= end) return;
+    const uint16_t* src = source(head);
+    if (src == nullptr) return;
+    const bool is_v = SINK != kSinkTensors && head >= k_end;
+    r[0] = *reinterpret_cast<const uint4*>(src + (is_v ? v_run0 : run0));
+    r[1] = *reinterpret_cast<const uint4*>(src + (is_v ? v_run1 : run1));
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(mine + i * at_once, raw[i]);
+
+  // cosines of the token's pairs
+  float2 cs[8];
+  if (a.rot > 0) {
+    float2* const table = turns + (threadIdx.x >> 5) * (a.rot / 2);
+    for (int p = lane; p < a.rot / 2; p += 32) {
+      const int axis = a.pair_axis[p];
+      const int32_t pos = axis < a.axes ? a.positions[(int64_t)axis * a.T + t] : 0;
+      const uint64_t f = (uint64_t)(int64_t)pos * a.turns[p];
+      float s, c;
+      sincospif((float)(int32_t)(f >> 32) * 0x1p-31f, &s, &c);
+      table[p] = make_float2(c, a.inverse ? -s : s);
+    }
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 cs = turn[j * rot_units + u];
-      float& x1 = NEIGHBOURS ? x[2 * j] : x[j];
-      float& x2 = NEIGHBOURS ? x[2 * j + 1] : x[8 + j];
-      const float y1 = fmaf(x1, cs.x, -(x2 * cs.y));
-      x2 = fmaf(x2, cs.x, x1 * cs.y);
-      x1 = y1;
+      // pairs (i, i + rot / 2): run0[j] with run1[j]; neighbours: four in each run
+      const int p = NEIGHBOURS ? (j < 4 ? 4 * u + j : a.rot / 4 + 4 * u + j - 4) : 8 * u + j;
+      cs[j] = rotates ? table[p] : make_float2(1.f, 0.f);
     }
   }
 
-  if (SINK != kSinkTensors && kv_head >= 0) dst = nullptr;
-  if (dst != nullptr) {
-    *reinterpret_cast<uint4*>(dst + o0) = pack8(x);
-    *reinterpret_cast<uint4*>(dst + o1) = pack8(x + 8);
-  }
-  if (SINK == kSinkTensors) return;
-
-  float amax = 0.f;
-  if (SINK == kSinkE4m3) {
+  const int64_t row0 = ((int64_t)(slot >> a.page_shift) * a.k_heads << a.page_shift) +
+                       (slot & ((1 << a.page_shift) - 1));   // of kv head 0
+  for (int head0 = mine; head0 - mine + begin < end; head0 += kAhead * at_once) {
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) amax = fmaxf(amax, fabsf(x[j]));
-    for (int o = per_head >> 1; o > 0; o >>= 1)
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  }
-  if (kv_head < 0) return;
-  const int64_t row =
-      ((int64_t)(slot >> a.page_shift) * a.k_heads + kv_head) * (int64_t(1) << a.page_shift) +
-      (slot & ((1 << a.page_shift) - 1));
-  if (SINK == kSinkE4m3) {
-    const float s = __fdiv_rn(fmaxf(amax, 1e-12f), 448.0f);
-    uint8_t* out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
-    *reinterpret_cast<uint2*>(out + o0) = codes8(x, s);
-    *reinterpret_cast<uint2*>(out + o1) = codes8(x + 8, s);
-    if (u == 0) (is_v ? a.v_scale : a.k_scale)[row] = s;
-  } else {
-    uint16_t* out = static_cast<uint16_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
-    *reinterpret_cast<uint4*>(out + o0) = pack8(x);
-    *reinterpret_cast<uint4*>(out + o1) = pack8(x + 8);
+    for (int i = 0; i < kAhead; ++i) {
+      const int head = head0 + i * at_once;
+      const bool is_v = SINK != kSinkTensors && head >= k_end;
+      float x[kUnit];
+      unpack8(raw[i][0], x);
+      unpack8(raw[i][1], x + 8);
+      load(head + kAhead * at_once, raw[i]);
+      if (rotates && !is_v) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float& x1 = NEIGHBOURS ? x[2 * j] : x[j];
+          float& x2 = NEIGHBOURS ? x[2 * j + 1] : x[8 + j];
+          const float y1 = fmaf(x1, cs[j].x, -(x2 * cs[j].y));
+          x2 = fmaf(x2, cs[j].x, x1 * cs[j].y);
+          x1 = y1;
+        }
+      }
+      const int o0 = is_v ? v_run0 : run0, o1 = is_v ? v_run1 : run1;
+      uint16_t* dst = nullptr;
+      if (head < end) {
+        if (head < q_end) dst = a.q_out + t * a.q_out_stride + head * a.head_dim;
+        else if (SINK == kSinkTensors)
+          dst = a.k_out + t * a.k_out_stride + (head - q_end) * a.head_dim;
+      }
+      if (dst != nullptr) {
+        *reinterpret_cast<uint4*>(dst + o0) = pack8(x);
+        *reinterpret_cast<uint4*>(dst + o1) = pack8(x + 8);
+      }
+      if (SINK == kSinkTensors) continue;
+
+      float amax = 0.f;
+      if (SINK == kSinkE4m3) {
+#pragma unroll
+        for (int j = 0; j < kUnit; ++j) amax = fmaxf(amax, fabsf(x[j]));
+        for (int o = units >> 1; o > 0; o >>= 1)
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      }
+      if (head < q_end || head >= end || !kept) continue;
+      const int kv_head = is_v ? head - k_end : head - q_end;
+      const int64_t row = row0 + ((int64_t)kv_head << a.page_shift);
+      if (SINK == kSinkE4m3) {
+        const float s = __fdiv_rn(fmaxf(amax, 1e-12f), 448.0f), y = __frcp_rn(s);
+        uint8_t* out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
+        *reinterpret_cast<uint2*>(out + o0) = codes8(x, s, y);
+        *reinterpret_cast<uint2*>(out + o1) = codes8(x + 8, s, y);
+        if (u == 0) (is_v ? a.v_scale : a.k_scale)[row] = s;
+      } else {
+        uint16_t* out = static_cast<uint16_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
+        *reinterpret_cast<uint4*>(out + o0) = pack8(x);
+        *reinterpret_cast<uint4*>(out + o1) = pack8(x + 8);
+      }
+    }
   }
 }
 
@@ -171,19 +210,28 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
 
 int launch_rotary(const RotaryArgs& a, int sink, bool neighbours, cudaStream_t stream) {
   const int heads = a.q_heads + (sink == kSinkTensors ? a.k_heads : 2 * a.k_heads);
-  const int units = heads * (a.head_dim / kUnit);
-  const int chunks = (units + kThreads - 1) / kThreads;
-  const int64_t blocks = (int64_t)chunks * a.T;
+  const int at_once = 32 / (a.head_dim / kUnit);
+  const int steps = (heads + at_once - 1) / at_once;   // of a warp that has all heads
+  // Heads of a token go to one warp when the tokens fill the GPU (152 SMs with
+  // 24 warps each); with fewer tokens they are spread, down to one step a warp.
+  const int64_t full = 152 * 24;
+  const int64_t want = std::max<int64_t>(1, (int64_t)a.T * steps / full);
+  const int take = (int)std::min<int64_t>(steps, want);
+  const int per_warp = take * at_once;
+  const int parts = (heads + per_warp - 1) / per_warp;
+  const int64_t blocks = ((int64_t)parts * a.T + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffff) return -2;
-  void (*kernel)(RotaryArgs, int) = nullptr;
+  void (*kernel)(RotaryArgs, int, int) = nullptr;
   if (sink == kSinkTensors)
     kernel = neighbours ? rotary_kernel<kSinkTensors, true> : rotary_kernel<kSinkTensors, false>;
   else if (sink == kSinkE4m3)
     kernel = neighbours ? rotary_kernel<kSinkE4m3, true> : rotary_kernel<kSinkE4m3, false>;
   else
     kernel = neighbours ? rotary_kernel<kSinkBf16, true> : rotary_kernel<kSinkBf16, false>;
-  kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a, chunks);
-  return cudaGetLastError() == cudaSuccess ? 0 : -3;
+  const size_t smem = (size_t)kWarps * (a.rot / 2) * sizeof(float2);
+  const cudaError_t e = launch_kernel(true, dim3((unsigned)blocks), dim3(kWarps * 32), smem,
+                                      stream, kernel, a, parts, per_warp);
+  return e == cudaSuccess ? 0 : -3;
 }
 
 }  // namespace moe

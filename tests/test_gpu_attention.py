@@ -480,3 +480,28 @@ def test_attention_tensor_refusals():
     with pytest.raises(MoeError) as e:
         cache.attend(q, t, n, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == -4
+
+
+def test_write_divides_like_ieee_for_every_pair_of_mantissas():
+    """Every bf16 mantissa against every mantissa of the row's largest element,
+    over the 19 binades that reach a code: the codes equal those of an IEEE
+    division (the oracle's), for small and large rows."""
+    top = (128 + np.arange(128)) / 128.0                               # [1, 2)
+    small = ((128 + np.arange(128))[:, None] / 128.0 * 2.0 ** -np.arange(19.0)).reshape(-1)
+    for shift in (0, 60, -40):
+        rows = []
+        for m in top:
+            v = small[small <= m]
+            v = np.concatenate([v, np.zeros(-len(v) % 63)]).reshape(-1, 63)
+            rows.append(np.concatenate([np.full((len(v), 1), m), v], 1))
+        x = (np.concatenate(rows) * 2.0 ** shift).astype(np.float32)
+        x[::2] *= -1
+        t = torch.from_numpy(x)[:, None].to(torch.bfloat16).cuda()
+        assert np.array_equal(values(t)[:, 0], x)                      # bf16 values
+        T = len(x)
+        cache = fresh_cache(-(-T // 64), 1, 64, 64, "e4m3")
+        cache.write(t, t, torch.arange(T, dtype=torch.int32, device="cuda"))
+        codes, scales = oracle.quant_rows_ref(x)
+        kc, vc, ks, _ = host(cache)
+        assert np.array_equal(kc.reshape(-1, 64)[:T], codes)
+        assert np.array_equal(vc, kc) and np.array_equal(ks.reshape(-1)[:T], scales)
