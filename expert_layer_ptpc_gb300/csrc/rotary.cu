@@ -16,8 +16,8 @@
 // a run of its heads. It works out the token's cosines together, two pairs a lane
 // for 128 elements, and every lane keeps the 8 that its elements need in
 // registers over all the heads. A lane's unit of a head is two runs of 8 elements,
-// half a region apart, so that the lanes' 16-byte accesses are contiguous; four
-// units are loaded before the first is used. A cache head is 4, 8 or 16 units,
+// half a region apart, so that the lanes' 16-byte accesses are contiguous; the
+// next units are loaded before one is used. A cache head is 4, 8 or 16 units,
 // hence that many neighbouring lanes, and its row maximum is a shuffle.
 #include <algorithm>
 
@@ -31,7 +31,12 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kUnit = 16;     // elements of a lane
-constexpr int kAhead = 4;     // units loaded before the first is used
+// Blocks of an SM, and the units that a lane loads before it uses the first: 32
+// warps an SM, whose 64 registers a lane hold two units ahead, or one next to the
+// cosines and the quantiser. (GB300, 8192 tokens of 64 + 4 heads of 128: the
+// rotation takes 45.9 us with 2 ahead, 47.9 with 1, 46.7 with 4 and 24 warps; with
+// the cache's write 51.8 with 1, 56.8 with 2, 53.7 with 2 and 24 warps.)
+constexpr int kBlocks = 4;
 
 __device__ __forceinline__ void unpack8(const uint4& raw, float* v) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -76,12 +81,15 @@ __device__ __forceinline__ uint2 codes8(const float* v, float s, float y) {
 }
 
 enum Sink { kSinkTensors = 0, kSinkE4m3 = 1, kSinkBf16 = 2 };
+enum Pairs { kNoPairs = 0, kHalves = 1, kNeighbours = 2 };
 
 // A token's heads are q's, then k's, then (with a cache) v's. Warp w of the grid
 // takes heads [part * per_warp, ...) of token w / parts, part = w % parts.
-template <int SINK, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a, int parts,
-                                                             int per_warp) {
+template <int SINK, int PAIRS>
+__global__ void __launch_bounds__(kWarps * 32, kBlocks)
+    rotary_kernel(const RotaryArgs a, int parts, int per_warp) {
+  constexpr bool NEIGHBOURS = PAIRS == kNeighbours;
+  constexpr int kAhead = SINK == kSinkTensors || PAIRS == kNoPairs ? 2 : 1;
   extern __shared__ float2 turns[];   // (cos, sin) of the warp's token, [kWarps][rot / 2]
   pdl_wait();
   pdl_launch_dependents();
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a,
   const int begin = (int)(w - (int64_t)t * parts) * per_warp;
   const int end = min(heads, begin + per_warp);
   const int mine = lane < at_once * units ? begin + lane / units : end;   // first head
-  const int rot_units = a.rot / kUnit;
+  const int rot_units = PAIRS == kNoPairs ? 0 : a.rot / kUnit;
   const int32_t slot = SINK == kSinkTensors ? -1 : a.slots[t];
   const bool kept = SINK != kSinkTensors && (uint32_t)slot < a.cache_slots;
 
@@ -107,9 +115,10 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a,
   const int v_run0 = 8 * u, v_run1 = v_run0 + a.head_dim / 2;
   const int q_end = a.q_heads, k_end = q_end + a.k_heads;
 
+  // (keys and values of a token without a slot are read all the same: the
+  // loads need not wait for the slot)
   auto source = [&](int head) -> const uint16_t* {
-    if (head < q_end) return a.q + t * a.q_stride + head * a.head_dim;
-    if (SINK != kSinkTensors && !kept) return nullptr;
+    if (PAIRS != kNoPairs && head < q_end) return a.q + t * a.q_stride + head * a.head_dim;
     if (head < k_end) return a.k + t * a.k_stride + (head - q_end) * a.head_dim;
     return a.v + t * a.v_stride + (head - k_end) * a.head_dim;
   };
@@ -118,7 +127,6 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a,
     r[0] = r[1] = make_uint4(0u, 0u, 0u, 0u);
     if (head >= end) return;
     const uint16_t* src = source(head);
-    if (src == nullptr) return;
     const bool is_v = SINK != kSinkTensors && head >= k_end;
     r[0] = *reinterpret_cast<const uint4*>(src + (is_v ? v_run0 : run0));
     r[1] = *reinterpret_cast<const uint4*>(src + (is_v ? v_run1 : run1));
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a,
 
   // cosines of the token's pairs
   float2 cs[8];
-  if (a.rot > 0) {
+  if (PAIRS != kNoPairs) {
     float2* const table = turns + (threadIdx.x >> 5) * (a.rot / 2);
     for (int p = lane; p < a.rot / 2; p += 32) {
       const int axis = a.pair_axis[p];
@@ -158,7 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a,
       unpack8(raw[i][0], x);
       unpack8(raw[i][1], x + 8);
       load(head + kAhead * at_once, raw[i]);
-      if (rotates && !is_v) {
+      if (PAIRS != kNoPairs && rotates && !is_v) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float& x1 = NEIGHBOURS ? x[2 * j] : x[j];
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a,
       }
       const int o0 = is_v ? v_run0 : run0, o1 = is_v ? v_run1 : run1;
       uint16_t* dst = nullptr;
-      if (head < end) {
+      if (PAIRS != kNoPairs && head < end) {
         if (head < q_end) dst = a.q_out + t * a.q_out_stride + head * a.head_dim;
         else if (SINK == kSinkTensors)
           dst = a.k_out + t * a.k_out_stride + (head - q_end) * a.head_dim;
@@ -179,7 +187,8 @@ __global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a,
         *reinterpret_cast<uint4*>(dst + o0) = pack8(x);
         *reinterpret_cast<uint4*>(dst + o1) = pack8(x + 8);
       }
-      if (SINK == kSinkTensors) continue;
+      // (the warp's heads of this step, all q's: nothing for the cache)
+      if (SINK == kSinkTensors || head0 - mine + begin + (i + 1) * at_once <= q_end) continue;
 
       float amax = 0.f;
       if (SINK == kSinkE4m3) {
@@ -223,11 +232,15 @@ int launch_rotary(const RotaryArgs& a, int sink, bool neighbours, cudaStream_t s
   if (blocks > 0x7fffffff) return -2;
   void (*kernel)(RotaryArgs, int, int) = nullptr;
   if (sink == kSinkTensors)
-    kernel = neighbours ? rotary_kernel<kSinkTensors, true> : rotary_kernel<kSinkTensors, false>;
+    kernel = neighbours ? rotary_kernel<kSinkTensors, kNeighbours>
+                        : rotary_kernel<kSinkTensors, kHalves>;
+  else if (a.rot == 0)   // keys and values as they are
+    kernel = sink == kSinkE4m3 ? rotary_kernel<kSinkE4m3, kNoPairs>
+                               : rotary_kernel<kSinkBf16, kNoPairs>;
   else if (sink == kSinkE4m3)
-    kernel = neighbours ? rotary_kernel<kSinkE4m3, true> : rotary_kernel<kSinkE4m3, false>;
+    kernel = neighbours ? rotary_kernel<kSinkE4m3, kNeighbours> : rotary_kernel<kSinkE4m3, kHalves>;
   else
-    kernel = neighbours ? rotary_kernel<kSinkBf16, true> : rotary_kernel<kSinkBf16, false>;
+    kernel = neighbours ? rotary_kernel<kSinkBf16, kNeighbours> : rotary_kernel<kSinkBf16, kHalves>;
   const size_t smem = (size_t)kWarps * (a.rot / 2) * sizeof(float2);
   const cudaError_t e = launch_kernel(true, dim3((unsigned)blocks), dim3(kWarps * 32), smem,
                                       stream, kernel, a, parts, per_warp);

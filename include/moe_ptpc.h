@@ -665,7 +665,7 @@ typedef struct moe_kv_cache {
  * moe_kv_write - store T tokens' keys and values, quantised on the way when
  * the cache is e4m3. k, v [T, heads, head_dim] bf16 with k_stride and
  * v_stride elements between tokens; slots [T] int32. A token whose slot lies
- * outside [0, pages * page_size) is not read and not written. Two tokens of
+ * outside [0, pages * page_size) is not written. Two tokens of
  * one call in the same slot are outside the contract.
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
  *         pointers, bad strides, T < 0). T == 0 is a no-op.
