@@ -505,3 +505,37 @@ def test_write_divides_like_ieee_for_every_pair_of_mantissas():
         kc, vc, ks, _ = host(cache)
         assert np.array_equal(kc.reshape(-1, 64)[:T], codes)
         assert np.array_equal(vc, kc) and np.array_equal(ks.reshape(-1)[:T], scales)
+
+
+@pytest.mark.parametrize("lengths,hq,hk,d,kind", [
+    ([70001], 16, 1, 128, "e4m3"),            # one item on every CTA
+    ([40000, 1, 0, 300], 8, 2, 64, "bf16"), ([3000] * 5, 6, 6, 128, "e4m3"),
+    ([20000, 20000], 2, 1, 256, "e4m3"), ([0, 200], 40, 2, 128, "e4m3"),
+])
+def test_attention_workspace_of_any_content_is_not_passed(lengths, hq, hk, d, kind):
+    """A workspace of any content, between guard bands that stay."""
+    cache, q, table = attention_case(47, lengths, hq, hk, d, 16, kind)
+    want = check_attention(cache, q, table, lengths)
+    from expert_layer_ptpc_gb300 import binding
+    need = binding.moe_paged_attention_workspace_size(cache.struct, len(lengths), hq)
+    wide = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    t = torch.from_numpy(table).cuda()
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    for fill in (0xA5, 0xFF, 0):
+        wide[256:256 + need] = fill
+        out, lse = cache.attend(q, t, n, return_lse=True, ws=wide[256:256 + need])
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert bool((wide[:256] == 0xA5).all()) and bool((wide[256 + need:] == 0xA5).all())
+
+
+def test_attention_whole_contexts_and_cut_ones_agree():
+    """Short tables run without the cut; a wider table of the same contexts runs
+    with it, with the same results up to the order of the sums."""
+    lengths = [1, 0, 200, 256, 77]
+    cache, q, table = attention_case(53, lengths, 24, 2, 128, 16, "e4m3")
+    check_attention(cache, q, table, lengths)
+    wide = np.full((5, 4000), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    check_attention(cache, q, wide, lengths)
+    check_attention(cache, q, wide, lengths, window=100)
+    check_attention(cache, q, table, lengths, window=100)
