@@ -55,7 +55,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                 // tokens of one tensor core contraction
 constexpr int kRows = 16;                  // query heads of a work item
-constexpr int kMaxCtasPerSm = 4;
+constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxWorkers = kSms * kMaxCtasPerSm;
 constexpr float kSlack = 8.0f;             // log2 by which a weight may pass 1
 // What an item of a context costs beside its units, in units: fetching q, and
@@ -68,11 +68,13 @@ constexpr int kLengths = 256;              // contexts whose lengths a worker ke
 // 7.6 us against 8.0 us cut in three, and one launch less.)
 constexpr int kWholeUnits = 4;
 
-// Where a segment that several workers share left its pieces: the first
+// An item that several workers share, and where they left its pieces: the first
 // worker's in slot 2 first + 1, worker w's after it in slot 2 w.
 struct Joint {
+  int32_t item;     // of all the batch's
   int32_t first;    // the first worker
-  int32_t pieces;   // number of workers; 1: nothing to join
+  int32_t pieces;   // number of workers; below 2: nothing to join
+  int32_t pad;
 };
 
 struct Args {
@@ -87,7 +89,9 @@ struct Args {
   int whole;                   // a CTA takes one item, all of it
   uint16_t* out;
   float* lse;
-  Joint* joints;               // [batch][heads * chunks]
+  Joint* joints;               // [joint_count]: by item, or by the item's first worker
+  int joint_count;             // the fewer of the two
+  int by_worker;
   float2* stats;               // [slots][kRows] (M, l)
   float* parts;                // [slots][kRows][D]
 };
@@ -138,7 +142,7 @@ struct Shape {
     const int row = piece / (kRowBytes / 16);
     return (piece ^ (row & 6)) * 16;
   }
-  static_assert(kCtas * (kSmemBytes + 1536) <= 227 * 1024, "shared memory");
+  static_assert(kCtas * (kSmemBytes + 1024 + 2048) <= 228 * 1024, "shared memory");
   static_assert(kCtas <= kMaxCtasPerSm, "workspace slots");
 };
 
@@ -307,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 stats[2][kRows];
   __shared__ int lengths[kLengths];
+  __shared__ Walker walkers[kWarps][2];   // a warp's: of the work, and of the copies
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;    // row (or column) and place in a tile's fragments
   uint8_t* const stage0 = smem + warp * S::kWarpBytes;
@@ -339,6 +344,10 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     for (int b = lane; b < a.batch; b += 32) total += places_of(b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x)
+      if (places_of(b) == 0)
+        for (int item = 0; item < items; ++item) zero_rows(a, b, item, D);
+    if (a.by_worker && threadIdx.x == 0) a.joints[worker].pieces = 0;
     workers = min((int64_t)gridDim.x, total);
     if (worker >= workers) return;
     const int64_t cut = quotient(total * (worker + (lane & 1)), workers);
@@ -366,21 +375,31 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       lengths[i] = first + i < a.batch ? a.lengths[first + i] : 0;
     __syncthreads();
   }
-  Walker walker;
-  walker.place = lo;
-  walker.stop = hi;
-  walker.b = first;
-  walker.span = span_of(a, a.lengths[first], S::kUnit);
   {
+    Walker w;
+    w.place = lo;
+    w.stop = hi;
+    w.b = first;
+    w.span = span_of(a, a.lengths[first], S::kUnit);
     const int64_t past = lo - before;
-    const uint32_t size = kItemCost + walker.span.units;
+    const uint32_t size = kItemCost + w.span.units;
     const int item = (int)quotient(past, size);
-    walker.kv = item / a.chunks;
-    walker.chunk = item - walker.kv * a.chunks;
-    walker.in = (uint32_t)(past - (int64_t)item * size);
-    if (walker.kv >= a.c.heads) walker.stop = lo;   // (as above)
+    w.kv = item / a.chunks;
+    w.chunk = item - w.kv * a.chunks;
+    w.in = (uint32_t)(past - (int64_t)item * size);
+    if (w.kv >= a.c.heads) w.stop = lo;   // (as above)
+    if (lane < 2) walkers[warp][lane] = w;
+    __syncwarp();
   }
-
+  // (in shared memory: they are wanted once a segment, and registers are scarce)
+  auto next_segment = [&](int which, Segment& s) -> bool {
+    Walker w = walkers[warp][which];
+    const bool got = w.next(a, lengths, first, S::kUnit, s);
+    __syncwarp();   // every lane has read it
+    if (lane == 0) walkers[warp][which] = w;
+    __syncwarp();
+    return got;
+  };
   // ---- copies: the tiles of all segments, one after the other ----
   // Tile i of a segment holds the tokens from first_token + i kUnit on; the
   // warps' tiles of a unit follow each other.
@@ -403,13 +422,12 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     int kv;
     uint32_t begin;
   };
-  Walker ahead = walker;
   Segment source;
   int source_left = 0;          // its tiles still to copy, the next one included
   Pending next_tile = {true, 0u, -1, 0, 0u};
   auto ask = [&]() {
     while (source_left == 0) {
-      if (!ahead.next(a, lengths, first, S::kUnit, source)) {
+      if (!next_segment(1, source)) {
         next_tile.more = false;
         return;
       }
@@ -566,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   }
   Segment seg;
   int stage = 0, n = 0;   // of the next tile: its stage, and its number (for put_scales)
-  bool running = walker.next(a, lengths, first, S::kUnit, seg);
+  bool running = next_segment(0, seg);
   if (running) ask_q(seg);
   {
     float ks[S::kStages], vs[S::kStages];
@@ -787,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
 
     // ---- join the warps ----
     const Segment done = seg;
-    running = walker.next(a, lengths, first, S::kUnit, seg);
+    running = next_segment(0, seg);
     if (running) ask_q(seg);
 #pragma unroll
     for (int r = 0; r < 2; ++r) sum[r] = quad_sum(sum[r]);
@@ -873,23 +891,27 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     }
     if (done.u0 == 0 && threadIdx.x == 0 && !a.whole) {
       Joint j;
+      j.item = (int32_t)(((int64_t)done.b * a.c.heads + done.kv) * a.chunks + done.chunk);
       j.first = (int32_t)worker;
       j.pieces = 1;
+      j.pad = 0;
       if (!whole) {
         // place p belongs to the largest worker w with floor(total w / workers) <= p
-        const int64_t last = min(quotient(done.end * workers + total - 1, total), workers) - 1;
+        const int64_t last =
+            min(quotient(done.end * workers + total - 1, total), workers) - 1;
         j.pieces = (int32_t)(last - worker + 1);
       }
-      a.joints[((int64_t)done.b * a.c.heads + done.kv) * a.chunks + done.chunk] = j;
+      if (!a.by_worker) a.joints[j.item] = j;
+      else if (!whole) a.joints[worker] = j;   // (a worker has one such item at most)
     }
   }
   cp_wait<0>();   // (only empty groups are left)
 }
 
-// Joins the pieces of the items that several workers share, and writes the
-// rows of contexts without tokens. A block takes one item's rows, or a share of
-// them when there are few items; a row gets kJoinWarps / rows-a-block warps, each
-// of which takes every so many-th piece with a running bound.
+// Joins the pieces of the items that several workers share. A block takes one
+// item's rows, or a share of them when there are few items; a row gets kJoinWarps /
+// rows-a-block warps, each of which takes every so many-th piece with a running
+// bound.
 constexpr int kJoinWarps = 16;
 
 template <int D>
@@ -899,19 +921,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int
   __shared__ float sacc[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int items = a.c.heads * a.chunks;
-  const int b = blockIdx.x / items, item = blockIdx.x - b * items;
+  const int share = gridDim.y;                 // warps of a row: a power of two
+  const int row = blockIdx.y * (kJoinWarps / share) + warp / share;
+  // by item, one of a context without tokens has no joint
+  const bool none =
+      !a.by_worker && span_of(a, a.lengths[blockIdx.x / items], unit).units == 0;
+  pdl_wait();
+  if (none) return;
+  const Joint j = a.joints[blockIdx.x];
+  if (j.pieces < 2) return;
+  const int b = j.item / items, item = j.item - b * items;
   const int kv = item / a.chunks;
   const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;
   const int rows = min(kRows, (kv + 1) * a.group - head0);
-  const int share = gridDim.y;                 // warps of a row: a power of two
-  const int row = blockIdx.y * (kJoinWarps / share) + warp / share;
-  const bool empty = span_of(a, a.lengths[b], unit).units == 0;
-  pdl_wait();
-  Joint j = {0, 0};
-  if (!empty) {
-    j = a.joints[blockIdx.x];
-    if (j.pieces == 1) return;
-  }
   float m = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
@@ -1007,14 +1029,16 @@ int launch(const Args& a, cudaStream_t stream) {
   args.whole = room <= kWholeUnits * S::kUnit && items <= kSms * S::kCtas;
   const int grid = args.whole ? (int)items
                               : (int)std::min<int64_t>(kSms * S::kCtas, items * (units + kItemCost));
+  args.joint_count = (int)std::min<int64_t>(items, grid);
+  args.by_worker = args.joint_count < items;
   cudaError_t e = launch_kernel(true, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
                                 paged_attention_kernel<E4M3, D>, args);
   if (e != cudaSuccess) return -3;
   if (args.whole) return 0;
   // few items: a row's pieces go to several warps (2 blocks an SM hold 16 each)
   int share = 1;
-  while (share < kJoinWarps && 2 * share * items <= 2 * kSms) share *= 2;
-  e = launch_kernel(true, dim3((unsigned)items, share), dim3(kJoinWarps * 32), 0, stream,
+  while (share < kJoinWarps && 2 * share * args.joint_count <= 2 * kSms) share *= 2;
+  e = launch_kernel(true, dim3(args.joint_count, share), dim3(kJoinWarps * 32), 0, stream,
                     join_kernel<D>, args, S::kUnit);
   return e == cudaSuccess ? 0 : -3;
 }
@@ -1022,7 +1046,8 @@ int launch(const Args& a, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_attention_ws_bytes(int heads, int head_dim, int batch, int q_heads) {
-  const size_t items = (size_t)batch * heads * chunks_of(q_heads / heads);
+  const size_t items =
+      std::min<size_t>((size_t)batch * heads * chunks_of(q_heads / heads), kMaxWorkers);
   const size_t slots = 2 * kMaxWorkers;
   return align256(items * sizeof(Joint)) + align256(slots * kRows * sizeof(float2)) +
          slots * kRows * head_dim * sizeof(float);
@@ -1046,7 +1071,8 @@ int launch_paged_attention(const CacheView& c, const uint16_t* q, int64_t q_stri
   a.lse = lse;
   uint8_t* p = static_cast<uint8_t*>(ws);
   a.joints = reinterpret_cast<Joint*>(p);
-  p += align256((size_t)batch * c.heads * a.chunks * sizeof(Joint));
+  p += align256(std::min<size_t>((size_t)batch * c.heads * a.chunks, kMaxWorkers) *
+                sizeof(Joint));
   a.stats = reinterpret_cast<float2*>(p);
   p += align256(2 * kMaxWorkers * kRows * sizeof(float2));
   a.parts = reinterpret_cast<float*>(p);
