@@ -111,7 +111,8 @@ class PagedKVCache:
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if coded else None,
             v_scale.data_ptr() if coded else None, self.pages, self.heads, self.page_size,
             self.head_dim, dtypes[k.dtype])
-        self._ws, self._need_ws = {}, {}
+        self._ws = {}
+        self._scale = 1.0 / math.sqrt(self.head_dim)
 
     @classmethod
     def empty(cls, pages, heads, page_size, head_dim, dtype="e4m3", device="cuda"):
@@ -151,18 +152,20 @@ class PagedKVCache:
     def workspace(self, batch, q_heads, stream=None):
         """The attention workspace of one stream, kept for the next step (calls
         on different streams may overlap, so each stream has its own)."""
-        need = self._need_ws.get((batch, q_heads))
-        if need is None:
-            need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
-            self._need_ws[batch, q_heads] = need
+        if torch.cuda.is_current_stream_capturing():
+            return self._new_workspace(batch, q_heads, stream)   # the graph's own
         on = binding._raw_stream(stream, self.k)
-        ws = self._ws.get(on)
-        if ws is None or ws.numel() < need:
-            ws = binding._empty(max(need, 1), torch.uint8, self.k.device, stream)
-            # memory of a graph under capture belongs to that graph
-            if not torch.cuda.is_current_stream_capturing():
-                self._ws[on] = ws
+        ws = self._ws.get((on, batch, q_heads))
+        if ws is None:
+            need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
+            held = [w for (o, *_), w in self._ws.items() if o == on and w.numel() >= need]
+            ws = held[0] if held else self._new_workspace(batch, q_heads, stream)
+            self._ws[on, batch, q_heads] = ws
         return ws
+
+    def _new_workspace(self, batch, q_heads, stream):
+        need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
+        return binding._empty(max(need, 1), torch.uint8, self.k.device, stream)
 
     def attend(self, q, block_table, lengths, scale=None, window=0, out=None, lse=None,
                return_lse=False, ws=None, stream=None):
@@ -171,11 +174,8 @@ class PagedKVCache:
         `window` of them when window > 0). scale: default 1 / sqrt(head_dim).
         Returns out, or (out, lse) with `return_lse` or `lse`."""
         if scale is None:
-            scale = 1.0 / math.sqrt(self.head_dim)
+            scale = self._scale
         if ws is None:
             ws = self.workspace(q.shape[0], q.shape[1], stream)
-        if return_lse and lse is None:
-            lse = binding._empty(q.shape[:2], torch.float32, q.device, stream)
-        out = binding.moe_paged_attention(self.struct, q, block_table, lengths, scale, window,
-                                          out, lse, ws, stream)
-        return out if lse is None else (out, lse)
+        return binding.moe_paged_attention(self.struct, q, block_table, lengths, scale, window,
+                                           out, lse, ws, stream, return_lse or lse is not None)

@@ -705,10 +705,12 @@ def moe_rotary(plan, positions, q, k=None, inverse=False, q_out=None, k_out=None
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _check("moe_rotary", load_library().moe_rotary(
+    status = (_lib or load_library()).moe_rotary(
         ctypes.byref(plan), positions.data_ptr(), T, d, q.data_ptr(), q_stride, hq,
         q_out.data_ptr(), qo_stride, k_ptr, k_stride, hk, ko_ptr, ko_stride,
-        int(bool(inverse)), _raw_stream(stream, q)))
+        int(bool(inverse)), _raw_stream(stream, q))
+    if status:
+        raise MoeError("moe_rotary", status)
     return q_out, k_out
 
 
@@ -720,9 +722,11 @@ def moe_kv_write(cache, k, v, slots, stream=None):
     if v.shape[0] != T:
         raise ValueError("k and v must have as many tokens")
     _need_slots(slots, T, cache)
-    _check("moe_kv_write", load_library().moe_kv_write(
+    status = (_lib or load_library()).moe_kv_write(
         ctypes.byref(cache), slots.data_ptr(), T, k.data_ptr(), k_stride, v.data_ptr(),
-        v_stride, _raw_stream(stream, k)))
+        v_stride, _raw_stream(stream, k))
+    if status:
+        raise MoeError("moe_kv_write", status)
 
 
 def moe_rotary_kv_write(plan, positions, cache, q, k, v, slots, q_out=None, stream=None):
@@ -741,10 +745,12 @@ def moe_rotary_kv_write(plan, positions, cache, q, k, v, slots, q_out=None, stre
         qo_stride = _need_heads(q_out, hq, d, "q_out")
         if q_out.shape[0] != T:
             raise ValueError("q_out must have as many tokens as q")
-    _check("moe_rotary_kv_write", load_library().moe_rotary_kv_write(
+    status = (_lib or load_library()).moe_rotary_kv_write(
         ctypes.byref(plan), positions.data_ptr(), ctypes.byref(cache), slots.data_ptr(), T,
         q.data_ptr(), q_stride, hq, q_out.data_ptr(), qo_stride, k.data_ptr(), k_stride,
-        v.data_ptr(), v_stride, _raw_stream(stream, q)))
+        v.data_ptr(), v_stride, _raw_stream(stream, q))
+    if status:
+        raise MoeError("moe_rotary_kv_write", status)
     return q_out
 
 
@@ -764,9 +770,11 @@ def moe_kv_read(cache, block_table, offsets, rows, k_out=None, v_out=None, strea
             if tuple(t.shape) != shape:
                 raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
         outs.append(t)
-    _check("moe_kv_read", load_library().moe_kv_read(
+    status = (_lib or load_library()).moe_kv_read(
         ctypes.byref(cache), block_table.data_ptr(), stride, pages, offsets.data_ptr(), batch,
-        rows, outs[0].data_ptr(), outs[1].data_ptr(), _raw_stream(stream, offsets)))
+        rows, outs[0].data_ptr(), outs[1].data_ptr(), _raw_stream(stream, offsets))
+    if status:
+        raise MoeError("moe_kv_read", status)
     return tuple(outs)
 
 
@@ -776,10 +784,11 @@ def moe_paged_attention_workspace_size(cache, batch, q_heads):
 
 
 def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=None, lse=None,
-                        ws=None, stream=None):
+                        ws=None, stream=None, return_lse=False):
     """Attention of one new token per context: q [batch, q_heads, head_dim]
-    bf16 over the cached tokens; returns out, of q's shape. `lse`: optional
-    [batch, q_heads] fp32 tensor that receives the log of the sums."""
+    bf16 over the cached tokens; returns out, of q's shape, or (out, lse) with
+    return_lse. `lse`: optional [batch, q_heads] fp32 tensor that receives the
+    log of the sums."""
     batch, hq, d = q.shape
     q_stride = _need_heads(q, hq, cache.head_dim, "q")
     stride, pages = _need_table(block_table, batch)
@@ -796,12 +805,16 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
         _need(lse, torch.float32, "lse")
         if tuple(lse.shape) != (batch, hq):
             raise ValueError(f"lse must be {(batch, hq)}, got {tuple(lse.shape)}")
+    elif return_lse:
+        lse = _empty((batch, hq), torch.float32, q.device, stream)
     if ws is None:
         need = moe_paged_attention_workspace_size(cache, batch, hq)
         ws = _empty(max(need, 1), torch.uint8, q.device, stream)
-    _check("moe_paged_attention", load_library().moe_paged_attention(
+    status = (_lib or load_library()).moe_paged_attention(
         ctypes.byref(cache), q.data_ptr(), q_stride, batch, hq, block_table.data_ptr(), stride,
-        pages, lengths.data_ptr(), float(scale), int(window), out.data_ptr(),
+        pages, lengths.data_ptr(), scale, window, out.data_ptr(),
         None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, q)))
-    return out
+        _raw_stream(stream, q))
+    if status:
+        raise MoeError("moe_paged_attention", status)
+    return (out, lse) if return_lse else out
