@@ -131,16 +131,37 @@ struct Shape {
   static constexpr int kWarpBytes = kStages * kStageBytes + kScaleBytes;
   static constexpr int kJoinBytes = kRows * D * 4;         // an accumulator tile
   static constexpr int kSmemBytes = kWarps * kWarpBytes + 2 * kJoinBytes;
-  // Byte at which 16-byte piece `piece` of a tile lies in shared memory. Keys
-  // are read by 8 lanes at a time, 4 pieces of two neighbouring rows; values,
-  // 2 pieces (of 64-byte rows 2 halves each of 2) of 4 rows two apart.
-  static __device__ __forceinline__ int key_place(int piece) {
-    const int row = piece / (kRowBytes / 16);
-    return (piece ^ (kRowBytes == 64 ? 0 : (row & 1) << 2)) * 16;
+  // A tile's rows lie in shared memory as in the cache, except that within each
+  // 128-byte line the 16-byte pieces are permuted: the number of a key's piece is
+  // xored with 4 in odd rows (8 lanes read 4 pieces of two neighbouring rows), a
+  // value's with row & 6 (8 lanes read 2 pieces of 4 rows two apart), 64-byte
+  // keys excepted (two rows are a line). Written out as what depends on the lane,
+  // once a kernel, and what the compiler knows.
+  //
+  // Writing: lane's piece 32 j + lane of a group of rows goes to byte
+  // (lane part ^ step part) + 512 j.
+  static __device__ __forceinline__ int key_write(int lane) {
+    const int odd = kRowBytes == 128 ? (lane >> 3) & 1 : kRowBytes == 256 ? (lane >> 4) & 1 : 0;
+    return (lane ^ (odd << 2)) * 16;
   }
-  static __device__ __forceinline__ int value_place(int piece) {
-    const int row = piece / (kRowBytes / 16);
-    return (piece ^ (row & 6)) * 16;
+  static __device__ __forceinline__ constexpr int key_write_step(int j) { return kRowBytes == 512 ? (j & 1) * 64 : 0; }
+  static __device__ __forceinline__ int value_write(int lane) {
+    const int key = kRowBytes == 64 ? (lane >> 2) & 6 : kRowBytes == 128 ? (lane >> 3) & 2 : 0;
+    return (lane ^ key) * 16;
+  }
+  static __device__ __forceinline__ constexpr int value_write_step(int j) {   // 512 / kRowBytes rows a step
+    return (j * (512 / kRowBytes) & 6 & (kRowBytes == 64 ? 0 : kRowBytes == 128 ? 4 : 6)) * 16;
+  }
+  // Reading: pieces 4 p + t of key row 8 n + g, at byte (lane part ^ (p odd ? 64 : 0))
+  // + 128 (p / 2) + 8 n kRowBytes; the operands of value row 2 t + r, r = 0, 1, 8, 9, at
+  // lane part + r kRowBytes + 128 p (64-byte rows: (lane part ^ (r odd ? 64 : 0)) +
+  // (r & 8) kRowBytes).
+  static __device__ __forceinline__ int key_read(int g, int t) {
+    return ((g * (kRowBytes / 16) + t) ^ (kRowBytes == 64 ? 0 : (g & 1) << 2)) * 16;
+  }
+  static __device__ __forceinline__ int value_read(int g, int t) {
+    return kRowBytes == 64 ? ((8 * t + (g >> 1)) ^ (2 * t)) * 16 + (g & 1) * 8
+                           : 2 * t * kRowBytes + (g ^ (2 * t)) * 16;
   }
   static_assert(kCtas * (kSmemBytes + 1024 + 2048) <= 228 * 1024, "shared memory");
   static_assert(kCtas <= kMaxCtasPerSm, "workspace slots");
@@ -461,13 +482,12 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     k.here = __ballot_sync(0xffffffffu, paged && p.token >= p.begin) & kAll;
     return k;
   };
-  // Rows lie in shared memory as in the cache, with their 16-byte pieces
-  // permuted within 128-byte lines so that the lanes' reads meet no bank twice.
-  // Eight lanes copy a line: whole lines leave L2 at once. A group of 16
+  // Eight lanes copy a 128-byte line: whole lines leave L2 at once. A group of 16
   // tokens of a full tile is one run of memory when pages have at least 16;
   // otherwise every row's place comes from the lane that looked it up.
   const bool runs = a.c.page_shift >= 4;
-  auto copy_tile = [&](uint32_t to, const void* cache, const Tokens k, auto place) {
+  const int key_write = S::key_write(lane), value_write = S::value_write(lane);
+  auto copy_tile = [&](const void* cache, const Tokens k, auto place) {
     if (runs && k.here == kAll) {
 #pragma unroll
       for (int h = 0; h < S::kGroups; ++h) {
@@ -475,10 +495,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
             static_cast<const uint8_t*>(cache) +
             (uint64_t)__shfl_sync(0xffffffffu, k.row, kGroup * h) * S::kRowBytes + lane * 16;
 #pragma unroll
-        for (int j = 0; j < kGroup * S::kRowBytes / 512; ++j) {
-          const int piece = h * (kGroup * S::kRowBytes / 16) + 32 * j + lane;
-          cp_async_16(to + place(piece), src + 512 * j);
-        }
+        for (int j = 0; j < kGroup * S::kRowBytes / 512; ++j)
+          cp_async_16(place(j) + (h * (kGroup * S::kRowBytes / 512) + j) * 512, src + 512 * j);
       }
     } else {
 #pragma unroll
@@ -488,17 +506,17 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
             static_cast<const uint8_t*>(cache) +
             (uint64_t)__shfl_sync(0xffffffffu, k.row, row) * S::kRowBytes +
             piece % (S::kRowBytes / 16) * 16;
-        cp_async_16(to + place(piece), src, ((k.here >> row) & 1u) * 16u);
+        cp_async_16(place(j) + j * 512, src, ((k.here >> row) & 1u) * 16u);
       }
     }
   };
   auto copy_keys = [&](int stage, const Tokens k) {
-    copy_tile(stage_u32 + stage * S::kStageBytes, a.c.k, k,
-              [](int piece) { return S::key_place(piece); });
+    const uint32_t to = stage_u32 + stage * S::kStageBytes;
+    copy_tile(a.c.k, k, [&](int j) { return to + (key_write ^ S::key_write_step(j)); });
   };
   auto copy_values = [&](int stage, const Tokens k) {
-    copy_tile(stage_u32 + stage * S::kStageBytes + S::kKeyBytes, a.c.v, k,
-              [](int piece) { return S::value_place(piece); });
+    const uint32_t to = stage_u32 + S::kKeyBytes + stage * S::kStageBytes;
+    copy_tile(a.c.v, k, [&](int j) { return to + (value_write ^ S::value_write_step(j)); });
   };
   // What the tokens of a tile bring to the scores: (scale of the key, log2 of
   // the value's scale a) and 1 / a, a token a lane. They are asked for with the
@@ -583,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     step();
   }
   Segment seg;
+  const int key_read = S::key_read(g, t), value_read = S::value_read(g, t);
   int stage = 0, n = 0;   // of the next tile: its stage, and its number (for put_scales)
   bool running = next_segment(0, seg);
   if (running) ask_q(seg);
@@ -638,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const uint4 w = *reinterpret_cast<const uint4*>(
-                tile + S::key_place((8 * (2 * h + n) + g) * (S::kRowBytes / 16) + 4 * p + t));
+                tile + (key_read ^ ((p & 1) * 64)) + 128 * (p >> 1) +
+                8 * (2 * h + n) * S::kRowBytes);
             if (E4M3) {
               const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -753,11 +773,11 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
           uint32_t w[4][S::kPieceBytes / 4];
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            const int row = kGroup * h + 8 * (n >> 1) + 2 * t + (n & 1);
+            const int r = 8 * (n >> 1) + (n & 1);
             const uint8_t* const piece =
-                values + (S::kPieceBytes == 16
-                              ? S::value_place(row * (S::kRowBytes / 16) + 8 * p + g)
-                              : S::value_place(row * (S::kRowBytes / 16) + (g >> 1)) + (g & 1) * 8);
+                S::kRowBytes == 64
+                    ? values + (value_read ^ ((n & 1) * 64)) + (kGroup * h + (r & 8)) * S::kRowBytes
+                    : values + value_read + (kGroup * h + r) * S::kRowBytes + 128 * p;
             if (S::kPieceBytes == 16) {
               const uint4 raw = *reinterpret_cast<const uint4*>(piece);
               w[n][0] = raw.x;
