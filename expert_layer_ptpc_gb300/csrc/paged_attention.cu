@@ -5,13 +5,14 @@
 //
 // One pass over the cached tokens. In base 2, with x_j = s_j log2(e) and an
 // e4m3 value row v_j = a_j c_j (a_j its scale, c_j its codes), a warp keeps
-//   M (a bound of max_j x_j + log2 a_j),  w_j = 2^(x_j + log2 a_j - M),
+//   M (near max_j x_j + log2 a_j),  w_j = 2^(x_j + log2 a_j - M),
 //   acc = sum_j w_j c_j,   l = sum_j w_j / a_j,
 // so that out = acc / l and lse = (M + log2 l) ln 2. The scale of a value row
 // goes into its weight's exponent: the weights stay in fp16's range whatever
-// the scales, and the codes go to the tensor cores unscaled. M moves only when
-// a tile's maximum passes it by 2^8 (fp16 weights reach 2^16), so that the
-// accumulators are rarely rescaled. Sums and accumulators are fp32.
+// the scales, and the codes go to the tensor cores unscaled. M is set 7 below a
+// tile's maximum, and moves only when a later one passes it by 15 (fp16 ends at
+// 2^16), so that the accumulators are rarely rescaled; weights that are rounded to
+// zero are 2^-32 of the largest and less. Sums and accumulators are fp32.
 //
 // The work is bound by the cache's bytes: 4 D flops a token and query head
 // against 2 D + 8 bytes a token and kv head, 31 flop/byte with 16 query heads a
@@ -57,7 +58,8 @@ constexpr int kGroup = 16;                 // tokens of one tensor core contract
 constexpr int kRows = 16;                  // query heads of a work item
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxWorkers = kSms * kMaxCtasPerSm;
-constexpr float kSlack = 8.0f;             // log2 by which a weight may pass 1
+constexpr float kMostWeight = 15.0f;       // log2 of the largest weight let stand,
+constexpr float kNewWeight = 7.0f;         // and of a tile's largest when M is set by it
 // What an item of a context costs beside its units, in units: fetching q, and
 // joining the warps. The work is cut with this included, or the workers that
 // get many short contexts would be the last to finish.
@@ -720,13 +722,14 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
         for (int n = 1; n < 2 * S::kGroups; ++n)
           high[r] = fmaxf(high[r], fmaxf(x[n][2 * r], x[n][2 * r + 1]));
       }
-      const bool moves = high[0] > top[0] + kSlack || high[1] > top[1] + kSlack;
+      const bool moves =
+          high[0] > top[0] + kMostWeight || high[1] > top[1] + kMostWeight;
       if (__any_sync(0xffffffffu, moves)) {
         float f[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float was = top[r];
-          top[r] = fmaxf(was, quad_max(high[r]));
+          top[r] = fmaxf(was, quad_max(high[r]) - kNewWeight);
           f[r] = weight(was, top[r]);
           sum[r] *= f[r];
         }

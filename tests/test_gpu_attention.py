@@ -539,3 +539,35 @@ def test_attention_whole_contexts_and_cut_ones_agree():
     check_attention(cache, q, wide, lengths)
     check_attention(cache, q, wide, lengths, window=100)
     check_attention(cache, q, table, lengths, window=100)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+@pytest.mark.parametrize("gap", [12.0, 18.0, 21.0])
+def test_attention_sink_and_a_long_faint_tail(kind, gap):
+    """One token of great weight and very many of e^-gap of it, whose values agree in
+    elements where the first's are zero: what the tail adds there must not be
+    rounded away. Weights are exact powers apart, so the bound is the weights'
+    and the sums' rounding; a weight of e^-21 = 2^-30.3 of the largest keeps at
+    least 2 bits of fp16's subnormals (2^-32 of it is half a step)."""
+    n, d, size = 20000, 128, 64
+    pages = -(-n // size)
+    cache = fresh_cache(pages, 1, size, d, kind)
+    k = torch.zeros((n, 1, d), device="cuda")
+    v = torch.zeros((n, 1, d), device="cuda")
+    k[7, 0, 0] = 1.0                       # the sink
+    v[7, 0, :64] = 1.0
+    v[:7, 0, 64:] = 1.0
+    v[8:, 0, 64:] = 1.0
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    cache.write(k.to(torch.bfloat16), v.to(torch.bfloat16), slots)
+    q = torch.zeros((1, 16, d), device="cuda")
+    q[..., 0] = gap
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = cache.attend(q.to(torch.bfloat16), table, lengths, scale=1.0)
+    tail = (n - 1) * np.exp(-gap)
+    want = np.concatenate([np.full(64, 1 / (1 + tail)), np.full(64, tail / (1 + tail))])
+    got = values(out)[0]
+    # half a step of a weight: 2^-11 of it, or 2^-32 of the largest
+    rel = HALF_BF16 + max(2.0 ** -11, 2.0 ** -32 * np.exp(gap)) + 4 * n * U32
+    assert np.all(np.abs(got - want) <= rel * want), (got[0, [0, 64]], want[[0, 64]])
