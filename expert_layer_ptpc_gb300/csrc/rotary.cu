@@ -17,8 +17,10 @@
 // for 128 elements, and every lane keeps the 8 that its elements need in
 // registers over all the heads. A lane's unit of a head is two runs of 8 elements,
 // half a region apart, so that the lanes' 16-byte accesses are contiguous; the
-// next units are loaded before one is used. A cache head is 4, 8 or 16 units,
+// next units are in flight while one is used. A cache head is 4, 8 or 16 units,
 // hence that many neighbouring lanes, and its row maximum is a shuffle.
+// GB300, 8192 tokens of 64 + 4 heads of 128: the rotation 44 us (6.5 TB/s of the copy's
+// 6.8), with k and v quantised into the cache 46 us (6.3 TB/s).
 #include <algorithm>
 
 #include "attention.h"
@@ -31,12 +33,17 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kUnit = 16;     // elements of a lane
-// Blocks of an SM, and the units that a lane loads before it uses the first: 32
-// warps an SM, whose 64 registers a lane hold two units ahead, or one next to the
-// cosines and the quantiser. (GB300, 8192 tokens of 64 + 4 heads of 128: the
-// rotation takes 45.9 us with 2 ahead, 47.9 with 1, 46.7 with 4 and 24 warps; with
-// the cache's write 51.8 with 1, 56.8 with 2, 53.7 with 2 and 24 warps.)
+// Blocks of an SM: 32 warps of 64 registers a lane. A lane's units travel through
+// shared memory (cp.async, each lane reads back its own), so that more of them are
+// in flight than registers would hold. (GB300, 8192 tokens of 64 + 4 heads of 128, the
+// rotation and the fused write: 44.1 and 46.5 us with three units in flight; in
+// registers, two and one, 45.9 and 51.8, and more of them spill.)
 constexpr int kBlocks = 4;
+constexpr int kAhead = 3;     // units of a lane in flight
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 __device__ __forceinline__ void unpack8(const uint4& raw, float* v) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -89,8 +96,10 @@ template <int SINK, int PAIRS>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks)
     rotary_kernel(const RotaryArgs a, int parts, int per_warp) {
   constexpr bool NEIGHBOURS = PAIRS == kNeighbours;
-  constexpr int kAhead = SINK == kSinkTensors || PAIRS == kNoPairs ? 2 : 1;
-  extern __shared__ float2 turns[];   // (cos, sin) of the warp's token, [kWarps][rot / 2]
+  // the warps' units in flight, and the (cos, sin) of their tokens' pairs
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* const flight = smem + (threadIdx.x >> 5) * (kAhead * 1024);
+  float2* const turns = reinterpret_cast<float2*>(smem + kWarps * kAhead * 1024);
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -122,17 +131,21 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks)
     if (head < k_end) return a.k + t * a.k_stride + (head - q_end) * a.head_dim;
     return a.v + t * a.v_stride + (head - k_end) * a.head_dim;
   };
-  uint4 raw[kAhead][2];
-  auto load = [&](int head, uint4 (&r)[2]) {
-    r[0] = r[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (head >= end) return;
-    const uint16_t* src = source(head);
-    const bool is_v = SINK != kSinkTensors && head >= k_end;
-    r[0] = *reinterpret_cast<const uint4*>(src + (is_v ? v_run0 : run0));
-    r[1] = *reinterpret_cast<const uint4*>(src + (is_v ? v_run1 : run1));
+  // A unit goes to shared memory and back to the lane that asked for it: 32
+  // bytes a lane, in flight without registers.
+  auto load = [&](int step) {
+    const int head = mine + step * at_once;
+    const uint32_t to = smem_u32(flight) + (step % kAhead) * 1024 + lane * 16;
+    if (head < end) {
+      const uint16_t* src = source(head);
+      const bool is_v = SINK != kSinkTensors && head >= k_end;
+      cp_async_16(to, src + (is_v ? v_run0 : run0));
+      cp_async_16(to + 512, src + (is_v ? v_run1 : run1));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(mine + i * at_once, raw[i]);
+  for (int i = 0; i < kAhead; ++i) load(i);
 
   // cosines of the token's pairs
   float2 cs[8];
@@ -157,60 +170,60 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks)
 
   const int64_t row0 = ((int64_t)(slot >> a.page_shift) * a.k_heads << a.page_shift) +
                        (slot & ((1 << a.page_shift) - 1));   // of kv head 0
-  for (int head0 = mine; head0 - mine + begin < end; head0 += kAhead * at_once) {
+  const int steps = (end - begin + at_once - 1) / at_once;
+  for (int step = 0; step < steps; ++step) {
+    const int head = mine + step * at_once;
+    const bool is_v = SINK != kSinkTensors && head >= k_end;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    float x[kUnit];
+    const uint8_t* const unit = flight + (step % kAhead) * 1024 + lane * 16;
+    unpack8(*reinterpret_cast<const uint4*>(unit), x);
+    unpack8(*reinterpret_cast<const uint4*>(unit + 512), x + 8);
+    load(step + kAhead);
+    if (PAIRS != kNoPairs && rotates && !is_v) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int head = head0 + i * at_once;
-      const bool is_v = SINK != kSinkTensors && head >= k_end;
-      float x[kUnit];
-      unpack8(raw[i][0], x);
-      unpack8(raw[i][1], x + 8);
-      load(head + kAhead * at_once, raw[i]);
-      if (PAIRS != kNoPairs && rotates && !is_v) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float& x1 = NEIGHBOURS ? x[2 * j] : x[j];
-          float& x2 = NEIGHBOURS ? x[2 * j + 1] : x[8 + j];
-          const float y1 = fmaf(x1, cs[j].x, -(x2 * cs[j].y));
-          x2 = fmaf(x2, cs[j].x, x1 * cs[j].y);
-          x1 = y1;
-        }
+      for (int j = 0; j < 8; ++j) {
+        float& x1 = NEIGHBOURS ? x[2 * j] : x[j];
+        float& x2 = NEIGHBOURS ? x[2 * j + 1] : x[8 + j];
+        const float y1 = fmaf(x1, cs[j].x, -(x2 * cs[j].y));
+        x2 = fmaf(x2, cs[j].x, x1 * cs[j].y);
+        x1 = y1;
       }
-      const int o0 = is_v ? v_run0 : run0, o1 = is_v ? v_run1 : run1;
-      uint16_t* dst = nullptr;
-      if (PAIRS != kNoPairs && head < end) {
-        if (head < q_end) dst = a.q_out + t * a.q_out_stride + head * a.head_dim;
-        else if (SINK == kSinkTensors)
-          dst = a.k_out + t * a.k_out_stride + (head - q_end) * a.head_dim;
-      }
-      if (dst != nullptr) {
-        *reinterpret_cast<uint4*>(dst + o0) = pack8(x);
-        *reinterpret_cast<uint4*>(dst + o1) = pack8(x + 8);
-      }
-      // (the warp's heads of this step, all q's: nothing for the cache)
-      if (SINK == kSinkTensors || head0 - mine + begin + (i + 1) * at_once <= q_end) continue;
+    }
+    const int o0 = is_v ? v_run0 : run0, o1 = is_v ? v_run1 : run1;
+    uint16_t* dst = nullptr;
+    if (PAIRS != kNoPairs && head < end) {
+      if (head < q_end) dst = a.q_out + t * a.q_out_stride + head * a.head_dim;
+      else if (SINK == kSinkTensors)
+        dst = a.k_out + t * a.k_out_stride + (head - q_end) * a.head_dim;
+    }
+    if (dst != nullptr) {
+      *reinterpret_cast<uint4*>(dst + o0) = pack8(x);
+      *reinterpret_cast<uint4*>(dst + o1) = pack8(x + 8);
+    }
+    // (the warp's heads of this step, all q's: nothing for the cache)
+    if (SINK == kSinkTensors || begin + (step + 1) * at_once <= q_end) continue;
 
-      float amax = 0.f;
-      if (SINK == kSinkE4m3) {
+    float amax = 0.f;
+    if (SINK == kSinkE4m3) {
 #pragma unroll
-        for (int j = 0; j < kUnit; ++j) amax = fmaxf(amax, fabsf(x[j]));
-        for (int o = units >> 1; o > 0; o >>= 1)
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      }
-      if (head < q_end || head >= end || !kept) continue;
-      const int kv_head = is_v ? head - k_end : head - q_end;
-      const int64_t row = row0 + ((int64_t)kv_head << a.page_shift);
-      if (SINK == kSinkE4m3) {
-        const float s = __fdiv_rn(fmaxf(amax, 1e-12f), 448.0f), y = __frcp_rn(s);
-        uint8_t* out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
-        *reinterpret_cast<uint2*>(out + o0) = codes8(x, s, y);
-        *reinterpret_cast<uint2*>(out + o1) = codes8(x + 8, s, y);
-        if (u == 0) (is_v ? a.v_scale : a.k_scale)[row] = s;
-      } else {
-        uint16_t* out = static_cast<uint16_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
-        *reinterpret_cast<uint4*>(out + o0) = pack8(x);
-        *reinterpret_cast<uint4*>(out + o1) = pack8(x + 8);
-      }
+      for (int j = 0; j < kUnit; ++j) amax = fmaxf(amax, fabsf(x[j]));
+      for (int o = units >> 1; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    if (head < q_end || head >= end || !kept) continue;
+    const int kv_head = is_v ? head - k_end : head - q_end;
+    const int64_t row = row0 + ((int64_t)kv_head << a.page_shift);
+    if (SINK == kSinkE4m3) {
+      const float s = __fdiv_rn(fmaxf(amax, 1e-12f), 448.0f), y = __frcp_rn(s);
+      uint8_t* out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
+      *reinterpret_cast<uint2*>(out + o0) = codes8(x, s, y);
+      *reinterpret_cast<uint2*>(out + o1) = codes8(x + 8, s, y);
+      if (u == 0) (is_v ? a.v_scale : a.k_scale)[row] = s;
+    } else {
+      uint16_t* out = static_cast<uint16_t*>(is_v ? a.cache_v : a.cache_k) + row * a.head_dim;
+      *reinterpret_cast<uint4*>(out + o0) = pack8(x);
+      *reinterpret_cast<uint4*>(out + o1) = pack8(x + 8);
     }
   }
 }
@@ -221,11 +234,16 @@ int launch_rotary(const RotaryArgs& a, int sink, bool neighbours, cudaStream_t s
   const int heads = a.q_heads + (sink == kSinkTensors ? a.k_heads : 2 * a.k_heads);
   const int at_once = 32 / (a.head_dim / kUnit);
   const int steps = (heads + at_once - 1) / at_once;   // of a warp that has all heads
-  // Heads of a token go to one warp when the tokens fill the GPU (152 SMs with
-  // 24 warps each); with fewer tokens they are spread, down to one step a warp.
-  const int64_t full = 152 * 24;
-  const int64_t want = std::max<int64_t>(1, (int64_t)a.T * steps / full);
-  const int take = (int)std::min<int64_t>(steps, want);
+  // Steps of a warp: so many that the work fills the GPU three times over (152 SMs
+  // with 32 warps each; the rotation above takes 44.1 us, 45.8 with all 17 steps of a
+  // token in one warp, the last warps being few); but up to 8, as long as it is
+  // filled once (4099 tokens of 18 heads of 256 take 14.1 us in steps of 5 and 4, 16.6
+  // in steps of 2: each warp works out the cosines anew); at least one.
+  const int64_t fill = 152 * 32, work = (int64_t)a.T * steps;
+  const int most = (int)std::min<int64_t>(
+      steps, std::max<int64_t>({1, work / (3 * fill), std::min<int64_t>(8, work / fill)}));
+  const int even = (steps + most - 1) / most;          // warps of a token
+  const int take = (steps + even - 1) / even;
   const int per_warp = take * at_once;
   const int parts = (heads + per_warp - 1) / per_warp;
   const int64_t blocks = ((int64_t)parts * a.T + kWarps - 1) / kWarps;
@@ -241,7 +259,7 @@ int launch_rotary(const RotaryArgs& a, int sink, bool neighbours, cudaStream_t s
     kernel = neighbours ? rotary_kernel<kSinkE4m3, kNeighbours> : rotary_kernel<kSinkE4m3, kHalves>;
   else
     kernel = neighbours ? rotary_kernel<kSinkBf16, kNeighbours> : rotary_kernel<kSinkBf16, kHalves>;
-  const size_t smem = (size_t)kWarps * (a.rot / 2) * sizeof(float2);
+  const size_t smem = (size_t)kWarps * (kAhead * 1024 + (a.rot / 2) * sizeof(float2));
   const cudaError_t e = launch_kernel(true, dim3((unsigned)blocks), dim3(kWarps * 32), smem,
                                       stream, kernel, a, parts, per_warp);
   return e == cudaSuccess ? 0 : -3;
