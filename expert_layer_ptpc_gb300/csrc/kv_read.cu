@@ -5,7 +5,8 @@
 // and written once (2 bytes). A block takes 16 rows: 16 lanes look their cache rows
 // up (context, then page), then all threads stream the rows' runs of 8 elements,
 // 8-byte loads of codes against 16-byte stores, both contiguous over the lanes, with
-// 8 loads in flight a thread.
+// 8 loads in flight a thread. GB300, two contexts of 60001 tokens, 4 heads of 128 (372
+// MB): 58 us, 6.45 TB/s of the copy's 6.8.
 #include "attention.h"
 #include "common.cuh"
 #include "internal.h"

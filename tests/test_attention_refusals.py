@@ -141,6 +141,8 @@ def test_read_refusals(lib, kw, want):
     (dict(stride=3), INVALID), (dict(pages=-1, stride=0), INVALID), (dict(lengths=None), INVALID),
     (dict(out=None), INVALID), (dict(out=MIS), INVALID), (dict(lse=A + 2), INVALID),
     (dict(ws=None), WORKSPACE), (dict(ws=MIS), WORKSPACE), (dict(ws_bytes=16), WORKSPACE),
+    # 2 x 65535 items of 2^24 tokens: more units than the cut can number
+    (dict(batch=65535, stride=1 << 20, pages=1 << 20), UNSUPPORTED),
 ])
 def test_attention_refusals(lib, kw, want):
     f = dict(q=A, qs=1024, batch=2, hq=8, table=A, stride=4, pages=4, lengths=A, scale=0.1,

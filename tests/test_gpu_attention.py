@@ -571,3 +571,28 @@ def test_attention_sink_and_a_long_faint_tail(kind, gap):
     # half a step of a weight: 2^-11 of it, or 2^-32 of the largest
     rel = HALF_BF16 + max(2.0 ** -11, 2.0 ** -32 * np.exp(gap)) + 4 * n * U32
     assert np.all(np.abs(got - want) <= rel * want), (got[0, [0, 64]], want[[0, 64]])
+
+
+def test_attention_a_bad_context_does_not_reach_others():
+    """NaN in the keys, values or scales of some contexts stays in their rows."""
+    for kind in ("e4m3", "bf16"):
+        lengths = [40 + b % 30 for b in range(700)]
+        cache, q, table = attention_case(59, lengths, 4, 1, 128, 16, kind)
+        wide = np.full((700, 100), -1, np.int32)       # cut and joined, not one CTA an item
+        wide[:, :table.shape[1]] = table
+        t = torch.from_numpy(wide).cuda()
+        n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        want = cache.attend(q, t, n, return_lse=True)
+        bad = range(0, 700, 7)
+        for i, b in enumerate(bad):
+            page, at = int(table[b, (lengths[b] - 1) // 16]), (lengths[b] - 1) % 16
+            if kind == "bf16":
+                (cache.k if i % 2 else cache.v)[page, 0, at, 5] = float("nan")
+            elif i % 3 == 0:
+                (cache.k if i % 2 else cache.v)[page, 0, at, 5] = 0x7F
+            else:
+                (cache.k_scale if i % 2 else cache.v_scale)[page, 0, at] = float("nan")
+        got = cache.attend(q, t, n, return_lse=True)
+        good = torch.tensor([b not in set(bad) for b in range(700)], device="cuda")
+        assert torch.equal(got[0][good], want[0][good])
+        assert torch.equal(got[1][good], want[1][good])
