@@ -39,7 +39,7 @@
 // bf16 numbers (16 bits).
 //
 // GB300: 128 contexts of 0 to 16384 tokens, 64 query heads on 4 of 128, e4m3 (1.11 GB):
-// 184 us, 6.0 TB/s of the copy's 6.8; one context of 262143 tokens (277 MB): 54 us, of
+// 182 us, 6.1 TB/s of the copy's 6.8; one context of 262143 tokens (277 MB): 54 us, of
 // which 40 are the tiles at the copy's rate and the rest the first loads, the last CTA
 // and the joining kernel. 8 warps an SM of up to 255 registers; the tensor cores are 30%
 // busy, and the issue slots 41%.
@@ -138,7 +138,12 @@ struct Shape {
   static constexpr int kStageBytes = 2 * kKeyBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes + kScaleBytes;
   static constexpr int kJoinBytes = kRows * D * 4;         // an accumulator tile
-  static constexpr int kSmemBytes = kWarps * kWarpBytes + 2 * kJoinBytes;
+  // q's operands: 64 registers with 256 elements, next to 128 of accumulators. There
+  // they are in shared memory, and fetched when a segment begins instead of before (64
+  // contexts of 8000 tokens, 16 heads on 2: 101 us, 137 with them in registers).
+  static constexpr bool kSharedQ = E4M3 && D == 256;
+  static constexpr int kQBytes = kSharedQ ? D / 16 * 512 : 0;
+  static constexpr int kSmemBytes = kWarps * kWarpBytes + 2 * kJoinBytes + kQBytes;
   // A tile's rows lie in shared memory as in the cache, except that within each
   // 128-byte line the 16-byte pieces are permuted: the number of a key's piece is
   // xored with 4 in odd rows (8 lanes read 4 pieces of two neighbouring rows), a
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   const int key_read = S::key_read(g, t), value_read = S::value_read(g, t);
   int stage = 0, n = 0;   // of the next tile: its stage, and its number (for put_scales)
   bool running = next_segment(0, seg);
-  if (running) ask_q(seg);
+  if (running && !S::kSharedQ) ask_q(seg);
   {
     float ks[S::kStages], vs[S::kStages];
 #pragma unroll
@@ -633,8 +638,18 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       if (i + 1 < S::kStages) put_scales(i);
     }
   }
+  uint4* const shared_q =
+      reinterpret_cast<uint4*>(smem + kWarps * S::kWarpBytes + 2 * S::kJoinBytes) + lane;
   while (running) {
+    if (S::kSharedQ) ask_q(seg);
     convert_q();
+    if (S::kSharedQ) {   // (all warps have left the last segment's tiles)
+#pragma unroll
+      for (int step = 0; step < D / 16; ++step)
+        if (step % kWarps == warp)
+          shared_q[32 * step] = make_uint4(qf[step][0], qf[step][1], qf[step][2], qf[step][3]);
+      __syncthreads();
+    }
     const int tiles = tiles_of(seg);
 
     float acc[D / 8][4];
@@ -660,25 +675,41 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[2 * h + n][j] = 0.f;
 #pragma unroll
-        for (int p = 0; p < S::kKeyPieces; ++p)
+        for (int p = 0; p < S::kKeyPieces; ++p) {
+          uint4 w[2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint4 w = *reinterpret_cast<const uint4*>(
+          for (int n = 0; n < 2; ++n)
+            w[n] = *reinterpret_cast<const uint4*>(
                 tile + (key_read ^ ((p & 1) * 64)) + 128 * (p >> 1) +
                 8 * (2 * h + n) * S::kRowBytes);
-            if (E4M3) {
-              const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+          if (E4M3) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16(v[j], b0, b1);
-                mma16816<true>(x[2 * h + n], qf[4 * p + j], b0, b1);
+            for (int j = 0; j < 4; ++j) {
+              uint32_t aq[4] = {qf[4 * p + j][0], qf[4 * p + j][1], qf[4 * p + j][2],
+                                qf[4 * p + j][3]};
+              if (S::kSharedQ) {
+                const uint4 v = shared_q[32 * (4 * p + j)];
+                aq[0] = v.x;
+                aq[1] = v.y;
+                aq[2] = v.z;
+                aq[3] = v.w;
               }
-            } else {
-              mma16816<false>(x[2 * h + n], qf[2 * p], w.x, w.y);
-              mma16816<false>(x[2 * h + n], qf[2 * p + 1], w.z, w.w);
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16(j == 0 ? w[n].x : j == 1 ? w[n].y : j == 2 ? w[n].z : w[n].w, b0,
+                              b1);
+                mma16816<true>(x[2 * h + n], aq, b0, b1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              mma16816<false>(x[2 * h + n], qf[2 * p], w[n].x, w[n].y);
+              mma16816<false>(x[2 * h + n], qf[2 * p + 1], w[n].z, w[n].w);
             }
           }
+        }
         // base 2, with the value rows' scales in the exponent
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -834,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     // ---- join the warps ----
     const Segment done = seg;
     running = next_segment(0, seg);
-    if (running) ask_q(seg);
+    if (running && !S::kSharedQ) ask_q(seg);
 #pragma unroll
     for (int r = 0; r < 2; ++r) sum[r] = quad_sum(sum[r]);
     auto put_acc = [&](int to) {
