@@ -715,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
         for (int n = 0; n < 2; ++n) {
           float (&y)[4] = x[2 * h + n];
           if (E4M3) {
-            const float4 sc = *reinterpret_cast<const float4*>(side + 2 * (8 * (2 * h + n) + 2 * t));
+            const float4 sc =
+                *reinterpret_cast<const float4*>(side + 2 * (8 * (2 * h + n) + 2 * t));
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               y[2 * r] = fmaf(y[2 * r] * sc.x, row_scale[r], sc.y);
@@ -1087,8 +1088,8 @@ int launch(const Args& a, cudaStream_t stream) {
   }
   Args args = a;
   args.whole = room <= kWholeUnits * S::kUnit && items <= kSms * S::kCtas;
-  const int grid = args.whole ? (int)items
-                              : (int)std::min<int64_t>(kSms * S::kCtas, items * (units + kItemCost));
+  const int grid = (int)std::min<int64_t>(kSms * S::kCtas,
+                                          args.whole ? items : items * (units + kItemCost));
   args.joint_count = (int)std::min<int64_t>(items, grid);
   args.by_worker = args.joint_count < items;
   cudaError_t e = launch_kernel(true, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
