@@ -23,8 +23,10 @@
 //   context that ends up on several CTAs leaves partial results, which a
 //   second kernel joins.
 // * the up to 16 query heads of a kv head are the rows of one m16n8k16 tensor
-//   core tile. More heads a kv head are further work items, which find the
-//   tokens in L2.
+//   core tile; in larger calls up to 32 of 64 or 128 elements are two tiles, for
+//   which a token is copied and converted once (64 contexts of 8000 tokens, 80 heads on
+//   4, 128 elements: e4m3 126 us, bf16 177; as two work items 180 and 319). More heads
+//   a kv head are further work items, which find the tokens in L2.
 // * each warp has tiles of 16 or 32 tokens of its own in flight (cp.async),
 //   kStages deep, with barriers of the warp only.
 // * the order of the head's elements in the contraction is free (q is laid out
@@ -61,7 +63,7 @@ constexpr int kSms = 152;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                 // tokens of one tensor core contraction
-constexpr int kRows = 16;                  // query heads of a work item
+constexpr int kMmaRows = 16;               // query heads of a tensor core tile
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxWorkers = kSms * kMaxCtasPerSm;
 constexpr float kMostWeight = 15.0f;       // log2 of the largest weight let stand,
@@ -90,7 +92,8 @@ struct Args {
   const uint16_t* q;
   int64_t q_stride;
   int batch, q_heads, group;   // group: query heads of a kv head
-  int chunks;                  // items of at most kRows heads a group is cut into
+  int chunks;                  // items that a group is cut into
+  int rows;                    // query heads of an item, at most
   const int32_t* lengths;
   float scale;
   int window;
@@ -100,8 +103,8 @@ struct Args {
   Joint* joints;               // [joint_count]: by item, or by the item's first worker
   int joint_count;             // the fewer of the two
   int by_worker;
-  float2* stats;               // [slots][kRows] (M, l)
-  float* parts;                // [slots][kRows][D]
+  float2* stats;               // [slots][rows] (M, l)
+  float* parts;                // [slots][rows][D]
 };
 
 // First and last tokens that take part, and the units (of `unit` tokens) they
@@ -120,8 +123,10 @@ __device__ __forceinline__ Span span_of(const Args& a, int length, int unit) {
   return s;
 }
 
-template <bool E4M3, int D>
+// M: tensor core tiles of query heads an item has.
+template <bool E4M3, int D, int M>
 struct Shape {
+  static constexpr int kRows = M * kMmaRows;                // query heads of an item
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kTile = kRowBytes <= 128 ? 32 : 16;  // tokens a warp takes at a time
   static constexpr int kUnit = kWarps * kTile;              // tokens of a work unit
@@ -131,18 +136,19 @@ struct Shape {
   static constexpr int kPieceBytes = kChunk * (E4M3 ? 1 : 2);
   static constexpr int kValuePieces = D / 8 / kChunk;      // pieces a lane holds of a value
   static constexpr int kKeyBytes = kTile * kRowBytes;      // of a stage, and as much of values
-  static constexpr int kCtas = kRowBytes == 64 ? 3 : kRowBytes == 512 ? 1 : 2;
+  static constexpr int kCtas = kRowBytes == 64 && M == 1 ? 3 : kRowBytes == 512 ? 1 : 2;
   static constexpr int kStages = kRowBytes == 64 || kRowBytes == 512 ? 3 : 2;
   static constexpr int kSides = 4;                         // at least kStages + 1
   static constexpr int kScaleBytes = E4M3 ? kSides * kTile * 12 : 0;
   static constexpr int kStageBytes = 2 * kKeyBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes + kScaleBytes;
   static constexpr int kJoinBytes = kRows * D * 4;         // an accumulator tile
-  // q's operands: 64 registers with 256 elements, next to 128 of accumulators. There
-  // they are in shared memory, and fetched when a segment begins instead of before (64
-  // contexts of 8000 tokens, 16 heads on 2: 101 us, 137 with them in registers).
-  static constexpr bool kSharedQ = E4M3 && D == 256;
-  static constexpr int kQBytes = kSharedQ ? D / 16 * 512 : 0;
+  // q's operands: 64 registers with 256 elements or two tiles of 128, next to 128 of
+  // accumulators. There they are in shared memory, and fetched when a segment begins
+  // instead of before (64 contexts of 8000 tokens, 16 heads on 2 of 256 elements: 101 us,
+  // 137 with them in registers; two tiles of 64: 82 us, 87).
+  static constexpr bool kSharedQ = M == 2 || (E4M3 && D == 256);
+  static constexpr int kQBytes = kSharedQ ? M * (D / 16) * 512 : 0;
   static constexpr int kSmemBytes = kWarps * kWarpBytes + 2 * kJoinBytes + kQBytes;
   // A tile's rows lie in shared memory as in the cache, except that within each
   // 128-byte line the 16-byte pieces are permuted: the number of a key's piece is
@@ -326,18 +332,19 @@ struct Walker {
 // out and lse of an item of a context without tokens.
 __device__ __forceinline__ void zero_rows(const Args& a, int b, int item, int head_dim) {
   const int kv = item / a.chunks;
-  const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;
-  const int rows = min(kRows, (kv + 1) * a.group - head0);
+  const int head0 = kv * a.group + (item - kv * a.chunks) * a.rows;
+  const int rows = min(a.rows, (kv + 1) * a.group - head0);
   const int64_t at = (int64_t)b * a.q_heads + head0;
   for (int i = threadIdx.x; i < rows * (head_dim / 8); i += kThreads)
     reinterpret_cast<uint4*>(a.out + at * head_dim)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (a.lse != nullptr && threadIdx.x < rows) a.lse[at + threadIdx.x] = -INFINITY;
 }
 
-template <bool E4M3, int D>
-__global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
+template <bool E4M3, int D, int M>
+__global__ void __launch_bounds__(kThreads, Shape<E4M3, D, M>::kCtas)
     paged_attention_kernel(const Args a) {
-  using S = Shape<E4M3, D>;
+  using S = Shape<E4M3, D, M>;
+  constexpr int kRows = S::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 stats[2][kRows];
   __shared__ int lengths[kLengths];
@@ -551,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
   };
 
   // ---- q, in the order in which the lanes hold the keys ----
-  uint32_t qf[D / 16][4];
-  float row_scale[2];
+  uint32_t qf[M][D / 16][4];
+  float row_scale[2 * M];   // of rows g + 8 r
   auto heads_of = [&](const Segment& s, int& head0, int& rows) {
     head0 = s.kv * a.group + s.chunk * kRows;
     rows = min(kRows, (s.kv + 1) * a.group - head0);
@@ -566,26 +573,27 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       const int d = E4M3 ? 64 * (step >> 2) + 16 * t + 4 * (step & 3)
                          : 32 * (step >> 1) + 8 * t + 4 * (step & 1);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < 2 * M; ++r) {
         uint2 w = make_uint2(0u, 0u);
         if (g + 8 * r < rows) w = *reinterpret_cast<const uint2*>(q0 + (g + 8 * r) * D + d);
-        qf[step][r] = w.x;
-        qf[step][2 + r] = w.y;
+        qf[r >> 1][step][r & 1] = w.x;
+        qf[r >> 1][step][2 + (r & 1)] = w.y;
       }
     }
   };
   auto convert_q = [&]() {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) row_scale[r] = a.scale * 1.4426950408889634f;
+    for (int r = 0; r < 2 * M; ++r) row_scale[r] = a.scale * 1.4426950408889634f;
     if (E4M3) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < 2 * M; ++r) {
         float top = 0.f;
 #pragma unroll
         for (int step = 0; step < D / 16; ++step)
 #pragma unroll
-          for (int i = r; i < 4; i += 2)
-            top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[step][i])), fabsf(bf16_hi(qf[step][i]))));
+          for (int i = r & 1; i < 4; i += 2)
+            top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[r >> 1][step][i])),
+                                   fabsf(bf16_hi(qf[r >> 1][step][i]))));
         top = quad_max(top);
         // a power of two brings the head's largest element into [1, 2)
         const uint32_t e = min(max((__float_as_uint(top) >> 23) & 255u, 1u), 253u);
@@ -594,8 +602,10 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
 #pragma unroll
         for (int step = 0; step < D / 16; ++step)
 #pragma unroll
-          for (int i = r; i < 4; i += 2)
-            qf[step][i] = pack_f16(bf16_lo(qf[step][i]) * down, bf16_hi(qf[step][i]) * down);
+          for (int i = r & 1; i < 4; i += 2) {
+            uint32_t& w = qf[r >> 1][step][i];
+            w = pack_f16(bf16_lo(w) * down, bf16_hi(w) * down);
+          }
       }
     }
   };
@@ -646,18 +656,39 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     if (S::kSharedQ) {   // (all warps have left the last segment's tiles)
 #pragma unroll
       for (int step = 0; step < D / 16; ++step)
-        if (step % kWarps == warp)
-          shared_q[32 * step] = make_uint4(qf[step][0], qf[step][1], qf[step][2], qf[step][3]);
+        if (step % kWarps == warp) {
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+            shared_q[32 * (M * step + m)] = make_uint4(qf[m][step][0], qf[m][step][1],
+                                                       qf[m][step][2], qf[m][step][3]);
+        }
       __syncthreads();
     }
     const int tiles = tiles_of(seg);
 
-    float acc[D / 8][4];
+    // q's operands of contraction step `step`
+    auto q_of = [&](int m, int step, uint32_t (&q)[4]) {
+      uint4 v = make_uint4(qf[m][step][0], qf[m][step][1], qf[m][step][2], qf[m][step][3]);
+      if (S::kSharedQ) v = shared_q[32 * (M * step + m)];
+      q[0] = v.x;
+      q[1] = v.y;
+      q[2] = v.z;
+      q[3] = v.w;
+    };
+
+    float acc[M][D / 8][4];
+    float top[2 * M], sum[2 * M];   // of rows g + 8 r
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
+#pragma unroll
+    for (int r = 0; r < 2 * M; ++r) {
+      top[r] = -INFINITY;
+      sum[r] = 0.f;
+    }
 
     for (int i = 0; i < tiles; ++i, ++n) {
       const uint8_t* const tile = stage0 + stage * S::kStageBytes;
@@ -666,14 +697,16 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       cp_wait<2 * S::kStages - 1>();   // this tile's keys
       __syncwarp();
 
-      // scores: [heads g, g + 8] x [tokens 8 n + 2 t, + 1]
-      float x[2 * S::kGroups][4];
+      // scores: [heads g + 8 r] x [tokens 8 n + 2 t, + 1]
+      float x[M][2 * S::kGroups][4];
 #pragma unroll
       for (int h = 0; h < S::kGroups; ++h) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int m = 0; m < M; ++m)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[2 * h + n][j] = 0.f;
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[m][2 * h + n][j] = 0.f;
 #pragma unroll
         for (int p = 0; p < S::kKeyPieces; ++p) {
           uint4 w[2];
@@ -685,46 +718,50 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
           if (E4M3) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              uint32_t aq[4] = {qf[4 * p + j][0], qf[4 * p + j][1], qf[4 * p + j][2],
-                                qf[4 * p + j][3]};
-              if (S::kSharedQ) {
-                const uint4 v = shared_q[32 * (4 * p + j)];
-                aq[0] = v.x;
-                aq[1] = v.y;
-                aq[2] = v.z;
-                aq[3] = v.w;
-              }
+              uint32_t b[2][2];
 #pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16(j == 0 ? w[n].x : j == 1 ? w[n].y : j == 2 ? w[n].z : w[n].w, b0,
-                              b1);
-                mma16816<true>(x[2 * h + n], aq, b0, b1);
+              for (int n = 0; n < 2; ++n)
+                e4m3x4_to_f16(j == 0 ? w[n].x : j == 1 ? w[n].y : j == 2 ? w[n].z : w[n].w,
+                              b[n][0], b[n][1]);
+#pragma unroll
+              for (int m = 0; m < M; ++m) {
+                uint32_t aq[4];
+                q_of(m, 4 * p + j, aq);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                  mma16816<true>(x[m][2 * h + n], aq, b[n][0], b[n][1]);
               }
             }
           } else {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              mma16816<false>(x[2 * h + n], qf[2 * p], w[n].x, w[n].y);
-              mma16816<false>(x[2 * h + n], qf[2 * p + 1], w[n].z, w[n].w);
+            for (int m = 0; m < M; ++m) {
+              uint32_t a0[4], a1[4];
+              q_of(m, 2 * p, a0);
+              q_of(m, 2 * p + 1, a1);
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                mma16816<false>(x[m][2 * h + n], a0, w[n].x, w[n].y);
+                mma16816<false>(x[m][2 * h + n], a1, w[n].z, w[n].w);
+              }
             }
           }
         }
         // base 2, with the value rows' scales in the exponent
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          float (&y)[4] = x[2 * h + n];
-          if (E4M3) {
-            const float4 sc =
-                *reinterpret_cast<const float4*>(side + 2 * (8 * (2 * h + n) + 2 * t));
+          float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
+          if (E4M3)
+            sc = *reinterpret_cast<const float4*>(side + 2 * (8 * (2 * h + n) + 2 * t));
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              y[2 * r] = fmaf(y[2 * r] * sc.x, row_scale[r], sc.y);
-              y[2 * r + 1] = fmaf(y[2 * r + 1] * sc.z, row_scale[r], sc.w);
+          for (int r = 0; r < 2 * M; ++r) {
+            float* const y = x[r >> 1][2 * h + n] + 2 * (r & 1);
+            if (E4M3) {
+              y[0] = fmaf(y[0] * sc.x, row_scale[r], sc.y);
+              y[1] = fmaf(y[1] * sc.z, row_scale[r], sc.w);
+            } else {
+              y[0] *= row_scale[r];
+              y[1] *= row_scale[r];
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] *= row_scale[j >> 1];
           }
         }
       }
@@ -740,7 +777,10 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
         for (int n = 0; n < 2 * S::kGroups; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (!((here[0] >> (8 * n + 2 * t + (j & 1))) & 1u)) x[n][j] = -INFINITY;
+            if (!((here[0] >> (8 * n + 2 * t + (j & 1))) & 1u)) {
+#pragma unroll
+              for (int m = 0; m < M; ++m) x[m][n][j] = -INFINITY;
+            }
       }
 #pragma unroll
       for (int j = 0; j + 1 < S::kStages; ++j) {
@@ -751,54 +791,54 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
       step();
 
       // a tile that passes the bound moves it
-      float high[2];
+      float high[2 * M];
+      bool moves = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        high[r] = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
+      for (int r = 0; r < 2 * M; ++r) {
+        const float* const y0 = x[r >> 1][0] + 2 * (r & 1);
+        high[r] = fmaxf(y0[0], y0[1]);
 #pragma unroll
-        for (int n = 1; n < 2 * S::kGroups; ++n)
-          high[r] = fmaxf(high[r], fmaxf(x[n][2 * r], x[n][2 * r + 1]));
+        for (int n = 1; n < 2 * S::kGroups; ++n) {
+          const float* const y = x[r >> 1][n] + 2 * (r & 1);
+          high[r] = fmaxf(high[r], fmaxf(y[0], y[1]));
+        }
+        moves = moves || high[r] > top[r] + kMostWeight;
       }
-      const bool moves =
-          high[0] > top[0] + kMostWeight || high[1] > top[1] + kMostWeight;
       if (__any_sync(0xffffffffu, moves)) {
-        float f[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < 2 * M; ++r) {
           const float was = top[r];
           top[r] = fmaxf(was, quad_max(high[r]) - kNewWeight);
-          f[r] = weight(was, top[r]);
-          sum[r] *= f[r];
-        }
+          const float f = weight(was, top[r]);
+          sum[r] *= f;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          acc[n][0] *= f[0];
-          acc[n][1] *= f[0];
-          acc[n][2] *= f[1];
-          acc[n][3] *= f[1];
+          for (int n = 0; n < D / 8; ++n) {
+            acc[r >> 1][n][2 * (r & 1)] *= f;
+            acc[r >> 1][n][2 * (r & 1) + 1] *= f;
+          }
         }
       }
       // weights
-      const float bound[2] = {top[0] == -INFINITY ? 0.f : top[0],
-                              top[1] == -INFINITY ? 0.f : top[1]};
-      uint32_t wf[S::kGroups][4], wr[S::kGroups][4];
+      uint32_t wf[M][S::kGroups][4], wr[M][S::kGroups][4];
 #pragma unroll
       for (int n = 0; n < 2 * S::kGroups; ++n) {
         float2 inverse = make_float2(1.f, 1.f);
         if (E4M3)
           inverse = *reinterpret_cast<const float2*>(side + 2 * S::kTile + 8 * n + 2 * t);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float w0 = exp2_approx(x[n][2 * r] - bound[r]);
-          const float w1 = exp2_approx(x[n][2 * r + 1] - bound[r]);
-          uint32_t& to = wf[n >> 1][2 * (n & 1) + r];
+        for (int r = 0; r < 2 * M; ++r) {
+          const float bound = top[r] == -INFINITY ? 0.f : top[r];
+          const float* const y = x[r >> 1][n] + 2 * (r & 1);
+          const float w0 = exp2_approx(y[0] - bound), w1 = exp2_approx(y[1] - bound);
+          const int e = 2 * (n & 1) + (r & 1);
+          uint32_t& to = wf[r >> 1][n >> 1][e];
           if (E4M3) {
             sum[r] = fmaf(w0, inverse.x, fmaf(w1, inverse.y, sum[r]));
             to = pack_f16(w0, w1);
           } else {
             sum[r] += w0 + w1;
             to = pack_bf16(w0, w1);
-            wr[n >> 1][2 * (n & 1) + r] = pack_bf16(w0 - bf16_lo(to), w1 - bf16_hi(to));
+            wr[r >> 1][n >> 1][e] = pack_bf16(w0 - bf16_lo(to), w1 - bf16_hi(to));
           }
         }
       }
@@ -844,15 +884,20 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
               }
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma16816<true>(acc[p * S::kChunk + 4 * j + k], wf[h], b[k][0], b[k][1]);
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                  mma16816<true>(acc[m][p * S::kChunk + 4 * j + k], wf[m][h], b[k][0], b[k][1]);
             } else {
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const uint32_t pick = k == 0 ? 0x5410 : 0x7632;
                 const uint32_t b0 = __byte_perm(w[0][j], w[1][j], pick);
                 const uint32_t b1 = __byte_perm(w[2][j], w[3][j], pick);
-                mma16816<false>(acc[p * S::kChunk + 2 * j + k], wf[h], b0, b1);
-                mma16816<false>(acc[p * S::kChunk + 2 * j + k], wr[h], b0, b1);
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                  mma16816<false>(acc[m][p * S::kChunk + 2 * j + k], wf[m][h], b0, b1);
+                  mma16816<false>(acc[m][p * S::kChunk + 2 * j + k], wr[m][h], b0, b1);
+                }
               }
             }
           }
@@ -868,14 +913,14 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     running = next_segment(0, seg);
     if (running && !S::kSharedQ) ask_q(seg);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) sum[r] = quad_sum(sum[r]);
+    for (int r = 0; r < 2 * M; ++r) sum[r] = quad_sum(sum[r]);
     auto put_acc = [&](int to) {
       if (t == 0) {
-        stats[to][g] = make_float2(top[0], sum[0]);
-        stats[to][g + 8] = make_float2(top[1], sum[1]);
+#pragma unroll
+        for (int r = 0; r < 2 * M; ++r) stats[to][g + 8 * r] = make_float2(top[r], sum[r]);
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < 2 * M; ++r) {
         float4* const row = reinterpret_cast<float4*>(join0 + to * S::kJoinBytes) +
                             (g + 8 * r) * (D / 4);
 #pragma unroll
@@ -884,10 +929,11 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int j = 0; j < S::kChunk / 4; ++j) {
-              const int i = p * S::kChunk + 4 * j, e = 2 * r + half;
+              const int i = p * S::kChunk + 4 * j, e = 2 * (r & 1) + half;
               const int f = ((p * 8 + 2 * t + half) * S::kChunk) / 4 + j;
+              const float (&from)[D / 8][4] = acc[r >> 1];
               row[join_place<S::kChunk>(g, f)] =
-                  make_float4(acc[i][e], acc[i + 1][e], acc[i + 2][e], acc[i + 3][e]);
+                  make_float4(from[i][e], from[i + 1][e], from[i + 2][e], from[i + 3][e]);
             }
       }
     };
@@ -896,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
     __syncthreads();
     if (warp < 2) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < 2 * M; ++r) {
         const float2 other = stats[warp][g + 8 * r];
         const float m = fmaxf(top[r], other.x);
         const float mine = weight(top[r], m), its = weight(other.x, m);
@@ -910,13 +956,14 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int j = 0; j < S::kChunk / 4; ++j) {
-              const int i = p * S::kChunk + 4 * j, e = 2 * r + half;
+              const int i = p * S::kChunk + 4 * j, e = 2 * (r & 1) + half;
               const int f = ((p * 8 + 2 * t + half) * S::kChunk) / 4 + j;
+              float (&to)[D / 8][4] = acc[r >> 1];
               const float4 v = row[join_place<S::kChunk>(g, f)];
-              acc[i][e] = acc[i][e] * mine + v.x * its;
-              acc[i + 1][e] = acc[i + 1][e] * mine + v.y * its;
-              acc[i + 2][e] = acc[i + 2][e] * mine + v.z * its;
-              acc[i + 3][e] = acc[i + 3][e] * mine + v.w * its;
+              to[i][e] = to[i][e] * mine + v.x * its;
+              to[i + 1][e] = to[i + 1][e] * mine + v.y * its;
+              to[i + 2][e] = to[i + 2][e] * mine + v.z * its;
+              to[i + 3][e] = to[i + 3][e] * mine + v.w * its;
             }
       }
       __syncwarp();   // every lane has read the statistics it replaces
@@ -969,19 +1016,19 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D>::kCtas)
 }
 
 // Joins the pieces of the items that several workers share. A block takes one
-// item's rows, or a share of them when there are few items; a row gets kJoinWarps /
-// rows-a-block warps, each of which takes every so many-th piece with a running
-// bound.
+// item's rows, or a share of them when there are few items; a row gets `share` warps (a
+// power of two), each of which takes every so many-th piece with a running bound.
 constexpr int kJoinWarps = 16;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int unit) {
+template <int D, int M>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int unit,
+                                                                int share) {
+  constexpr int kRows = M * kMmaRows;
   constexpr int N = D / 32;
   __shared__ float2 stats[kJoinWarps];
   __shared__ float sacc[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int items = a.c.heads * a.chunks;
-  const int share = gridDim.y;                 // warps of a row: a power of two
   const int row = blockIdx.y * (kJoinWarps / share) + warp / share;
   // by item, one of a context without tokens has no joint
   const bool none =
@@ -1062,14 +1109,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-int chunks_of(int group) { return (group + kRows - 1) / kRows; }
+// Whether items can have two tensor core tiles of query heads, and whether they do:
+// two tiles save half the copies and conversions of a token and put down twice as much
+// an item. Measured with 20 heads a kv head (one tile, two tiles): 2^17 tokens of 128 e4m3
+// elements 22.8, 24.8 us; 2^18 33.0, 32.5; 2^19 51.1, 46.4; of 128 bf16 elements 25.9,
+// 28.3; 39.2, 39.7; 83.3, 60.6; of 64 e4m3 15.4, 16.3; 21.4, 21.2; 33.0, 30.7. The
+// lengths are on the device: the table's room stands for them.
+bool two_tiles_fit(int group, int head_dim) { return group > kMmaRows && head_dim <= 128; }
+constexpr int64_t kTwoTileTokens = 1 << 18;
+int chunks_of(int group, int rows) { return (group + rows - 1) / rows; }
 
-template <bool E4M3, int D>
+int64_t table_room(const CacheView& c) {
+  return std::min<int64_t>((int64_t)c.max_pages << c.page_shift, 0x7fffffff);
+}
+
+template <bool E4M3, int D, int M>
 int launch(const Args& a, cudaStream_t stream) {
-  using S = Shape<E4M3, D>;
+  using S = Shape<E4M3, D, M>;
   const int64_t items = (int64_t)a.batch * a.c.heads * a.chunks;
-  const int64_t room =
-      std::min<int64_t>((int64_t)a.c.max_pages << a.c.page_shift, 0x7fffffff);
+  const int64_t room = table_room(a.c);
   // units of the longest context the table can hold (a window's can start
   // before it by a group)
   const int64_t units = (room + kGroup + S::kUnit - 1) / S::kUnit;
@@ -1080,7 +1138,7 @@ int launch(const Args& a, cudaStream_t stream) {
   if (cudaGetDevice(&device) != cudaSuccess) return -3;
   const uint64_t bit = uint64_t(1) << (device & 63);
   if ((opted.load(std::memory_order_relaxed) & bit) == 0 || device >= 64) {
-    if (cudaFuncSetAttribute(paged_attention_kernel<E4M3, D>,
+    if (cudaFuncSetAttribute(paged_attention_kernel<E4M3, D, M>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::kSmemBytes) != cudaSuccess)
       return -3;
@@ -1093,25 +1151,35 @@ int launch(const Args& a, cudaStream_t stream) {
   args.joint_count = (int)std::min<int64_t>(items, grid);
   args.by_worker = args.joint_count < items;
   cudaError_t e = launch_kernel(true, dim3(grid), dim3(kThreads), S::kSmemBytes, stream,
-                                paged_attention_kernel<E4M3, D>, args);
+                                paged_attention_kernel<E4M3, D, M>, args);
   if (e != cudaSuccess) return -3;
   if (args.whole) return 0;
   // few items: a row's pieces go to several warps (2 blocks an SM hold 16 each)
   int share = 1;
   while (share < kJoinWarps && 2 * share * args.joint_count <= 2 * kSms) share *= 2;
-  e = launch_kernel(true, dim3(args.joint_count, share), dim3(kJoinWarps * 32), 0, stream,
-                    join_kernel<D>, args, S::kUnit);
+  e = launch_kernel(true, dim3(args.joint_count, share * M), dim3(kJoinWarps * 32), 0, stream,
+                    join_kernel<D, M>, args, S::kUnit, share);
   return e == cudaSuccess ? 0 : -3;
+}
+
+// The workspace's parts: the joints, of as many items as there can be, then the slots'
+// statistics and rows.
+struct Parts {
+  size_t joints, stats, rows;
+};
+Parts parts_of(int group, int heads, int head_dim, int batch) {
+  const size_t items = (size_t)batch * heads * chunks_of(group, kMmaRows);
+  const size_t slot_rows =
+      (size_t)2 * kMaxWorkers * (two_tiles_fit(group, head_dim) ? 2 : 1) * kMmaRows;
+  return {align256(std::min<size_t>(items, kMaxWorkers) * sizeof(Joint)),
+          align256(slot_rows * sizeof(float2)), slot_rows * head_dim * sizeof(float)};
 }
 
 }  // namespace
 
 size_t paged_attention_ws_bytes(int heads, int head_dim, int batch, int q_heads) {
-  const size_t items =
-      std::min<size_t>((size_t)batch * heads * chunks_of(q_heads / heads), kMaxWorkers);
-  const size_t slots = 2 * kMaxWorkers;
-  return align256(items * sizeof(Joint)) + align256(slots * kRows * sizeof(float2)) +
-         slots * kRows * head_dim * sizeof(float);
+  const Parts p = parts_of(q_heads / heads, heads, head_dim, batch);
+  return p.joints + p.stats + p.rows;
 }
 
 int launch_paged_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int batch,
@@ -1124,27 +1192,34 @@ int launch_paged_attention(const CacheView& c, const uint16_t* q, int64_t q_stri
   a.batch = batch;
   a.q_heads = q_heads;
   a.group = q_heads / c.heads;
-  a.chunks = chunks_of(a.group);
+  const int64_t reach = window > 0 ? std::min<int64_t>(window, table_room(c)) : table_room(c);
+  const int64_t spans = (int64_t)batch * c.heads;
+  const bool two = two_tiles_fit(a.group, c.head_dim) &&
+                   reach >= (kTwoTileTokens + spans - 1) / spans;
+  a.rows = (two ? 2 : 1) * kMmaRows;
+  a.chunks = chunks_of(a.group, a.rows);
   a.lengths = lengths;
   a.scale = scale;
   a.window = window;
   a.out = out;
   a.lse = lse;
-  uint8_t* p = static_cast<uint8_t*>(ws);
+  const Parts parts = parts_of(a.group, c.heads, c.head_dim, batch);
+  uint8_t* const p = static_cast<uint8_t*>(ws);
   a.joints = reinterpret_cast<Joint*>(p);
-  p += align256(std::min<size_t>((size_t)batch * c.heads * a.chunks, kMaxWorkers) *
-                sizeof(Joint));
-  a.stats = reinterpret_cast<float2*>(p);
-  p += align256(2 * kMaxWorkers * kRows * sizeof(float2));
-  a.parts = reinterpret_cast<float*>(p);
+  a.stats = reinterpret_cast<float2*>(p + parts.joints);
+  a.parts = reinterpret_cast<float*>(p + parts.joints + parts.stats);
   if (c.e4m3) {
-    if (c.head_dim == 64) return launch<true, 64>(a, stream);
-    if (c.head_dim == 128) return launch<true, 128>(a, stream);
-    return launch<true, 256>(a, stream);
+    if (c.head_dim == 64)
+      return two ? launch<true, 64, 2>(a, stream) : launch<true, 64, 1>(a, stream);
+    if (c.head_dim == 128)
+      return two ? launch<true, 128, 2>(a, stream) : launch<true, 128, 1>(a, stream);
+    return launch<true, 256, 1>(a, stream);
   }
-  if (c.head_dim == 64) return launch<false, 64>(a, stream);
-  if (c.head_dim == 128) return launch<false, 128>(a, stream);
-  return launch<false, 256>(a, stream);
+  if (c.head_dim == 64)
+    return two ? launch<false, 64, 2>(a, stream) : launch<false, 64, 1>(a, stream);
+  if (c.head_dim == 128)
+    return two ? launch<false, 128, 2>(a, stream) : launch<false, 128, 1>(a, stream);
+  return launch<false, 256, 1>(a, stream);
 }
 
 }  // namespace moe

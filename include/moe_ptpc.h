@@ -727,8 +727,8 @@ MOE_API int moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table,
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
  *         pointers, q_heads not a multiple of heads, scale not finite, batch
  *         < 0, max_pages < 0), MOE_ERR_UNSUPPORTED (batch > 65535, or tables
- *         of more than about 2^31 units of 64 tokens and 16 query heads in
- *         all), MOE_ERR_WORKSPACE. batch == 0 is a no-op.
+ *         of more than about 2^31 units of 64 tokens and 16 to 32 query
+ *         heads in all), MOE_ERR_WORKSPACE. batch == 0 is a no-op.
  */
 MOE_API size_t moe_paged_attention_workspace_size(const moe_kv_cache* cache, int batch,
                                                   int q_heads);

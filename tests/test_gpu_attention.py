@@ -320,6 +320,49 @@ def test_attention(lengths, hq, hk, d, size, kind):
     check_attention(cache, q, table, lengths)
 
 
+@pytest.mark.parametrize("group", [17, 24, 32, 33, 71])
+@pytest.mark.parametrize("d,kind", [(64, "e4m3"), (128, "e4m3"), (64, "bf16"), (128, "bf16")])
+def test_attention_many_heads_a_kv_head(group, d, kind):
+    """Groups that fill two tensor core tiles, end inside the second or need more:
+    one CTA an item, and in wide tables, whose items have two tiles, cut and joined."""
+    for lengths, hk, size in (([1, 0, 63, 64, 65, 127, 128, 129, 200], 2, 16),
+                              ([6000, 17], 1, 64)):
+        cache, q, table = attention_case(group, lengths, hk * group, hk, d, size, kind)
+        check_attention(cache, q, table, lengths)
+        wide = np.full((len(lengths), 5000), -1, np.int32)
+        wide[:, :table.shape[1]] = table
+        check_attention(cache, q, wide, lengths)
+
+
+@pytest.mark.parametrize("d,kind", [(64, "e4m3"), (128, "e4m3"), (64, "bf16"), (128, "bf16")])
+def test_attention_many_heads_in_a_window(d, kind):
+    lengths = [4000, 3001, 3000, 2999, 0] + [17 + b for b in range(45)]
+    cache, q, table = attention_case(d, lengths, 40, 2, d, 16, kind)
+    table[0, :1000 // 16] = -1
+    table[1, 5:9] = cache.pages
+    check_attention(cache, q, table, lengths, window=3000)
+
+
+def test_attention_many_heads_in_a_workspace_of_any_content():
+    """The largest workspace a call can ask for, between guard bands that stay, and the
+    same results from call to call."""
+    lengths = [40000, 0, 20000, 5]
+    cache, q, table = attention_case(61, lengths, 48, 2, 128, 64, "e4m3")
+    wide = np.full((4, 2000), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    want = check_attention(cache, q, wide, lengths)
+    from expert_layer_ptpc_gb300 import binding
+    need = binding.moe_paged_attention_workspace_size(cache.struct, 4, 48)
+    space = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    t = torch.from_numpy(wide).cuda()
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    for fill in (0xFF, 0):
+        space[256:256 + need] = fill
+        out, lse = cache.attend(q, t, n, return_lse=True, ws=space[256:256 + need])
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert bool((space[:256] == 0xA5).all()) and bool((space[256 + need:] == 0xA5).all())
+
+
 @pytest.mark.parametrize("window", [1, 15, 64, 100, 5000])
 @pytest.mark.parametrize("kind,d", [("e4m3", 128), ("bf16", 64)])
 def test_attention_window(window, kind, d):
