@@ -788,7 +788,8 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
     """Attention of one new token per context: q [batch, q_heads, head_dim]
     bf16 over the cached tokens; returns out, of q's shape, or (out, lse) with
     return_lse. `lse`: optional [batch, q_heads] fp32 tensor that receives the
-    log of the sums."""
+    log of the sums. ws: a contiguous tensor of at least
+    moe_paged_attention_workspace_size bytes (None: a new one)."""
     batch, hq, d = q.shape
     q_stride = _need_heads(q, hq, cache.head_dim, "q")
     stride, pages = _need_table(block_table, batch)
@@ -810,11 +811,13 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
     if ws is None:
         need = moe_paged_attention_workspace_size(cache, batch, hq)
         ws = _empty(max(need, 1), torch.uint8, q.device, stream)
+    elif not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor")
     status = (_lib or load_library()).moe_paged_attention(
         ctypes.byref(cache), q.data_ptr(), q_stride, batch, hq, block_table.data_ptr(), stride,
         pages, lengths.data_ptr(), scale, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, q))
+        None if lse is None else lse.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(stream, q))
     if status:
         raise MoeError("moe_paged_attention", status)
     return (out, lse) if return_lse else out
