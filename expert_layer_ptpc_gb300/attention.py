@@ -77,6 +77,7 @@ class Rotary:
         self.rot_dim, self.axes = 2 * freq.numel(), axes
         self.plan = binding.moe_rotary_plan(self.turns.data_ptr(), self.pair_axis.data_ptr(),
                                             axes, self.rot_dim, int(bool(neighbours)))
+        self.plan.device = self.turns.get_device()
 
     def apply(self, positions, q, k=None, inverse=False, q_out=None, k_out=None, stream=None):
         """q [T, heads, head_dim] bf16, and k, rotated by positions [axes, T]
@@ -98,11 +99,12 @@ class PagedKVCache:
         coded = k.dtype == torch.uint8
         if coded != (k_scale is not None) or coded != (v_scale is not None):
             raise ValueError("an e4m3 cache has scales for k and v, a bf16 cache has none")
+        index = k.get_device()
         for t, n in ((k, "k"), (v, "v")):
-            binding._need(t, k.dtype, n)
+            binding._need_on(t, k.dtype, n, index)
         if coded:
             for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                binding._need(t, torch.float32, n)
+                binding._need_on(t, torch.float32, n, index)
                 if t.shape != k.shape[:3]:
                     raise ValueError(f"{n} must be {tuple(k.shape[:3])}, got {tuple(t.shape)}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
@@ -111,6 +113,7 @@ class PagedKVCache:
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if coded else None,
             v_scale.data_ptr() if coded else None, self.pages, self.heads, self.page_size,
             self.head_dim, dtypes[k.dtype])
+        self.struct.device = index
         self._ws = {}
         self._scale = 1.0 / math.sqrt(self.head_dim)
 
@@ -154,7 +157,7 @@ class PagedKVCache:
         on different streams may overlap, so each stream has its own)."""
         if torch.cuda.is_current_stream_capturing():
             return self._new_workspace(batch, q_heads, stream)   # the graph's own
-        on = binding._raw_stream(stream, self.k)
+        on = binding._raw_stream(stream, self.struct.device)
         ws = self._ws.get((on, batch, q_heads))
         if ws is None:
             need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)

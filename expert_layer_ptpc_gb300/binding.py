@@ -44,6 +44,7 @@ class moe_rotary_plan(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
                 ("axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
                 ("neighbours", ctypes.c_int32)]
+    device = None   # index of the GPU that the pointers belong to, where known
 
 
 class moe_kv_cache(ctypes.Structure):
@@ -52,6 +53,7 @@ class moe_kv_cache(ctypes.Structure):
                 ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+    device = None   # as above
 
 
 _P = ctypes.c_void_p
@@ -615,15 +617,39 @@ def moe_workspace_status(ws, stream=None):
 
 # ---------------------------------------------------------------------------
 # Attention operators. `plan` and `cache` are moe_rotary_plan and moe_kv_cache
-# structures (expert_layer_ptpc_gb300.attention builds them from tensors).
+# structures (expert_layer_ptpc_gb300.attention builds them from tensors). A call's
+# tensors all lie on the current GPU.
 # ---------------------------------------------------------------------------
-def _raw_stream(stream, t):
-    """The handle of `stream`, or of the current stream of t's device (asked
+def _gpu_of(t, name, *structs):
+    """The index of t's GPU. The library launches on the current GPU, so that it
+    has to be that one, and the one that the call's plan and cache lie on."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    index = t.get_device()
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current GPU, is on GPU {index}")
+    for s in structs:
+        if s.device is not None and s.device != index:
+            what = "cache" if isinstance(s, moe_kv_cache) else "plan"
+            raise ValueError(f"{name} is on GPU {index}, the {what} on GPU {s.device}")
+    return index
+
+
+def _need_on(t, dtype, name, index):
+    _need(t, dtype, name)
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on GPU {index}")
+
+
+def _raw_stream(stream, index):
+    """The handle of `stream`, or of the current stream of GPU `index` (asked
     for without making a Stream object: a small call costs about 10 us, and
     that object would be 3 of them)."""
     if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"the stream must be one of GPU {index}")
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(shape, dtype, device, stream):
@@ -635,11 +661,12 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _need_heads(t, heads, head_dim, name):
+def _need_heads(t, heads, head_dim, name, index):
     """A [T, heads, head_dim] bf16 tensor whose tokens may be strided (a slice
-    of a wider projection); returns the token stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    of a wider projection) on GPU `index`; returns the token stride."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on GPU {index}" if t.is_cuda else
+                         f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     n, h, d = t.shape
@@ -652,22 +679,23 @@ def _need_heads(t, heads, head_dim, name):
     return stride if n > 1 else h * d
 
 
-def _need_slots(slots, T, cache):
-    _need(slots, torch.int32, "slots")
+def _need_slots(slots, T, index):
+    _need_on(slots, torch.int32, "slots", index)
     if slots.numel() != T:
         raise ValueError(f"slots must have {T} entries, got {slots.numel()}")
 
 
-def _need_positions(positions, plan, T):
-    _need(positions, torch.int32, "positions")
+def _need_positions(positions, plan, T, index):
+    _need_on(positions, torch.int32, "positions", index)
     if tuple(positions.shape) != (plan.axes, T):
         raise ValueError(f"positions must be [{plan.axes}, {T}], got {tuple(positions.shape)}")
 
 
-def _need_table(table, batch):
+def _need_table(table, batch, index):
     """A [batch, max_pages] int32 block table; returns (row stride, max_pages)."""
-    if not table.is_cuda:
-        raise ValueError("block_table must be a CUDA tensor")
+    if table.get_device() != index:
+        raise ValueError(f"block_table must be on GPU {index}" if table.is_cuda else
+                         "block_table must be a CUDA tensor")
     if table.dtype != torch.int32:
         raise ValueError(f"block_table must be {torch.int32}, got {table.dtype}")
     n, pages = table.shape
@@ -683,23 +711,24 @@ def moe_rotary(plan, positions, q, k=None, inverse=False, q_out=None, k_out=None
     """q [T, heads, head_dim] bf16 (and k) rotated by positions [axes, T];
     returns (q_out, k_out), k_out None without k."""
     T, hq, d = q.shape
-    q_stride = _need_heads(q, hq, d, "q")
-    _need_positions(positions, plan, T)
+    index = _gpu_of(q, "q", plan)
+    q_stride = _need_heads(q, hq, d, "q", index)
+    _need_positions(positions, plan, T, index)
     if q_out is None:
         q_out, qo_stride = _empty((T, hq, d), torch.bfloat16, q.device, stream), hq * d
     else:
-        qo_stride = _need_heads(q_out, hq, d, "q_out")
+        qo_stride = _need_heads(q_out, hq, d, "q_out", index)
         if q_out.shape[0] != T:
             raise ValueError("q_out must have as many tokens as q")
     hk = k_stride = ko_stride = 0
     k_ptr = ko_ptr = None
     if k is not None:
         hk = k.shape[1]
-        k_stride = _need_heads(k, hk, d, "k")
+        k_stride = _need_heads(k, hk, d, "k", index)
         if k_out is None:
             k_out, ko_stride = _empty((T, hk, d), torch.bfloat16, q.device, stream), hk * d
         else:
-            ko_stride = _need_heads(k_out, hk, d, "k_out")
+            ko_stride = _need_heads(k_out, hk, d, "k_out", index)
         if k.shape[0] != T or k_out.shape[0] != T:
             raise ValueError("k and k_out must have as many tokens as q")
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
@@ -708,7 +737,7 @@ def moe_rotary(plan, positions, q, k=None, inverse=False, q_out=None, k_out=None
     status = (_lib or load_library()).moe_rotary(
         ctypes.byref(plan), positions.data_ptr(), T, d, q.data_ptr(), q_stride, hq,
         q_out.data_ptr(), qo_stride, k_ptr, k_stride, hk, ko_ptr, ko_stride,
-        int(bool(inverse)), _raw_stream(stream, q))
+        int(bool(inverse)), _raw_stream(stream, index))
     if status:
         raise MoeError("moe_rotary", status)
     return q_out, k_out
@@ -717,14 +746,15 @@ def moe_rotary(plan, positions, q, k=None, inverse=False, q_out=None, k_out=None
 def moe_kv_write(cache, k, v, slots, stream=None):
     """k, v [T, heads, head_dim] bf16 into the cache's slots [T] int32."""
     T = k.shape[0]
-    k_stride = _need_heads(k, cache.heads, cache.head_dim, "k")
-    v_stride = _need_heads(v, cache.heads, cache.head_dim, "v")
+    index = _gpu_of(k, "k", cache)
+    k_stride = _need_heads(k, cache.heads, cache.head_dim, "k", index)
+    v_stride = _need_heads(v, cache.heads, cache.head_dim, "v", index)
     if v.shape[0] != T:
         raise ValueError("k and v must have as many tokens")
-    _need_slots(slots, T, cache)
+    _need_slots(slots, T, index)
     status = (_lib or load_library()).moe_kv_write(
         ctypes.byref(cache), slots.data_ptr(), T, k.data_ptr(), k_stride, v.data_ptr(),
-        v_stride, _raw_stream(stream, k))
+        v_stride, _raw_stream(stream, index))
     if status:
         raise MoeError("moe_kv_write", status)
 
@@ -732,23 +762,24 @@ def moe_kv_write(cache, k, v, slots, stream=None):
 def moe_rotary_kv_write(plan, positions, cache, q, k, v, slots, q_out=None, stream=None):
     """q rotated (returned), k rotated and v as it is into the cache."""
     T, hq, d = q.shape
-    q_stride = _need_heads(q, hq, cache.head_dim, "q")
-    k_stride = _need_heads(k, cache.heads, d, "k")
-    v_stride = _need_heads(v, cache.heads, d, "v")
+    index = _gpu_of(q, "q", plan, cache)
+    q_stride = _need_heads(q, hq, cache.head_dim, "q", index)
+    k_stride = _need_heads(k, cache.heads, d, "k", index)
+    v_stride = _need_heads(v, cache.heads, d, "v", index)
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("q, k and v must have as many tokens")
-    _need_positions(positions, plan, T)
-    _need_slots(slots, T, cache)
+    _need_positions(positions, plan, T, index)
+    _need_slots(slots, T, index)
     if q_out is None:
         q_out, qo_stride = _empty((T, hq, d), torch.bfloat16, q.device, stream), hq * d
     else:
-        qo_stride = _need_heads(q_out, hq, d, "q_out")
+        qo_stride = _need_heads(q_out, hq, d, "q_out", index)
         if q_out.shape[0] != T:
             raise ValueError("q_out must have as many tokens as q")
     status = (_lib or load_library()).moe_rotary_kv_write(
         ctypes.byref(plan), positions.data_ptr(), ctypes.byref(cache), slots.data_ptr(), T,
         q.data_ptr(), q_stride, hq, q_out.data_ptr(), qo_stride, k.data_ptr(), k_stride,
-        v.data_ptr(), v_stride, _raw_stream(stream, q))
+        v.data_ptr(), v_stride, _raw_stream(stream, index))
     if status:
         raise MoeError("moe_rotary_kv_write", status)
     return q_out
@@ -757,22 +788,23 @@ def moe_rotary_kv_write(plan, positions, cache, q, k, v, slots, q_out=None, stre
 def moe_kv_read(cache, block_table, offsets, rows, k_out=None, v_out=None, stream=None):
     """Contexts offsets[b]..offsets[b + 1] of the cache as bf16 (k, v)
     [rows, heads, head_dim]."""
+    index = _gpu_of(offsets, "offsets", cache)
     _need(offsets, torch.int32, "offsets")
     batch = offsets.numel() - 1
-    stride, pages = _need_table(block_table, batch)
+    stride, pages = _need_table(block_table, batch, index)
     shape = (rows, cache.heads, cache.head_dim)
     outs = []
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
             t = _empty(shape, torch.bfloat16, offsets.device, stream)
         else:
-            _need(t, torch.bfloat16, n)
+            _need_on(t, torch.bfloat16, n, index)
             if tuple(t.shape) != shape:
                 raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
         outs.append(t)
     status = (_lib or load_library()).moe_kv_read(
         ctypes.byref(cache), block_table.data_ptr(), stride, pages, offsets.data_ptr(), batch,
-        rows, outs[0].data_ptr(), outs[1].data_ptr(), _raw_stream(stream, offsets))
+        rows, outs[0].data_ptr(), outs[1].data_ptr(), _raw_stream(stream, index))
     if status:
         raise MoeError("moe_kv_read", status)
     return tuple(outs)
@@ -791,19 +823,20 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
     log of the sums. ws: a contiguous tensor of at least
     moe_paged_attention_workspace_size bytes (None: a new one)."""
     batch, hq, d = q.shape
-    q_stride = _need_heads(q, hq, cache.head_dim, "q")
-    stride, pages = _need_table(block_table, batch)
-    _need(lengths, torch.int32, "lengths")
+    index = _gpu_of(q, "q", cache)
+    q_stride = _need_heads(q, hq, cache.head_dim, "q", index)
+    stride, pages = _need_table(block_table, batch, index)
+    _need_on(lengths, torch.int32, "lengths", index)
     if lengths.numel() != batch:
         raise ValueError(f"lengths must have {batch} entries, got {lengths.numel()}")
     if out is None:
         out = _empty((batch, hq, d), torch.bfloat16, q.device, stream)
     else:
-        _need(out, torch.bfloat16, "out")
+        _need_on(out, torch.bfloat16, "out", index)
         if tuple(out.shape) != (batch, hq, d):
             raise ValueError(f"out must be {(batch, hq, d)}, got {tuple(out.shape)}")
     if lse is not None:
-        _need(lse, torch.float32, "lse")
+        _need_on(lse, torch.float32, "lse", index)
         if tuple(lse.shape) != (batch, hq):
             raise ValueError(f"lse must be {(batch, hq)}, got {tuple(lse.shape)}")
     elif return_lse:
@@ -811,13 +844,13 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
     if ws is None:
         need = moe_paged_attention_workspace_size(cache, batch, hq)
         ws = _empty(max(need, 1), torch.uint8, q.device, stream)
-    elif not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous CUDA tensor")
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous CUDA tensor on GPU {index}")
     status = (_lib or load_library()).moe_paged_attention(
         ctypes.byref(cache), q.data_ptr(), q_stride, batch, hq, block_table.data_ptr(), stride,
         pages, lengths.data_ptr(), scale, window, out.data_ptr(),
         None if lse is None else lse.data_ptr(), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _raw_stream(stream, q))
+        ws.numel() * ws.element_size(), _raw_stream(stream, index))
     if status:
         raise MoeError("moe_paged_attention", status)
     return (out, lse) if return_lse else out

@@ -5,7 +5,7 @@ call gets. No call here reaches a kernel."""
 import pytest
 import torch
 
-from expert_layer_ptpc_gb300 import binding
+from expert_layer_ptpc_gb300 import attention, binding
 
 
 class OnGpu:
@@ -87,3 +87,118 @@ def test_a_workspace_counts_in_bytes(calls, dtype, size):
     attend(ws=OnGpu(torch.zeros(64, dtype=dtype)))
     (name, args), = calls.made
     assert name == "moe_paged_attention" and args[-2] == size
+
+
+# ---------------------------------------------------------------------------
+# devices
+# ---------------------------------------------------------------------------
+def plan_struct(axes=1, rot=64):
+    return binding.moe_rotary_plan(0x10000, 0x10000, axes, rot, 0)
+
+
+def rotate(**kw):
+    args = dict(plan=plan_struct(), positions=int32(1, 3), q=bf16(3, 8, 64), k=bf16(3, 2, 64),
+                q_out=bf16(3, 8, 64), k_out=bf16(3, 2, 64))
+    args.update(kw)
+    return binding.moe_rotary(**args)
+
+
+def write(**kw):
+    args = dict(cache=cache_struct(), k=bf16(3, 2, 64), v=bf16(3, 2, 64), slots=int32(3))
+    args.update(kw)
+    return binding.moe_kv_write(**args)
+
+
+def write_rotary(**kw):
+    args = dict(plan=plan_struct(), positions=int32(1, 3), cache=cache_struct(),
+                q=bf16(3, 8, 64), k=bf16(3, 2, 64), v=bf16(3, 2, 64), slots=int32(3),
+                q_out=bf16(3, 8, 64))
+    args.update(kw)
+    return binding.moe_rotary_kv_write(**args)
+
+
+def read(**kw):
+    args = dict(cache=cache_struct(), block_table=int32(3, 4), offsets=int32(4), rows=9,
+                k_out=bf16(9, 2, 64), v_out=bf16(9, 2, 64))
+    args.update(kw)
+    return binding.moe_kv_read(**args)
+
+
+EVERY_CALL = [rotate, write, write_rotary, read, attend]
+
+
+def tensors_of(call):
+    """The names of a call's tensor arguments, with stand-ins on GPU 1."""
+    other = dict(positions=int32(1, 3, index=1), q=bf16(3, 8, 64, index=1),
+                 k=bf16(3, 2, 64, index=1), v=bf16(3, 2, 64, index=1),
+                 q_out=bf16(3, 8, 64, index=1), slots=int32(3, index=1),
+                 block_table=int32(3, 4, index=1))
+    own = {rotate: dict(k_out=bf16(3, 2, 64, index=1)),
+           read: dict(offsets=int32(4, index=1), k_out=bf16(9, 2, 64, index=1),
+                      v_out=bf16(9, 2, 64, index=1)),
+           attend: dict(lengths=int32(3, index=1), out=bf16(3, 8, 64, index=1),
+                        lse=OnGpu(torch.zeros(3, 8), 1),
+                        ws=OnGpu(torch.zeros(64, dtype=torch.uint8), 1))}
+    shared = {rotate: ("positions", "q", "k", "q_out"), write: ("k", "v", "slots"),
+              write_rotary: ("positions", "q", "k", "v", "slots", "q_out"),
+              read: ("block_table",), attend: ("q", "block_table")}
+    return {**{n: other[n] for n in shared[call]}, **own.get(call, {})}
+
+
+@pytest.mark.parametrize("call", EVERY_CALL, ids=lambda f: f.__name__)
+def test_tensors_of_two_gpus_are_refused(calls, call):
+    call()
+    assert len(calls.made) == 1
+    for name, t in tensors_of(call).items():
+        with pytest.raises(ValueError, match="GPU"):
+            call(**{name: t})
+    assert len(calls.made) == 1
+
+
+@pytest.mark.parametrize("call", EVERY_CALL, ids=lambda f: f.__name__)
+def test_tensors_of_a_gpu_that_is_not_current_are_refused(calls, call, monkeypatch):
+    """The library launches on the current GPU."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="current"):
+        call()
+    with pytest.raises(ValueError, match="current"):
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+        call(**tensors_of(call))
+    assert not calls.made
+
+
+@pytest.mark.parametrize("call", [write, write_rotary, read, attend], ids=lambda f: f.__name__)
+def test_a_cache_on_another_gpu_is_refused(calls, call):
+    cache = cache_struct()
+    cache.device = 1
+    with pytest.raises(ValueError, match="cache"):
+        call(cache=cache)
+    assert not calls.made
+
+
+@pytest.mark.parametrize("call", [rotate, write_rotary], ids=lambda f: f.__name__)
+def test_a_plan_on_another_gpu_is_refused(calls, call):
+    plan = plan_struct()
+    plan.device = 1
+    with pytest.raises(ValueError, match="plan"):
+        call(plan=plan)
+    assert not calls.made
+
+
+@pytest.mark.parametrize("call", EVERY_CALL, ids=lambda f: f.__name__)
+def test_a_stream_of_another_gpu_is_refused(calls, call):
+    class Stream:
+        cuda_stream, device_index = 77, 0
+    call(stream=Stream())
+    assert calls.made.pop()[1][-1] == 77
+    Stream.device_index = 1
+    with pytest.raises(ValueError, match="stream"):
+        call(stream=Stream())
+    assert not calls.made
+
+
+def test_a_plan_on_the_host_is_refused(calls):
+    r = attention.Rotary(attention.frequencies(64), device="cpu")
+    with pytest.raises(ValueError, match="plan"):
+        r.apply(int32(1, 3), bf16(3, 8, 64), q_out=bf16(3, 8, 64))
+    assert not calls.made
