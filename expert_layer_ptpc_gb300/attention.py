@@ -8,6 +8,7 @@ frequencies, the cache's tensors) and call the library entry points of
 """
 
 import math
+import threading
 
 import torch
 
@@ -114,7 +115,7 @@ class PagedKVCache:
             v_scale.data_ptr() if coded else None, self.pages, self.heads, self.page_size,
             self.head_dim, dtypes[k.dtype])
         self.struct.device = index
-        self._ws = {}
+        self._kept = threading.local()
         self._scale = 1.0 / math.sqrt(self.head_dim)
 
     @classmethod
@@ -153,17 +154,20 @@ class PagedKVCache:
         return binding.moe_kv_read(self.struct, block_table, offsets, rows, k_out, v_out, stream)
 
     def workspace(self, batch, q_heads, stream=None):
-        """The attention workspace of one stream, kept for the next step (calls
-        on different streams may overlap, so each stream has its own)."""
+        """The attention workspace of one stream and host thread, kept for the
+        next step. Calls on different streams may overlap, so each stream has its
+        own. A call is two launches, between which another thread may enqueue its
+        own on the same stream, so each thread has its own too."""
         if torch.cuda.is_current_stream_capturing():
             return self._new_workspace(batch, q_heads, stream)   # the graph's own
         on = binding._raw_stream(stream, self.struct.device)
-        ws = self._ws.get((on, batch, q_heads))
+        kept = self._kept.__dict__
+        ws = kept.get((on, batch, q_heads))
         if ws is None:
             need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
-            held = [w for (o, *_), w in self._ws.items() if o == on and w.numel() >= need]
+            held = [w for (o, *_), w in kept.items() if o == on and w.numel() >= need]
             ws = held[0] if held else self._new_workspace(batch, q_heads, stream)
-            self._ws[on, batch, q_heads] = ws
+            kept[on, batch, q_heads] = ws
         return ws
 
     def _new_workspace(self, batch, q_heads, stream):

@@ -2,10 +2,12 @@
 tensors: what is refused before the library is called, and which workspace a
 call gets. No call here reaches a kernel."""
 
+import threading
+
 import pytest
 import torch
 
-from expert_layer_ptpc_gb300 import attention, binding
+from expert_layer_ptpc_gb300 import attention, binding, build
 
 
 class OnGpu:
@@ -202,3 +204,37 @@ def test_a_plan_on_the_host_is_refused(calls):
     with pytest.raises(ValueError, match="plan"):
         r.apply(int32(1, 3), bf16(3, 8, 64), q_out=bf16(3, 8, 64))
     assert not calls.made
+
+
+# ---------------------------------------------------------------------------
+# the workspace a cache keeps
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def streams(monkeypatch):
+    """The real library (its sizes), no stream capturing, current stream 5."""
+    build.build()
+    binding.load_library()
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 5, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+
+def cache_of(heads=4, d=128, index=0):
+    pages = torch.zeros((2, heads, 16, d), dtype=torch.uint8)
+    scales = torch.ones((2, heads, 16))
+    return attention.PagedKVCache(OnGpu(pages, index), OnGpu(pages.clone(), index),
+                                  OnGpu(scales, index), OnGpu(scales.clone(), index))
+
+
+def test_threads_have_workspaces_of_their_own(streams):
+    """A call is two launches, and two threads' calls on one stream may be enqueued one
+    between the other's: they must not share the partial results."""
+    cache = cache_of()
+    mine = cache.workspace(8, 64)
+    assert cache.workspace(8, 64) is mine
+    other = []
+    thread = threading.Thread(target=lambda: other.extend(
+        (cache.workspace(8, 64), cache.workspace(8, 64))))
+    thread.start()
+    thread.join()
+    assert other[0] is other[1]
+    assert other[0].data_ptr() != mine.data_ptr()
