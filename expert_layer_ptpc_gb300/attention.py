@@ -87,6 +87,15 @@ class Rotary:
         return binding.moe_rotary(self.plan, positions, q, k, inverse, q_out, k_out, stream)
 
 
+def _captured(stream, on):
+    """Whether a graph is being captured from `stream` (None: the current one),
+    whose handle is `on`. (Making a stream current to ask costs some microseconds.)"""
+    if stream is None or on == torch._C._cuda_getCurrentRawStream(stream.device_index):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class PagedKVCache:
     """Pages of keys and values, [pages, heads, page_size, head_dim] each, as
     e4m3 codes with one fp32 scale per token and head, or in bf16."""
@@ -158,9 +167,9 @@ class PagedKVCache:
         next step. Calls on different streams may overlap, so each stream has its
         own. A call is two launches, between which another thread may enqueue its
         own on the same stream, so each thread has its own too."""
-        if torch.cuda.is_current_stream_capturing():
-            return self._new_workspace(batch, q_heads, stream)   # the graph's own
         on = binding._raw_stream(stream, self.struct.device)
+        if _captured(stream, on):
+            return self._new_workspace(batch, q_heads, stream)   # the graph's own
         kept = self._kept.__dict__
         ws = kept.get((on, batch, q_heads))
         if ws is None:

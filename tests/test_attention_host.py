@@ -2,6 +2,7 @@
 tensors: what is refused before the library is called, and which workspace a
 call gets. No call here reaches a kernel."""
 
+import contextlib
 import threading
 
 import pytest
@@ -238,3 +239,43 @@ def test_threads_have_workspaces_of_their_own(streams):
     thread.join()
     assert other[0] is other[1]
     assert other[0].data_ptr() != mine.data_ptr()
+
+
+class CurrentStream:
+    """torch.cuda's current stream, and which streams are being captured."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.capturing = None, set()
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream",
+                            lambda index: self.current.cuda_stream if self.current else 5)
+        monkeypatch.setattr(torch.cuda, "stream", self.switched)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
+                            lambda: self.current in self.capturing)
+
+    @contextlib.contextmanager
+    def switched(self, stream):
+        before, self.current = self.current, stream
+        yield
+        self.current = before
+
+
+class Side:
+    cuda_stream, device_index = 77, 0
+
+
+def test_a_captured_call_does_not_use_the_kept_workspace(streams, monkeypatch):
+    """A graph that holds the kept workspace would write to it at any later time. The
+    stream that counts is the call's, not the current one."""
+    on, side, cache = CurrentStream(monkeypatch), Side(), cache_of()
+    kept = cache.workspace(8, 64, side)
+    assert cache.workspace(8, 64, side) is kept
+    on.capturing = {side}
+    captured = cache.workspace(8, 64, side)
+    assert captured.data_ptr() != kept.data_ptr()
+    assert cache.workspace(4, 64, side).data_ptr() != kept.data_ptr()
+    on.capturing = set()
+    assert cache.workspace(8, 64, side) is kept
+    # the current stream captures, the call's does not
+    on.current, on.capturing = None, {None}
+    assert cache.workspace(8, 64, side) is kept
+    assert cache.workspace(8, 64) is not kept

@@ -53,3 +53,39 @@ def test_threads_on_one_stream():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("explicit", [False, True])
+def test_a_captured_call_has_a_workspace_of_its_own(explicit):
+    """A graph captured with the cache's own workspace, from the current stream or from
+    one that the call names, replayed between and next to eager calls."""
+    lengths = [3000, 0, 700]
+    cache, q, table = attention_case(73, lengths, 16, 2, 128, 16, "e4m3")
+    want = check_attention(cache, q, table, lengths)
+    args = (q, torch.from_numpy(table).cuda(), on_gpu(lengths))
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    side = torch.cuda.Stream()
+    kept = cache.workspace(3, 16, side)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    if explicit:
+        with torch.cuda.stream(side):
+            graph.capture_begin()
+        assert cache.workspace(3, 16, side).data_ptr() != kept.data_ptr()
+        cache.attend(*args, out=out, lse=lse, stream=side)
+        with torch.cuda.stream(side):
+            graph.capture_end()
+    else:
+        with torch.cuda.graph(graph, stream=side):
+            cache.attend(*args, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert cache.workspace(3, 16, side) is kept
+    for _ in range(20):
+        out.zero_()
+        lse.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        got = [cache.attend(*args, return_lse=True, stream=side) for _ in range(3)]
+        torch.cuda.synchronize()
+        for o, l in got + [(out, lse)]:
+            assert torch.equal(o, want[0]) and torch.equal(l, want[1])
