@@ -96,6 +96,9 @@ def _captured(stream, on):
         return torch.cuda.is_current_stream_capturing()
 
 
+_kept = threading.local()   # workspaces: this host thread's, by GPU and stream
+
+
 class PagedKVCache:
     """Pages of keys and values, [pages, heads, page_size, head_dim] each, as
     e4m3 codes with one fp32 scale per token and head, or in bf16."""
@@ -124,7 +127,7 @@ class PagedKVCache:
             v_scale.data_ptr() if coded else None, self.pages, self.heads, self.page_size,
             self.head_dim, dtypes[k.dtype])
         self.struct.device = index
-        self._kept = threading.local()
+        self._ws_bytes = {}       # by query heads
         self._scale = 1.0 / math.sqrt(self.head_dim)
 
     @classmethod
@@ -164,23 +167,24 @@ class PagedKVCache:
 
     def workspace(self, batch, q_heads, stream=None):
         """The attention workspace of one stream and host thread, kept for the
-        next step. Calls on different streams may overlap, so each stream has its
-        own. A call is two launches, between which another thread may enqueue its
-        own on the same stream, so each thread has its own too."""
+        next call, also of another cache. Calls on different streams may overlap, so
+        each stream has its own. A call is two launches, between which another
+        thread may enqueue its own on the same stream, so each thread has its own
+        too. A captured call's belongs to its graph."""
         on = binding._raw_stream(stream, self.struct.device)
+        need = self._ws_bytes.get(q_heads)
+        if need is None:          # (the same for every batch)
+            need = binding.moe_paged_attention_workspace_size(self.struct, 1, q_heads)
+            self._ws_bytes[q_heads] = need
         if _captured(stream, on):
-            return self._new_workspace(batch, q_heads, stream)   # the graph's own
-        kept = self._kept.__dict__
-        ws = kept.get((on, batch, q_heads))
-        if ws is None:
-            need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
-            held = [w for (o, *_), w in kept.items() if o == on and w.numel() >= need]
-            ws = held[0] if held else self._new_workspace(batch, q_heads, stream)
-            kept[on, batch, q_heads] = ws
+            return self._new_workspace(need, stream)
+        kept, key = _kept.__dict__, (self.struct.device, on)
+        ws = kept.get(key)
+        if ws is None or ws.numel() < need:
+            ws = kept[key] = self._new_workspace(need, stream)
         return ws
 
-    def _new_workspace(self, batch, q_heads, stream):
-        need = binding.moe_paged_attention_workspace_size(self.struct, batch, q_heads)
+    def _new_workspace(self, need, stream):
         return binding._empty(max(need, 1), torch.uint8, self.k.device, stream)
 
     def attend(self, q, block_table, lengths, scale=None, window=0, out=None, lse=None,

@@ -221,7 +221,7 @@ size_t moe_paged_attention_workspace_size(const moe_kv_cache* cache, int batch, 
   if (check_cache(cache) != MOE_OK || batch < 0 || batch > 65535 || q_heads < 1 ||
       q_heads % cache->heads != 0)
     return 0;
-  return paged_attention_ws_bytes(cache->heads, cache->head_dim, batch, q_heads);
+  return paged_attention_ws_bytes(cache->heads, cache->head_dim, q_heads);
 }
 
 int moe_paged_attention(const moe_kv_cache* cache, const uint16_t* q, int64_t q_stride, int batch,
@@ -239,8 +239,7 @@ int moe_paged_attention(const moe_kv_cache* cache, const uint16_t* q, int64_t q_
   if (!good_heads(q, q_stride, q_heads, cache->head_dim) || !good4(lengths) || !good16(out) ||
       (lse != nullptr && !good4(lse)))
     return MOE_ERR_INVALID_ARG;
-  if (!good16(ws) ||
-      ws_bytes < paged_attention_ws_bytes(cache->heads, cache->head_dim, batch, q_heads))
+  if (!good16(ws) || ws_bytes < paged_attention_ws_bytes(cache->heads, cache->head_dim, q_heads))
     return MOE_ERR_WORKSPACE;
   return launch_paged_attention(view_of(*cache, block_table, table_stride, max_pages), q,
                                 q_stride, batch, q_heads, lengths, scale, window, out, lse, ws,

@@ -43,7 +43,7 @@ struct CacheView {
 int launch_kv_read(const CacheView& c, const int32_t* offsets, int batch, int64_t rows,
                    uint16_t* k_out, uint16_t* v_out, cudaStream_t stream);
 
-size_t paged_attention_ws_bytes(int heads, int head_dim, int batch, int q_heads);
+size_t paged_attention_ws_bytes(int heads, int head_dim, int q_heads);
 int launch_paged_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int batch,
                            int q_heads, const int32_t* lengths, float scale, int window,
                            uint16_t* out, float* lse, void* ws, cudaStream_t stream);

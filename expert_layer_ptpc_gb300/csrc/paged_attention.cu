@@ -1162,23 +1162,22 @@ int launch(const Args& a, cudaStream_t stream) {
   return e == cudaSuccess ? 0 : -3;
 }
 
-// The workspace's parts: the joints, of as many items as there can be, then the slots'
-// statistics and rows.
+// The workspace's parts: the joints, at most one a worker, then the slots' statistics
+// and rows. The size does not depend on the batch, so that a buffer serves every batch.
 struct Parts {
   size_t joints, stats, rows;
 };
-Parts parts_of(int group, int heads, int head_dim, int batch) {
-  const size_t items = (size_t)batch * heads * chunks_of(group, kMmaRows);
+Parts parts_of(int group, int head_dim) {
   const size_t slot_rows =
       (size_t)2 * kMaxWorkers * (two_tiles_fit(group, head_dim) ? 2 : 1) * kMmaRows;
-  return {align256(std::min<size_t>(items, kMaxWorkers) * sizeof(Joint)),
-          align256(slot_rows * sizeof(float2)), slot_rows * head_dim * sizeof(float)};
+  return {align256(kMaxWorkers * sizeof(Joint)), align256(slot_rows * sizeof(float2)),
+          slot_rows * head_dim * sizeof(float)};
 }
 
 }  // namespace
 
-size_t paged_attention_ws_bytes(int heads, int head_dim, int batch, int q_heads) {
-  const Parts p = parts_of(q_heads / heads, heads, head_dim, batch);
+size_t paged_attention_ws_bytes(int heads, int head_dim, int q_heads) {
+  const Parts p = parts_of(q_heads / heads, head_dim);
   return p.joints + p.stats + p.rows;
 }
 
@@ -1203,7 +1202,7 @@ int launch_paged_attention(const CacheView& c, const uint16_t* q, int64_t q_stri
   a.window = window;
   a.out = out;
   a.lse = lse;
-  const Parts parts = parts_of(a.group, c.heads, c.head_dim, batch);
+  const Parts parts = parts_of(a.group, c.head_dim);
   uint8_t* const p = static_cast<uint8_t*>(ws);
   a.joints = reinterpret_cast<Joint*>(p);
   a.stats = reinterpret_cast<float2*>(p + parts.joints);

@@ -720,11 +720,11 @@ MOE_API int moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table,
  *   block_table as for moe_kv_read; lengths [batch] int32 (the new token's own
  *   key and value are in the cache already and counted); out [batch, q_heads,
  *   head_dim] bf16; lse [batch, q_heads] fp32 or NULL.
- *   ws: device workspace of moe_paged_attention_workspace_size bytes, 16-byte
- *   aligned, of any content; calls in flight at once need workspaces of their
- *   own. A call is two launches: calls that several host threads make on one
- *   stream can be enqueued between one another's, and count as in flight at
- *   once.
+ *   ws: device workspace of moe_paged_attention_workspace_size bytes (the same
+ *   for every batch), 16-byte aligned, of any content; calls in flight at once
+ *   need workspaces of their own. A call is two launches: calls that several
+ *   host threads make on one stream can be enqueued between one another's, and
+ *   count as in flight at once.
  *   Sums, maxima and accumulators are fp32; results do not depend on timing.
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
  *         pointers, q_heads not a multiple of heads, scale not finite, batch

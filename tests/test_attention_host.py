@@ -279,3 +279,30 @@ def test_a_captured_call_does_not_use_the_kept_workspace(streams, monkeypatch):
     on.current, on.capturing = None, {None}
     assert cache.workspace(8, 64, side) is kept
     assert cache.workspace(8, 64) is not kept
+
+
+def test_growing_batches_keep_one_workspace(streams):
+    """Not one of each size, for each cache and as long as it lives."""
+    caches = [cache_of(), cache_of(heads=8), cache_of()]
+    kept = {id(c.workspace(batch, 64)) for batch in (1, 2, 3, 16, 100, 128, 1000, 65535)
+            for c in caches}
+    assert len(kept) == 1
+
+
+def test_a_larger_workspace_takes_the_place_of_a_smaller(streams):
+    cache, wide = cache_of(), cache_of(d=256)
+    first = cache.workspace(4, 64)
+    larger = wide.workspace(4, 64)
+    size = binding.moe_paged_attention_workspace_size
+    assert larger.numel() >= size(wide.struct, 4, 64) > first.numel() >= size(cache.struct, 4, 64)
+    assert cache.workspace(4, 64) is larger and wide.workspace(9, 32) is larger
+    assert cache.workspace(4, 64, Side()) is not larger
+
+
+def test_the_workspace_size_is_the_same_for_every_batch(streams):
+    for d in (64, 128, 256):
+        for q_heads in (4, 64, 128):
+            sizes = {binding.moe_paged_attention_workspace_size(cache_of(d=d).struct, b, q_heads)
+                     for b in (0, 1, 5, 100, 65535)}
+            assert len(sizes) == 1 and sizes.pop() > 0
+    assert binding.moe_paged_attention_workspace_size(cache_of().struct, 65536, 64) == 0

@@ -89,3 +89,25 @@ def test_a_captured_call_has_a_workspace_of_its_own(explicit):
         torch.cuda.synchronize()
         for o, l in got + [(out, lse)]:
             assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+def test_caches_share_a_workspace_that_growing_batches_keep():
+    """One buffer serves caches of other shapes and every batch size, with the results of
+    a buffer of their own."""
+    shapes = [([3000, 100], 16, 2, 128, "e4m3"), ([2000, 0, 900], 8, 2, 256, "bf16"),
+              ([700] * 30, 40, 2, 64, "e4m3"), ([1500], 4, 4, 128, "bf16")]
+    cases = [(attention_case(80 + i, n, hq, hk, d, 16, kind), n)
+             for i, (n, hq, hk, d, kind) in enumerate(shapes)]
+    want = [check_attention(*case, n) for case, n in cases]
+    buffers = {(c.workspace(1, q.shape[1]).data_ptr()) for (c, q, _), _ in cases}
+    assert len(buffers) == 1
+    before = torch.cuda.memory_allocated()
+    for (cache, q, _), _ in cases:
+        for batch in range(1, 200, 7):
+            cache.workspace(batch, q.shape[1])
+    assert torch.cuda.memory_allocated() == before
+    # one after the other on one stream, without a wait between them
+    got = [c.attend(q, torch.from_numpy(t).cuda(), on_gpu(n), return_lse=True)
+           for _ in range(3) for (c, q, t), n in cases]
+    for (out, lse), (o, l) in zip(got, want * 3):
+        assert torch.equal(out, o) and torch.equal(lse, l)
