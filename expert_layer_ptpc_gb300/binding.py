@@ -620,6 +620,9 @@ def moe_workspace_status(ws, stream=None):
 # structures (expert_layer_ptpc_gb300.attention builds them from tensors). A call's
 # tensors all lie on the current GPU.
 # ---------------------------------------------------------------------------
+_INT_MAX = 2 ** 31 - 1   # ctypes takes the low bits of a larger number without a word
+
+
 def _gpu_of(t, name, *structs):
     """The index of t's GPU. The library launches on the current GPU, so that it
     has to be that one, and the one that the call's plan and cache lie on."""
@@ -672,6 +675,8 @@ def _need_heads(t, heads, head_dim, name, index):
     n, h, d = t.shape
     if h != heads or d != head_dim:
         raise ValueError(f"{name} must be [T, {heads}, {head_dim}], got {tuple(t.shape)}")
+    if n > _INT_MAX:
+        raise ValueError(f"{name} must have at most {_INT_MAX} tokens, got {n}")
     stride, sh, sd = t.stride()
     if (sd != 1 and d != 1) or (sh != d and h != 1):
         raise ValueError(f"{name}'s heads must be contiguous within a token")
@@ -701,6 +706,9 @@ def _need_table(table, batch, index):
     n, pages = table.shape
     if n != batch:
         raise ValueError(f"block_table must have {batch} rows, got {n}")
+    if n > _INT_MAX or pages > _INT_MAX:
+        raise ValueError(f"block_table must have at most {_INT_MAX} rows and columns, got "
+                         f"{tuple(table.shape)}")
     stride, inner = table.stride()
     if inner != 1 and pages > 1:
         raise ValueError("block_table's rows must be contiguous")
@@ -823,6 +831,8 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
     log of the sums. ws: a contiguous tensor of at least
     moe_paged_attention_workspace_size bytes (None: a new one)."""
     batch, hq, d = q.shape
+    if not -_INT_MAX <= window <= _INT_MAX:
+        raise ValueError(f"window must be at most {_INT_MAX}, got {window}")
     index = _gpu_of(q, "q", cache)
     q_stride = _need_heads(q, hq, cache.head_dim, "q", index)
     stride, pages = _need_table(block_table, batch, index)

@@ -3,6 +3,7 @@ tensors: what is refused before the library is called, and which workspace a
 call gets. No call here reaches a kernel."""
 
 import contextlib
+import math
 import threading
 
 import pytest
@@ -306,3 +307,55 @@ def test_the_workspace_size_is_the_same_for_every_batch(streams):
                      for b in (0, 1, 5, 100, 65535)}
             assert len(sizes) == 1 and sizes.pop() > 0
     assert binding.moe_paged_attention_workspace_size(cache_of().struct, 65536, 64) == 0
+
+
+# ---------------------------------------------------------------------------
+# numbers that the library's 32-bit arguments do not hold
+# ---------------------------------------------------------------------------
+def vast(t, *shape):
+    """t with a shape (contiguous) that no host memory would hold."""
+    class Vast(OnGpu):
+        def numel(self):
+            return math.prod(shape)
+
+        def stride(self):
+            return tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
+    made = Vast(t.t)
+    made.shape = torch.Size(shape)
+    return made
+
+
+def test_a_window_past_32_bits_is_refused(calls):
+    attend(window=2 ** 31 - 1)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 32 + 1):   # ctypes would take 0, 5, 1
+        with pytest.raises(ValueError, match="window"):
+            attend(window=window)
+    assert len(calls.made) == 1
+
+
+def test_a_table_past_32_bits_is_refused(calls):
+    for pages in (2 ** 31, 2 ** 32 + 4):
+        with pytest.raises(ValueError, match="block_table"):
+            attend(block_table=vast(int32(1), 3, pages))
+        with pytest.raises(ValueError, match="block_table"):
+            read(block_table=vast(int32(1), 3, pages))
+    assert not calls.made
+
+
+@pytest.mark.parametrize("T", [2 ** 31, 2 ** 32 + 3])
+def test_more_tokens_than_32_bits_are_refused(calls, T):
+    q, k, s = (vast(bf16(1), T, h, 64) for h in (8, 2, 2))
+    p, slots = vast(int32(1), 1, T), vast(int32(1), T)
+    for call in (lambda: rotate(q=q, q_out=q, k=None, k_out=None, positions=p),
+                 lambda: write(k=k, v=s, slots=slots),
+                 lambda: write_rotary(q=q, k=k, v=s, q_out=q, positions=p, slots=slots)):
+        with pytest.raises(ValueError, match="tokens"):
+            call()
+    assert not calls.made
+
+
+def test_more_contexts_to_read_than_32_bits_are_refused(calls):
+    n = 2 ** 32 + 3
+    with pytest.raises(ValueError, match="block_table|contexts"):
+        read(offsets=vast(int32(1), n + 1), block_table=vast(int32(1), n, 4))
+    assert not calls.made
