@@ -9,10 +9,14 @@ frequencies, the cache's tensors) and call the library entry points of
 
 import math
 import threading
+from fractions import Fraction
 
 import torch
 
 from . import binding
+
+
+_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494")
 
 
 def pair_axes(sections, woven=False):
@@ -69,9 +73,9 @@ class Rotary:
         for f in freq.tolist():
             if not math.isfinite(f):
                 raise ValueError("inv_freq must be finite")
-            # a fraction of a turn per position in units of 2^-64; the scaling
-            # by 2^64 is exact, so the one rounding is that of the quotient
-            n = round(f / (2.0 * math.pi) * 2.0 ** 64) % (1 << 64)
+            # a fraction of a turn per position in units of 2^-64, rounded once
+            # (a double's quotient would be 2^-24 turns off after 2^31 positions)
+            n = round(Fraction(f) * 2 ** 64 / _TWO_PI) % (1 << 64)
             turns.append(n - (1 << 64) if n >= 1 << 63 else n)
         self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
         self.pair_axis = axis.to(torch.uint8).to(device)

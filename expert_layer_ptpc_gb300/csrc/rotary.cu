@@ -9,7 +9,9 @@
 // The angle. A frequency is kept as a 64-bit fraction of a turn, so p * turns
 // wraps modulo 2^64 exactly as the angle wraps modulo a turn: the integer
 // product is the reduced angle, for any 32-bit position, without fp64 or an
-// argument reduction. Its upper 32 bits, as a signed fraction, go to sincospif.
+// argument reduction. Its upper 32 bits, as a signed fraction in [-1/2, 1/2) turns,
+// are rounded to fp32 (by at most 2^-26 turns, a step of fp32 below 1/2 being 2^-25)
+// and go to sincospif.
 //
 // Every element is read once and written once: the kernel is bound by memory
 // (4 bytes moved per element of q against 3 flops). A warp takes one token and

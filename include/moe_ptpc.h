@@ -608,8 +608,9 @@ MOE_API int moe_grouped_gemm_scaled(int scale_kind, const uint8_t* A, const floa
  * in fp32, rounded once to bf16; elements from rot_dim on are copied. turns
  * holds each frequency as a fraction of a turn per position, in units of
  * 2^-64: turns[i] = round(inv_freq[i] / (2 pi) * 2^64) mod 2^64, so that the
- * angle of any 32-bit position is exact to 2^-31 turns. The inverse is the
- * transpose of the rotation, hence also its gradient.
+ * angle of any 32-bit position is reduced to within 2^-31 turns; it is then
+ * rounded once to fp32 (by at most 2^-26 turns). The inverse is the transpose
+ * of the rotation, hence also its gradient.
  */
 typedef struct moe_rotary_plan {
   const uint64_t* turns;     /* [rot_dim / 2], device                        */

@@ -5,6 +5,7 @@ call gets. No call here reaches a kernel."""
 import contextlib
 import math
 import threading
+from fractions import Fraction
 
 import pytest
 import torch
@@ -359,3 +360,31 @@ def test_more_contexts_to_read_than_32_bits_are_refused(calls):
     with pytest.raises(ValueError, match="block_table|contexts"):
         read(offsets=vast(int32(1), n + 1), block_table=vast(int32(1), n, 4))
     assert not calls.made
+
+
+# ---------------------------------------------------------------------------
+# frequencies as fractions of a turn
+# ---------------------------------------------------------------------------
+def two_pi(bits=400):
+    """2 pi by Machin's formula, 8 (4 atan(1/5) - atan(1/239))."""
+    def atan_inverse(n):
+        power, total, i = (1 << bits) // n, 0, 0
+        while power:
+            total += (-1) ** i * (power // (2 * i + 1))
+            power //= n * n
+            i += 1
+        return total
+    return Fraction(8 * (4 * atan_inverse(5) - atan_inverse(239)), 1 << bits)
+
+
+@pytest.mark.parametrize("base", [10000.0, 1000000.0, 5.0, 0.01])
+def test_a_turn_is_exact_to_2_31_for_every_position(base):
+    """The nearest multiple of 2^-64 turns to the frequency as it is given, so that 2^31
+    positions are off by at most 2^31 halves of that."""
+    freq = attention.frequencies(64, base)
+    turns = attention.Rotary(freq, device="cpu").turns.tolist()
+    circle = two_pi()
+    for f, n in zip(freq.tolist(), turns):
+        for p in (1, 1000003, 2 ** 31 - 1, -2 ** 31):
+            off = (Fraction(p * n, 2 ** 64) - p * Fraction(f) / circle) % 1
+            assert min(off, 1 - off) <= abs(p) * Fraction(1, 2 ** 65), (p, f)
