@@ -70,7 +70,10 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 // nearest and q = v y within a unit in the last place of v / s, q + y (v - s q)
 // with fused products is v / s rounded to nearest (Markstein 1990), where nothing
 // under- or overflows. Here s >= 2^-49 and y is normal, and quotients below
-// 2^-10 become the code 0 whatever their last bits.
+// 2^-10 become the code 0 whatever their last bits. The product v y alone can be
+// up to 1.5 units off, which the theorem does not cover; so it was tried for all 2^23
+// mantissas of s, each with the 9 v around each of the 16 ties between codes and 100
+// others: 2 billion quotients, all rounded to nearest.
 __device__ __forceinline__ float quotient(float v, float s, float y) {
   const float q = v * y;
   return fmaf(-fmaf(s, q, -v), y, q);   // (this order keeps the sign of a zero)
