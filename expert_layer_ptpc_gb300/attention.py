@@ -91,15 +91,6 @@ class Rotary:
         return binding.moe_rotary(self.plan, positions, q, k, inverse, q_out, k_out, stream)
 
 
-def _captured(stream, on):
-    """Whether a graph is being captured from `stream` (None: the current one),
-    whose handle is `on`. (Making a stream current to ask costs some microseconds.)"""
-    if stream is None or on == torch._C._cuda_getCurrentRawStream(stream.device_index):
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
-        return torch.cuda.is_current_stream_capturing()
-
-
 _kept = threading.local()   # workspaces: this host thread's, by GPU and stream
 
 
@@ -116,6 +107,7 @@ class PagedKVCache:
         coded = k.dtype == torch.uint8
         if coded != (k_scale is not None) or coded != (v_scale is not None):
             raise ValueError("an e4m3 cache has scales for k and v, a bf16 cache has none")
+        binding._need(k, k.dtype, "k")
         index = k.get_device()
         for t, n in ((k, "k"), (v, "v")):
             binding._need_on(t, k.dtype, n, index)
@@ -175,14 +167,15 @@ class PagedKVCache:
         each stream has its own. A call is two launches, between which another
         thread may enqueue its own on the same stream, so each thread has its own
         too. A captured call's belongs to its graph."""
-        on = binding._raw_stream(stream, self.struct.device)
+        index = self.struct.device
+        on = binding._raw_stream(stream, index)
         need = self._ws_bytes.get(q_heads)
         if need is None:          # (the same for every batch)
             need = binding.moe_paged_attention_workspace_size(self.struct, 1, q_heads)
             self._ws_bytes[q_heads] = need
-        if _captured(stream, on):
+        if binding._capturing(stream, index):
             return self._new_workspace(need, stream)
-        kept, key = _kept.__dict__, (self.struct.device, on)
+        kept, key = _kept.__dict__, (index, on)
         ws = kept.get(key)
         if ws is None or ws.numel() < need:
             ws = kept[key] = self._new_workspace(need, stream)

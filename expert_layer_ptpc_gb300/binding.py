@@ -626,21 +626,21 @@ _INT_MAX = 2 ** 31 - 1   # ctypes takes the low bits of a larger number without 
 def _gpu_of(t, name, *structs):
     """The index of t's GPU. The library launches on the current GPU, so that it
     has to be that one, and the one that the call's plan and cache lie on."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if index != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current GPU, is on GPU {index}")
     for s in structs:
-        if s.device is not None and s.device != index:
+        if s.device != index and s.device is not None:
             what = "cache" if isinstance(s, moe_kv_cache) else "plan"
             raise ValueError(f"{name} is on GPU {index}, the {what} on GPU {s.device}")
     return index
 
 
 def _need_on(t, dtype, name, index):
-    _need(t, dtype, name)
-    if t.get_device() != index:
+    if t.get_device() != index or t.dtype != dtype or not t.is_contiguous():
+        _need(t, dtype, name)
         raise ValueError(f"{name} must be on GPU {index}")
 
 
@@ -653,6 +653,19 @@ def _raw_stream(stream, index):
             raise ValueError(f"the stream must be one of GPU {index}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _capturing(stream, index):
+    """Whether a graph is being captured from `stream` (None: the current one).
+    (Making the stream current by hand: torch.cuda.stream would cost 8 us.)"""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    before = torch._C._cuda_getCurrentStream(index)
+    torch._C._cuda_setStream(stream.stream_id, stream.device_index, stream.device_type)
+    try:
+        return torch.cuda.is_current_stream_capturing()
+    finally:
+        torch._C._cuda_setStream(*before)
 
 
 def _empty(shape, dtype, device, stream):
@@ -859,8 +872,8 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
     status = (_lib or load_library()).moe_paged_attention(
         ctypes.byref(cache), q.data_ptr(), q_stride, batch, hq, block_table.data_ptr(), stride,
         pages, lengths.data_ptr(), scale, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _raw_stream(stream, index))
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+        _raw_stream(stream, index))
     if status:
         raise MoeError("moe_paged_attention", status)
     return (out, lse) if return_lse else out

@@ -250,9 +250,16 @@ class CurrentStream:
         self.current, self.capturing = None, set()
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream",
                             lambda index: self.current.cuda_stream if self.current else 5)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentStream",
+                            lambda index: (self.current.stream_id if self.current else 0, 0, 1))
+        monkeypatch.setattr(torch._C, "_cuda_setStream", self.switch)
         monkeypatch.setattr(torch.cuda, "stream", self.switched)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
                             lambda: self.current in self.capturing)
+
+    def switch(self, stream_id, device_index, device_type):
+        assert (device_index, device_type) == (0, 1)
+        self.current = {Side.stream_id: Side, 0: None}[stream_id]
 
     @contextlib.contextmanager
     def switched(self, stream):
@@ -262,13 +269,13 @@ class CurrentStream:
 
 
 class Side:
-    cuda_stream, device_index = 77, 0
+    cuda_stream, stream_id, device_index, device_type = 77, 9, 0, 1
 
 
 def test_a_captured_call_does_not_use_the_kept_workspace(streams, monkeypatch):
     """A graph that holds the kept workspace would write to it at any later time. The
     stream that counts is the call's, not the current one."""
-    on, side, cache = CurrentStream(monkeypatch), Side(), cache_of()
+    on, side, cache = CurrentStream(monkeypatch), Side, cache_of()
     kept = cache.workspace(8, 64, side)
     assert cache.workspace(8, 64, side) is kept
     on.capturing = {side}
@@ -281,6 +288,7 @@ def test_a_captured_call_does_not_use_the_kept_workspace(streams, monkeypatch):
     on.current, on.capturing = None, {None}
     assert cache.workspace(8, 64, side) is kept
     assert cache.workspace(8, 64) is not kept
+    assert on.current is None
 
 
 def test_growing_batches_keep_one_workspace(streams):
@@ -291,14 +299,15 @@ def test_growing_batches_keep_one_workspace(streams):
     assert len(kept) == 1
 
 
-def test_a_larger_workspace_takes_the_place_of_a_smaller(streams):
+def test_a_larger_workspace_takes_the_place_of_a_smaller(streams, monkeypatch):
     cache, wide = cache_of(), cache_of(d=256)
     first = cache.workspace(4, 64)
     larger = wide.workspace(4, 64)
     size = binding.moe_paged_attention_workspace_size
     assert larger.numel() >= size(wide.struct, 4, 64) > first.numel() >= size(cache.struct, 4, 64)
     assert cache.workspace(4, 64) is larger and wide.workspace(9, 32) is larger
-    assert cache.workspace(4, 64, Side()) is not larger
+    CurrentStream(monkeypatch)
+    assert cache.workspace(4, 64, Side) is not larger
 
 
 def test_the_workspace_size_is_the_same_for_every_batch(streams):

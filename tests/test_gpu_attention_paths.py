@@ -181,7 +181,7 @@ def test_attention_q_of_many_sizes(low):
     top = np.exp2(rng.integers(-20, 20, size=(2, 8, 1)).astype(np.float64))
     q = torch.from_numpy(x * top).to(torch.bfloat16).cuda()
     kc, vc, ks, vs = host(cache)
-    for scale in np.unique(top):                       # one head size at a time counts
+    for scale in np.unique(top):       # heads of larger q are beyond any bound here
         s = 2.0 ** -low / scale / 32
         got, lse = cache.attend(q, torch.from_numpy(table).cuda(), on_gpu(lengths), scale=s,
                                 return_lse=True)
@@ -190,9 +190,9 @@ def test_attention_q_of_many_sizes(low):
         most = np.abs(oracle.e4m3_decode(kc) * ks.astype(np.float64)[..., None]).sum(-1).max()
         lost = s * 2.0 ** -25 * top[..., 0] * most if low < -17 else 0.0
         n = np.array(lengths)[:, None]
-        e = (2 * (128 + 8) + 4) * U32 * reach + lost
-        fine = np.broadcast_to(top[..., 0] <= scale, e.shape)
-        rel = 2 * e * np.exp(np.minimum(2 * e, 700)) + 2.0 ** -11 + 2 * n * U32
+        fine = top[..., 0] <= scale
+        e = np.where(fine, (2 * (128 + 8) + 4) * U32 * reach + lost, 0.0)
+        rel = 2 * e * np.exp(2 * e) + 2.0 ** -11 + 2 * n * U32
         tol = HALF_BF16 * np.abs(ref) + rel[..., None] * spread
         tol += 2.0 ** -32 * n[..., None] * np.abs(vs).max() * 448     # faint weights, see above
         assert np.all((np.abs(values(got) - ref) <= tol)[fine])
