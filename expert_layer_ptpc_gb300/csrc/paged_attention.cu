@@ -1036,7 +1036,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, int
   pdl_wait();
   if (none) return;
   const Joint j = a.joints[blockIdx.x];
-  if (j.pieces < 2) return;
+  // (lengths that changed under the kernels can leave an item's joint unwritten: what
+  // the workspace held must not lead out of it or of the outputs)
+  if (j.pieces < 2 || (uint32_t)j.item >= (uint32_t)(a.batch * items) || j.first < 0 ||
+      j.first > kMaxWorkers - j.pieces)
+    return;
   const int b = j.item / items, item = j.item - b * items;
   const int kv = item / a.chunks;
   const int head0 = kv * a.group + (item - kv * a.chunks) * kRows;

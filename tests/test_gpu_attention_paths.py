@@ -14,6 +14,7 @@ import pytest
 import torch
 
 import oracle
+from expert_layer_ptpc_gb300 import binding
 from tests import test_gpu_attention as base
 from tests.gpu_helpers import U32, ensure_library, require_gpu
 from tests.test_gpu_attention import (HALF_BF16, assert_rotated, attention_case,
@@ -343,6 +344,35 @@ def test_caches_share_a_workspace_that_growing_batches_keep():
            for _ in range(3) for (c, q, t), n in cases]
     for (out, lse), (o, l) in zip(got, want * 3):
         assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+def test_lengths_that_change_under_a_call():
+    """What a call then gives is not defined, but it stays in its buffers (joints that
+    nobody wrote hold what the workspace held), and the next call is right."""
+    lengths = [4000, 0, 2500, 700]
+    cache, q, table = attention_case(97, lengths, 16, 2, 128, 16, "e4m3")
+    want = check_attention(cache, q, table, lengths)
+    t, n, full = torch.from_numpy(table).cuda(), on_gpu(lengths), on_gpu(lengths)
+    need = binding.moe_paged_attention_workspace_size(cache.struct, 4, 16)
+    ws = torch.full((need + 512,), 0x01, dtype=torch.uint8, device="cuda")
+    outs = torch.full((3, 4, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    for _ in range(200):
+        torch.cuda.synchronize()
+        ws[256:256 + need] = 0x01
+        n.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                n.copy_(full)
+                n.zero_()
+            n.copy_(full)
+        cache.attend(q, t, n, out=outs[1], ws=ws[256:256 + need])
+    torch.cuda.synchronize()
+    assert bool((ws[:256] == 0x01).all()) and bool((ws[256 + need:] == 0x01).all())
+    assert bool((outs[0] == 7).all()) and bool((outs[2] == 7).all())
+    out, lse = cache.attend(q, t, n, return_lse=True, ws=ws[256:256 + need])
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 def test_streams_that_overlap():
