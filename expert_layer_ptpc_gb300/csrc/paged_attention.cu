@@ -11,8 +11,13 @@
 // goes into its weight's exponent: the weights stay in fp16's range whatever
 // the scales, and the codes go to the tensor cores unscaled. M is set 7 below a
 // tile's maximum, and moves only when a later one passes it by 15 (fp16 ends at
-// 2^16), so that the accumulators are rarely rescaled; weights that are rounded to
-// zero are 2^-32 of the largest and less. Sums and accumulators are fp32.
+// 2^16), so that the accumulators are rarely rescaled. A weight's rounding is off by up
+// to 2^-11 of it, or by 2^-32 of the largest weight where that is more: weights below
+// that are rounded to zero, and elements whose codes are zero in all heavier tokens
+// lose what they would have added. The sum takes the weights unrounded; in it a weight
+// vanishes below 2^-133 of the largest (fp32), so that tokens of equal p_j all
+// count as long as their value scales are within 2^100 of one another. Sums
+// and accumulators are fp32.
 //
 // The work is bound by the cache's bytes: 4 D flops a token and query head
 // against 2 D + 8 bytes a token and kv head, 31 flop/byte with 16 query heads a
@@ -25,7 +30,7 @@
 // * the up to 16 query heads of a kv head are the rows of one m16n8k16 tensor
 //   core tile; in larger calls up to 32 of 64 or 128 elements are two tiles, for
 //   which a token is copied and converted once (64 contexts of 8000 tokens, 80 heads on
-//   4, 128 elements: e4m3 126 us, bf16 177; as two work items 180 and 319). More heads
+//   4, 128 elements: e4m3 124 us, bf16 172; as two work items 180 and 319). More heads
 //   a kv head are further work items, which find the tokens in L2.
 // * each warp has tiles of 16 or 32 tokens of its own in flight (cp.async),
 //   kStages deep, with barriers of the warp only.
@@ -35,16 +40,17 @@
 //   is free too: a lane's operands of a value row are 16 neighbouring bytes,
 //   byte j of them belongs to output tile j.
 // e4m3 operands are converted to fp16, which holds every code. q goes from
-// bf16 to fp16 scaled by a power of two per head; only elements under 2^-24 of
-// the head's largest lose bits. The weights are rounded to fp16 (11 bits). With
+// bf16 to fp16 scaled by a power of two per head, which brings the head's largest
+// element into [1, 2): elements under 2^-17 lose bits of their 8 (fp16's smallest step
+// is 2^-24), and are off by up to 2^-25. The weights are rounded to fp16 (11 bits). With
 // a bf16 cache the operands are bf16, and the weights go in as the sum of two
 // bf16 numbers (16 bits).
 //
 // GB300: 128 contexts of 0 to 16384 tokens, 64 query heads on 4 of 128, e4m3 (1.11 GB):
-// 182 us, 6.1 TB/s of the copy's 6.8; one context of 262143 tokens (277 MB): 54 us, of
+// 183 us, 6.1 TB/s of the copy's 6.8; one context of 262143 tokens (277 MB): 54 us, of
 // which 40 are the tiles at the copy's rate and the rest the first loads, the last CTA
 // and the joining kernel. 8 warps an SM of up to 255 registers; the tensor cores are 30%
-// busy, and the issue slots 41%.
+// busy, and the issue slots 40%.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -144,9 +150,12 @@ struct Shape {
   static constexpr int kWarpBytes = kStages * kStageBytes + kScaleBytes;
   static constexpr int kJoinBytes = kRows * D * 4;         // an accumulator tile
   // q's operands: 64 registers with 256 elements or two tiles of 128, next to 128 of
-  // accumulators. There they are in shared memory, and fetched when a segment begins
-  // instead of before (64 contexts of 8000 tokens, 16 heads on 2 of 256 elements: 101 us,
-  // 137 with them in registers; two tiles of 64: 82 us, 87).
+  // accumulators. For two tiles and for e4m3 heads of 256 they are in shared memory, and
+  // fetched when a segment begins instead of before (64 contexts of 8000 tokens, 16 heads
+  // on 2 of 256 elements, e4m3: 101 us, 137 with them in registers; two tiles of 64: 82
+  // us, 87). bf16 heads of 256 keep them in registers: their stages and joins take 224 KB,
+  // and q's 8 do not fit beside them; the kernel moves 6.3 TB/s all the same. Kernels of 256 elements and
+  // of two tiles of 128 spill 44 to 164 bytes at 255 registers; the others none.
   static constexpr bool kSharedQ = M == 2 || (E4M3 && D == 256);
   static constexpr int kQBytes = kSharedQ ? M * (D / 16) * 512 : 0;
   static constexpr int kSmemBytes = kWarps * kWarpBytes + 2 * kJoinBytes + kQBytes;

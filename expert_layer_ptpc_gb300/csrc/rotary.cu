@@ -21,8 +21,10 @@
 // half a region apart, so that the lanes' 16-byte accesses are contiguous; the
 // next units are in flight while one is used. A cache head is 4, 8 or 16 units,
 // hence that many neighbouring lanes, and its row maximum is a shuffle.
-// GB300, 8192 tokens of 64 + 4 heads of 128: the rotation 44 us (6.5 TB/s of the copy's
-// 6.8), with k and v quantised into the cache 46 us (6.3 TB/s).
+// GB300, 8192 tokens of 64 + 4 heads of 128: the rotation 44.7 us (6.4 TB/s of the copy's
+// 6.8), with k and v quantised into the cache 47.2 us (6.2 TB/s). 16001 tokens' keys and
+// values alone, 8 heads: 19.9 us into an e4m3 cache (4.4 TB/s), 18.5 into a bf16 one
+// (6.3 TB/s).
 #include <algorithm>
 
 #include "attention.h"
@@ -38,8 +40,9 @@ constexpr int kUnit = 16;     // elements of a lane
 // Blocks of an SM: 32 warps of 64 registers a lane. A lane's units travel through
 // shared memory (cp.async, each lane reads back its own), so that more of them are
 // in flight than registers would hold. (GB300, 8192 tokens of 64 + 4 heads of 128, the
-// rotation and the fused write: 44.1 and 46.5 us with three units in flight; in
-// registers, two and one, 45.9 and 51.8, and more of them spill.)
+// rotation and the fused write, one after the other in one run: 44.1 and 46.5 us with
+// three units in flight; in registers, two and one, 45.9 and 51.8, and more of them spill.
+// As it is, the bf16 caches' fused writes spill 16 bytes, the others nothing.)
 constexpr int kBlocks = 4;
 constexpr int kAhead = 3;     // units of a lane in flight
 
@@ -240,7 +243,7 @@ int launch_rotary(const RotaryArgs& a, int sink, bool neighbours, cudaStream_t s
   const int at_once = 32 / (a.head_dim / kUnit);
   const int steps = (heads + at_once - 1) / at_once;   // of a warp that has all heads
   // Steps of a warp: so many that the work fills the GPU three times over (152 SMs
-  // with 32 warps each; the rotation above takes 44.1 us, 45.8 with all 17 steps of a
+  // with 32 warps each; the rotation above took 44.1 us, 45.8 with all 17 steps of a
   // token in one warp, the last warps being few); but up to 8, as long as it is
   // filled once (4099 tokens of 18 heads of 256 take 14.1 us in steps of 5 and 4, 16.6
   // in steps of 2: each warp works out the cosines anew); at least one.

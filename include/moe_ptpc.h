@@ -644,7 +644,8 @@ MOE_API int moe_rotary(const moe_rotary_plan* plan, const int32_t* positions, in
  *   k, v [pages, heads, page_size, head_dim], e4m3 codes or bf16;
  *   k_scale, v_scale [pages, heads, page_size] fp32 for e4m3, else NULL:
  *   one scale per token and head (the PTPC quantiser of moe_quant_ptpc on the
- *   head's row), value = code * scale.
+ *   head's row), value = code * scale. Scales are positive, as that quantiser
+ *   makes them.
  * head_dim is 64, 128 or 256; page_size a power of two <= 1024; the whole
  * cache has fewer than 2^31 slots and fewer than 2^32 - 1 rows (pages *
  * heads * page_size). Entry points return MOE_ERR_INVALID_ARG for null,
@@ -727,11 +728,22 @@ MOE_API int moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table,
  *   host threads make on one stream can be enqueued between one another's, and
  *   count as in flight at once.
  *   Sums, maxima and accumulators are fp32; results do not depend on timing.
+ *   What the tensor cores multiply has fewer bits:
+ *   - e4m3 cache: codes exactly, in fp16. q in fp16, with its head's largest
+ *     element scaled by a power of two into [1, 2): exact down to 2^-17 there,
+ *     below that off by up to 2^-25. The weights p_j * v_scale_j in fp16: off by
+ *     up to 2^-11 of each, or 2^-32 of the head's largest where that is more
+ *     (weights below that are zero). Value scales of a context that are more
+ *     than 2^100 apart can drop out of the sum; scales below 2^-100 count as
+ *     that.
+ *   - bf16 cache: q, k and v exactly; each weight as the sum of two bf16 numbers
+ *     (16 bits).
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
  *         pointers, q_heads not a multiple of heads, scale not finite, batch
- *         < 0, max_pages < 0), MOE_ERR_UNSUPPORTED (batch > 65535, or tables
- *         of more than about 2^31 units of 64 tokens and 16 to 32 query
- *         heads in all), MOE_ERR_WORKSPACE. batch == 0 is a no-op.
+ *         < 0, max_pages < 0, window < 0), MOE_ERR_UNSUPPORTED (batch > 65535,
+ *         q_heads > 65535, or tables of more than about 2^31 units of 64
+ *         tokens and 16 to 32 query heads in all), MOE_ERR_WORKSPACE. batch ==
+ *         0 is a no-op.
  */
 MOE_API size_t moe_paged_attention_workspace_size(const moe_kv_cache* cache, int batch,
                                                   int q_heads);

@@ -395,3 +395,19 @@ def test_streams_that_overlap():
     for i in range(2):
         for out, lse in got[i]:
             assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.parametrize("most", [24, 45])
+def test_attention_value_scales_far_apart(most):
+    """Scales of value rows from 2^-most to 2^most of the usual: each row's scale goes into
+    its weight's exponent and out of the sum again."""
+    lengths = [777, 60, 0, 1]
+    cache, q, table = attention_case(98, lengths, 16, 2, 128, 16, "e4m3", 1.0, spread=0.3)
+    cache.v_scale.mul_(torch.exp2(torch.randint(-most, most + 1, cache.v_scale.shape,
+                                                device="cuda").float()))
+    check(cache, q, table, lengths)
+    # rows of zeros among them, as the cache write leaves them: the smallest scale
+    zeros = torch.rand(cache.v_scale.shape, device="cuda") < 0.3
+    cache.v[zeros] = 0
+    cache.v_scale[zeros] = float(np.float32(1e-12) / np.float32(448))
+    check(cache, q, table, lengths)
