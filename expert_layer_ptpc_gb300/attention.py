@@ -16,7 +16,8 @@ import torch
 from . import binding
 
 
-_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494")
+_PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494")
+_RADIAN = round(2 ** 256 / (2 * _PI))   # in units of 2^-256 turns, to some 200 bits
 
 
 def pair_axes(sections, woven=False):
@@ -75,7 +76,9 @@ class Rotary:
                 raise ValueError("inv_freq must be finite")
             # a fraction of a turn per position in units of 2^-64, rounded once
             # (a double's quotient would be 2^-24 turns off after 2^31 positions)
-            n = round(Fraction(f) * 2 ** 64 / _TWO_PI) % (1 << 64)
+            top, below = f.as_integer_ratio()
+            shift = below.bit_length() - 1 + 256 - 64          # below = 2^(bits - 1)
+            n = (((top * _RADIAN >> (shift - 1)) + 1) >> 1) % (1 << 64)
             turns.append(n - (1 << 64) if n >= 1 << 63 else n)
         self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
         self.pair_axis = axis.to(torch.uint8).to(device)
