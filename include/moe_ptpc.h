@@ -701,7 +701,8 @@ MOE_API int moe_rotary_kv_write(const moe_rotary_plan* plan, const int32_t* posi
  *   offsets[batch] on, tokens past max_pages and pages outside [0, pages)
  *   read as zeros. Asynchronous on lengths: `rows` is the outputs' size.
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
- *         pointers, batch < 1, max_pages < 0, rows < 0). rows == 0 is a no-op.
+ *         pointers, batch < 1, max_pages < 0, table_stride < max_pages, rows <
+ *         0), MOE_ERR_UNSUPPORTED (rows >= 2^31). rows == 0 is a no-op.
  */
 MOE_API int moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table,
                         int64_t table_stride, int max_pages, const int32_t* offsets,
@@ -740,10 +741,10 @@ MOE_API int moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table,
  *     (16 bits).
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
  *         pointers, q_heads not a multiple of heads, scale not finite, batch
- *         < 0, max_pages < 0, window < 0), MOE_ERR_UNSUPPORTED (batch > 65535,
- *         q_heads > 65535, or tables of more than about 2^31 units of 64
- *         tokens and 16 to 32 query heads in all), MOE_ERR_WORKSPACE. batch ==
- *         0 is a no-op.
+ *         < 0, max_pages < 0, table_stride < max_pages, window < 0),
+ *         MOE_ERR_UNSUPPORTED (batch > 65535, q_heads > 65535, or tables of
+ *         more than about 2^31 units of 64 tokens and 16 to 32 query heads in
+ *         all), MOE_ERR_WORKSPACE. batch == 0 is a no-op.
  */
 MOE_API size_t moe_paged_attention_workspace_size(const moe_kv_cache* cache, int batch,
                                                   int q_heads);
