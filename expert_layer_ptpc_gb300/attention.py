@@ -1,10 +1,10 @@
 """The attention half of a decoder step next to the MoE layer: rotary
-positions with several axes, a paged key-value cache and attention of one new
-token over it.
+positions with several axes, a paged key-value cache, attention of one or of many
+new tokens over it, and the block tables and slot maps of a step.
 
-`Rotary` and `PagedKVCache` hold what a serving loop keeps between steps (the
-frequencies, the cache's tensors) and call the library entry points of
-`binding`; all arithmetic runs in the library's kernels.
+`Rotary`, `PagedKVCache` and `PagePool` hold what a serving loop keeps between
+steps (the frequencies, the cache's tensors, the requests' pages) and call the
+library entry points of `binding`; all arithmetic runs in the library's kernels.
 """
 
 import math
@@ -99,7 +99,9 @@ _kept = threading.local()   # workspaces: this host thread's, by GPU and stream
 
 class PagedKVCache:
     """Pages of keys and values, [pages, heads, page_size, head_dim] each, as
-    e4m3 codes with one fp32 scale per token and head, or in bf16."""
+    e4m3 codes with one fp32 scale per token and head (scales [pages, heads,
+    page_size]) or per page and head (a power of two, scales [pages, heads]), or in
+    bf16."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
@@ -114,31 +116,41 @@ class PagedKVCache:
         index = k.get_device()
         for t, n in ((k, "k"), (v, "v")):
             binding._need_on(t, k.dtype, n, index)
+        dtype = dtypes[k.dtype]
         if coded:
+            by_page = k_scale.dim() == 2
+            dtype = binding.MOE_DTYPE_E4M3_PAGE if by_page else dtype
+            shape = k.shape[:2 if by_page else 3]
             for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
                 binding._need_on(t, torch.float32, n, index)
-                if t.shape != k.shape[:3]:
-                    raise ValueError(f"{n} must be {tuple(k.shape[:3])}, got {tuple(t.shape)}")
+                if t.shape != shape:
+                    raise ValueError(f"{n} must be {tuple(shape)}, got {tuple(t.shape)}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
         self.struct = binding.moe_kv_cache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if coded else None,
             v_scale.data_ptr() if coded else None, self.pages, self.heads, self.page_size,
-            self.head_dim, dtypes[k.dtype])
+            self.head_dim, dtype)
         self.struct.device = index
         self._ws_bytes = {}       # by query heads
+        self._prompt_ws_bytes = {}
         self._scale = 1.0 / math.sqrt(self.head_dim)
 
     @classmethod
     def empty(cls, pages, heads, page_size, head_dim, dtype="e4m3", device="cuda"):
-        """A new cache; dtype "e4m3" or "bf16". Slots hold nothing until
-        written (no operator reads a slot that no context covers)."""
+        """A new cache; dtype "e4m3" (a scale per token and head), "e4m3_page" (per page
+        and head) or "bf16". Slots hold nothing until written (no operator reads a
+        slot that no context covers)."""
         shape = (pages, heads, page_size, head_dim)
         if dtype == "bf16":
             return cls(*(torch.empty(shape, dtype=torch.bfloat16, device=device)
                          for _ in range(2)))
+        if dtype == "e4m3_page":   # (scales of 0: whatever a page's first call brings is more)
+            return cls(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)),
+                       *(torch.zeros(shape[:2], dtype=torch.float32, device=device)
+                         for _ in range(2)))
         if dtype != "e4m3":
-            raise ValueError(f'dtype must be "e4m3" or "bf16", got {dtype!r}')
+            raise ValueError(f'dtype must be "e4m3", "e4m3_page" or "bf16", got {dtype!r}')
         return cls(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)),
                    *(torch.empty(shape[:3], dtype=torch.float32, device=device)
                      for _ in range(2)))
@@ -150,12 +162,13 @@ class PagedKVCache:
 
     def write(self, k, v, slots, stream=None):
         """Store k, v [T, heads, head_dim] bf16 at slots [T] int32 (slot =
-        page * page_size + offset; a slot outside the cache skips its token)."""
+        page * page_size + offset; a slot outside the cache skips its token). With a
+        scale per page, a page's tokens follow one another in the call."""
         binding.moe_kv_write(self.struct, k, v, slots, stream)
 
     def write_rotary(self, rotary, positions, q, k, v, slots, q_out=None, stream=None):
-        """Rotate q and k by `rotary` and store the rotated k and v, in one
-        launch; returns the rotated q."""
+        """Rotate q and k by `rotary` and store the rotated k and v; returns the
+        rotated q."""
         return binding.moe_rotary_kv_write(rotary.plan, positions, self.struct, q, k, v, slots,
                                            q_out, stream)
 
@@ -170,12 +183,23 @@ class PagedKVCache:
         each stream has its own. A call is two launches, between which another
         thread may enqueue its own on the same stream, so each thread has its own
         too. A captured call's belongs to its graph."""
-        index = self.struct.device
-        on = binding._raw_stream(stream, index)
         need = self._ws_bytes.get(q_heads)
         if need is None:          # (the same for every batch)
             need = binding.moe_paged_attention_workspace_size(self.struct, 1, q_heads)
             self._ws_bytes[q_heads] = need
+        return self._workspace(need, stream)
+
+    def prompt_workspace(self, q_heads, stream=None):
+        """The same for attend_prompt."""
+        need = self._prompt_ws_bytes.get(q_heads)
+        if need is None:
+            need = binding.moe_prompt_attention_workspace_size(self.struct, q_heads)
+            self._prompt_ws_bytes[q_heads] = need
+        return self._workspace(need, stream)
+
+    def _workspace(self, need, stream):
+        index = self.struct.device
+        on = binding._raw_stream(stream, index)
         if binding._capturing(stream, index):
             return self._new_workspace(need, stream)
         kept, key = _kept.__dict__, (index, on)
@@ -199,3 +223,83 @@ class PagedKVCache:
             ws = self.workspace(q.shape[0], q.shape[1], stream)
         return binding.moe_paged_attention(self.struct, q, block_table, lengths, scale, window,
                                            out, lse, ws, stream, return_lse or lse is not None)
+
+    def attend_prompt(self, q, offsets, block_table, lengths, scale=None, window=0, out=None,
+                      lse=None, return_lse=False, ws=None, stream=None):
+        """Attention of many new tokens per context: q [rows, q_heads, head_dim] bf16,
+        context b's in rows offsets[b] .. offsets[b + 1], which are the last of its
+        lengths[b] tokens (keys and values already written). Each sees the tokens
+        of its context up to its own (the last `window` of them when window > 0). Rows
+        from offsets[-1] on are left as they are. scale: default 1 / sqrt(head_dim).
+        Returns out, or (out, lse) with `return_lse` or `lse`."""
+        if scale is None:
+            scale = self._scale
+        if ws is None:
+            ws = self.prompt_workspace(q.shape[1], stream)
+        return binding.moe_prompt_attention(self.struct, q, offsets, block_table, lengths, scale,
+                                            window, out, lse, ws, stream,
+                                            return_lse or lse is not None)
+
+
+class StepPlan:
+    """What one step needs to know, all int32 on the GPU: `offsets` [batch + 1] of the
+    requests' rows, `lengths` [batch] of their contexts with the new tokens, `slots`
+    [rows] and `positions` [axes, rows] of the rows (-1 and 0 for rows behind the
+    last), `refused` [1], the number of requests that wait for pages or rows, and
+    `state`, the pool's after the step."""
+
+    __slots__ = ("offsets", "lengths", "slots", "positions", "state", "refused")
+
+    def __init__(self, offsets, slots, positions, state, refused):
+        self.offsets, self.slots, self.positions = offsets, slots, positions
+        self.state, self.refused = state, refused
+        self.lengths = state[:-1]
+
+
+class PagePool:
+    """The pages of a batch of requests: `table` [batch, max_pages] int32, request b's
+    pages in order; `stack` [pages] int32, the free pages, the next to be handed out
+    last; `state` [batch + 1] int32: the tokens that each request holds, then the
+    number of free pages. All of it lives on the GPU, and so a captured step can go
+    on handing out pages."""
+
+    def __init__(self, table, stack, state, page_size):
+        if table.dim() != 2 or stack.dim() != 1 or state.dim() != 1:
+            raise ValueError("table must be [batch, max_pages], stack [pages], state [batch + 1]")
+        if page_size < 1 or page_size > 1024 or page_size & (page_size - 1):
+            raise ValueError(f"page_size must be a power of two up to 1024, got {page_size}")
+        if state.numel() != table.shape[0] + 1:
+            raise ValueError(f"state must have {table.shape[0] + 1} entries, got {state.numel()}")
+        self.table, self.stack, self.state, self.page_size = table, stack, state, page_size
+
+    @classmethod
+    def empty(cls, pages, page_size, batch, max_pages, device="cuda"):
+        """A pool whose pages are all free, for up to `batch` requests at a time."""
+        state = torch.zeros(batch + 1, dtype=torch.int32, device=device)
+        state[-1] = pages
+        return cls(torch.full((batch, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device), state,
+                   page_size)
+
+    @classmethod
+    def from_tensors(cls, table, stack, state, page_size):
+        """A pool over the caller's tensors (shared, not copied)."""
+        return cls(table, stack, state, page_size)
+
+    def plan(self, new_tokens, rows, axes=1, stream=None):
+        """The StepPlan of new_tokens [batch] int32 more tokens for each request; a
+        negative number: the request leaves, and its pages are free for this
+        step already. The requests are served in order, until one would need more pages than
+        are free or more than `rows` rows in all; that one and those behind it, and a
+        request that outgrows its table, wait (their lengths stay). Updates table and
+        stack; state stays until `commit`, and planning again starts from there."""
+        return StepPlan(*binding.moe_kv_plan(self.state, new_tokens, self.table, self.stack,
+                                             self.page_size, rows, axes, stream))
+
+    def commit(self, plan, stream=None):
+        """Make the plan's state the pool's."""
+        if stream is None:
+            self.state.copy_(plan.state)
+        else:
+            with torch.cuda.stream(stream):
+                self.state.copy_(plan.state)

@@ -18,6 +18,7 @@ from . import build as _build
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
 MOE_DTYPE_E4M3 = 2   # key-value caches only
+MOE_DTYPE_E4M3_PAGE = 3
 MOE_GEMM_GATEUP_SWIGLU = 0
 MOE_GEMM_DOWN = 1
 
@@ -107,6 +108,10 @@ _SIGNATURES = {
     "moe_paged_attention_workspace_size": (_SZ, [_P, _I, _I]),
     "moe_paged_attention": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _I, _P, ctypes.c_float, _I,
                                  _P, _P, _P, _SZ, _P]),
+    "moe_kv_plan": (_I, [_P, _P, _I, _P, _I64, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_prompt_attention_workspace_size": (_SZ, [_P, _I]),
+    "moe_prompt_attention": (_I, [_P, _P, _I64, _I, _I, _P, _P, _I64, _I, _P, _I, ctypes.c_float,
+                                  _I, _P, _I64, _P, _P, _SZ, _P]),
 }
 
 MOE_SCALE_PTPC, MOE_SCALE_SUB512, MOE_SCALE_BLOCK128 = 0, 1, 2
@@ -876,4 +881,88 @@ def moe_paged_attention(cache, q, block_table, lengths, scale, window=0, out=Non
         _raw_stream(stream, index))
     if status:
         raise MoeError("moe_paged_attention", status)
+    return (out, lse) if return_lse else out
+
+
+def moe_kv_plan(state, new_tokens, block_table, stack, page_size, rows, axes=1, stream=None):
+    """Block tables and slot maps of a step. state [batch + 1] int32: the tokens that
+    each request holds, then the number of free pages; new_tokens [batch] int32
+    (negative: the request leaves); block_table [batch, max_pages] and stack [pages]
+    int32, both updated. Returns (offsets [batch + 1], slots [rows], positions
+    [axes, rows], state [batch + 1], refused [1]), all int32."""
+    batch = new_tokens.numel()
+    index = _gpu_of(state, "state")
+    _need_on(state, torch.int32, "state", index)
+    _need_on(new_tokens, torch.int32, "new_tokens", index)
+    _need_on(stack, torch.int32, "stack", index)
+    if batch < 1 or state.numel() != batch + 1:
+        raise ValueError(f"state must have an entry more than new_tokens, got {state.numel()} "
+                         f"and {batch}")
+    if not 0 <= rows <= _INT_MAX or not 1 <= axes <= 8:
+        raise ValueError(f"rows must be 0 to {_INT_MAX} and axes 1 to 8, got {rows} and {axes}")
+    if stack.numel() > _INT_MAX or not 1 <= page_size <= _INT_MAX:
+        raise ValueError(f"at most {_INT_MAX} pages are supported")
+    stride, pages = _need_table(block_table, batch, index)
+    made = _empty(2 * batch + 3 + (1 + axes) * rows, torch.int32, state.device, stream)
+    offsets, state_out, refused, slots, positions = made.split(
+        (batch + 1, batch + 1, 1, rows, axes * rows))
+    positions = positions.view(axes, rows)
+    status = (_lib or load_library()).moe_kv_plan(
+        state.data_ptr(), new_tokens.data_ptr(), batch, block_table.data_ptr(), stride, pages,
+        stack.data_ptr(), stack.numel(), page_size, rows, axes, offsets.data_ptr(),
+        slots.data_ptr(), positions.data_ptr(), state_out.data_ptr(), refused.data_ptr(),
+        _raw_stream(stream, index))
+    if status:
+        raise MoeError("moe_kv_plan", status)
+    return offsets, slots, positions, state_out, refused
+
+
+def moe_prompt_attention_workspace_size(cache, q_heads):
+    """Workspace bytes of moe_prompt_attention (0 for an unsupported shape)."""
+    return load_library().moe_prompt_attention_workspace_size(ctypes.byref(cache), q_heads)
+
+
+def moe_prompt_attention(cache, q, offsets, block_table, lengths, scale, window=0, out=None,
+                         lse=None, ws=None, stream=None, return_lse=False):
+    """Attention of the new tokens of each context: q [rows, q_heads, head_dim] bf16,
+    rows offsets[b]..offsets[b + 1] the last tokens of context b; returns out, of q's
+    shape, or (out, lse) with return_lse. `lse`: optional [rows, q_heads] fp32 tensor
+    that receives the log of the sums. Rows from offsets[-1] on are left as they are.
+    ws: a contiguous tensor of at least moe_prompt_attention_workspace_size bytes
+    (None: a new one)."""
+    rows, hq, d = q.shape
+    if not -_INT_MAX <= window <= _INT_MAX:
+        raise ValueError(f"window must be at most {_INT_MAX}, got {window}")
+    index = _gpu_of(q, "q", cache)
+    q_stride = _need_heads(q, hq, cache.head_dim, "q", index)
+    _need_on(lengths, torch.int32, "lengths", index)
+    _need_on(offsets, torch.int32, "offsets", index)
+    batch = lengths.numel()
+    stride, pages = _need_table(block_table, batch, index)
+    if offsets.numel() != batch + 1:
+        raise ValueError(f"offsets must have {batch + 1} entries, got {offsets.numel()}")
+    if out is None:
+        out, out_stride = _empty((rows, hq, d), torch.bfloat16, q.device, stream), hq * d
+    else:
+        out_stride = _need_heads(out, hq, d, "out", index)
+        if out.shape[0] != rows:
+            raise ValueError(f"out must have {rows} tokens, got {out.shape[0]}")
+    if lse is not None:
+        _need_on(lse, torch.float32, "lse", index)
+        if tuple(lse.shape) != (rows, hq):
+            raise ValueError(f"lse must be {(rows, hq)}, got {tuple(lse.shape)}")
+    elif return_lse:
+        lse = _empty((rows, hq), torch.float32, q.device, stream)
+    if ws is None:
+        need = moe_prompt_attention_workspace_size(cache, hq)
+        ws = _empty(max(need, 1), torch.uint8, q.device, stream)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous CUDA tensor on GPU {index}")
+    status = (_lib or load_library()).moe_prompt_attention(
+        ctypes.byref(cache), q.data_ptr(), q_stride, rows, hq, offsets.data_ptr(),
+        block_table.data_ptr(), stride, pages, lengths.data_ptr(), batch, scale, window,
+        out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), ws.data_ptr(),
+        ws.nbytes, _raw_stream(stream, index))
+    if status:
+        raise MoeError("moe_prompt_attention", status)
     return (out, lse) if return_lse else out

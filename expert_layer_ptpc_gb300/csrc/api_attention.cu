@@ -1,5 +1,6 @@
 // C ABI of the attention operators: argument checks in front of the kernels
-// of rotary.cu, kv_read.cu and paged_attention.cu. Declared in moe_ptpc.h.
+// of rotary.cu, page_write.cu, kv_plan.cu, kv_read.cu, paged_attention.cu and
+// prompt_attention.cu. Declared in moe_ptpc.h.
 #include <cmath>
 
 #include "../../include/moe_ptpc.h"
@@ -39,9 +40,11 @@ int check_plan(const moe_rotary_plan* p, const int32_t* positions, int head_dim)
 int check_cache(const moe_kv_cache* c) {
   if (c == nullptr || c->pages <= 0 || c->heads <= 0 || c->page_size <= 0 || c->head_dim <= 0)
     return MOE_ERR_INVALID_ARG;
-  if (c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_E4M3) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_E4M3 &&
+      c->dtype != MOE_DTYPE_E4M3_PAGE)
+    return MOE_ERR_INVALID_ARG;
   if (!good16(c->k) || !good16(c->v)) return MOE_ERR_INVALID_ARG;
-  const bool e4m3 = c->dtype == MOE_DTYPE_E4M3;
+  const bool e4m3 = c->dtype != MOE_DTYPE_BF16;
   if (e4m3 ? !good16(c->k_scale) || !good16(c->v_scale)
            : c->k_scale != nullptr || c->v_scale != nullptr)
     return MOE_ERR_INVALID_ARG;
@@ -68,7 +71,8 @@ CacheView view_of(const moe_kv_cache& c, const int32_t* table, int64_t table_str
   v.heads = c.heads;
   v.page_shift = log2_of(c.page_size);
   v.head_dim = c.head_dim;
-  v.e4m3 = c.dtype == MOE_DTYPE_E4M3;
+  v.e4m3 = c.dtype != MOE_DTYPE_BF16;
+  v.scale_shift = c.dtype == MOE_DTYPE_E4M3_PAGE ? v.page_shift : 0;
   v.table = table;
   v.table_stride = table_stride;
   v.max_pages = max_pages;
@@ -167,6 +171,7 @@ int moe_kv_write(const moe_kv_cache* cache, const int32_t* slots, int T, const u
   a.v = v;
   a.v_stride = v_stride;
   set_cache(&a, *cache, slots);
+  if (cache->dtype == MOE_DTYPE_E4M3_PAGE) return launch_page_write(a, false, stream);
   return launch_rotary(a, cache->dtype == MOE_DTYPE_E4M3 ? 1 : 2, false, stream);
 }
 
@@ -201,6 +206,8 @@ int moe_rotary_kv_write(const moe_rotary_plan* plan, const int32_t* positions,
   a.v_stride = v_stride;
   set_plan(&a, *plan, positions);
   set_cache(&a, *cache, slots);
+  if (cache->dtype == MOE_DTYPE_E4M3_PAGE)
+    return launch_page_write(a, plan->neighbours != 0, stream);
   return launch_rotary(a, cache->dtype == MOE_DTYPE_E4M3 ? 1 : 2, plan->neighbours != 0, stream);
 }
 
@@ -244,6 +251,68 @@ int moe_paged_attention(const moe_kv_cache* cache, const uint16_t* q, int64_t q_
   return launch_paged_attention(view_of(*cache, block_table, table_stride, max_pages), q,
                                 q_stride, batch, q_heads, lengths, scale, window, out, lse, ws,
                                 stream);
+}
+
+int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int batch, int32_t* block_table,
+                int64_t table_stride, int max_pages, int32_t* stack, int pages, int page_size,
+                int rows, int axes, int32_t* offsets, int32_t* slots, int32_t* positions,
+                int32_t* state_out, int32_t* refused, moe_stream_t stream) {
+  if (batch < 1 || max_pages < 1 || table_stride < max_pages || pages < 1 || page_size < 1 ||
+      rows < 0 || axes < 1 || axes > 8)
+    return MOE_ERR_INVALID_ARG;
+  if (!good4(state) || !good4(new_tokens) || !good4(block_table) || !good4(stack) ||
+      !good4(offsets) || !good4(state_out) || !good4(refused) ||
+      (rows > 0 && (!good4(slots) || !good4(positions))))
+    return MOE_ERR_INVALID_ARG;
+  if (batch > kPlanMaxBatch || page_size > 1024 || (page_size & (page_size - 1)) != 0 ||
+      (int64_t)pages * page_size >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  PlanArgs a{};
+  a.state = state;
+  a.new_tokens = new_tokens;
+  a.batch = batch;
+  a.page_shift = log2_of(page_size);
+  a.pages = pages;
+  a.max_pages = max_pages;
+  a.axes = axes;
+  a.rows = rows;
+  a.table_stride = table_stride;
+  a.table = block_table;
+  a.stack = stack;
+  a.offsets = offsets;
+  a.slots = slots;
+  a.positions = positions;
+  a.state_out = state_out;
+  a.refused = refused;
+  return launch_kv_plan(a, stream);
+}
+
+size_t moe_prompt_attention_workspace_size(const moe_kv_cache* cache, int q_heads) {
+  if (check_cache(cache) != MOE_OK || q_heads < 1 || q_heads % cache->heads != 0) return 0;
+  return prompt_attention_ws_bytes(cache->heads, cache->head_dim, q_heads);
+}
+
+int moe_prompt_attention(const moe_kv_cache* cache, const uint16_t* q, int64_t q_stride, int rows,
+                         int q_heads, const int32_t* offsets, const int32_t* block_table,
+                         int64_t table_stride, int max_pages, const int32_t* lengths, int batch,
+                         float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
+                         void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (rows < 0 || batch < 0 || q_heads < 1 || window < 0 || !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (const int st = check_cache(cache)) return st;
+  if (q_heads % cache->heads != 0) return MOE_ERR_INVALID_ARG;
+  if (batch > 65535 || q_heads > 65535 || (int64_t)rows * q_heads >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (rows == 0 || batch == 0) return MOE_OK;
+  if (const int st = check_table(block_table, table_stride, max_pages)) return st;
+  if (!good_heads(q, q_stride, q_heads, cache->head_dim) || !good4(offsets) || !good4(lengths) ||
+      !good_heads(out, out_stride, q_heads, cache->head_dim) || (lse != nullptr && !good4(lse)))
+    return MOE_ERR_INVALID_ARG;
+  if (!good16(ws) || ws_bytes < prompt_attention_ws_bytes(cache->heads, cache->head_dim, q_heads))
+    return MOE_ERR_WORKSPACE;
+  return launch_prompt_attention(view_of(*cache, block_table, table_stride, max_pages), q, q_stride,
+                                 rows, q_heads, offsets, lengths, batch, scale, window, out,
+                                 out_stride, lse, ws, stream);
 }
 
 }  // extern "C"

@@ -29,11 +29,15 @@ struct RotaryArgs {
 };
 int launch_rotary(const RotaryArgs& a, int sink, bool neighbours, cudaStream_t stream);
 
-// A checked cache and the block table of a batch of contexts.
+// The same for a cache with one scale per page and head.
+int launch_page_write(const RotaryArgs& a, bool neighbours, cudaStream_t stream);
+
+// A checked cache and the block table of a batch of contexts. The scale of cache
+// row r is number r >> scale_shift.
 struct CacheView {
   const void *k, *v;
   const float *k_scale, *v_scale;
-  int pages, heads, page_shift, head_dim;
+  int pages, heads, page_shift, head_dim, scale_shift;
   bool e4m3;
   const int32_t* table;
   int64_t table_stride;
@@ -47,5 +51,21 @@ size_t paged_attention_ws_bytes(int heads, int head_dim, int q_heads);
 int launch_paged_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int batch,
                            int q_heads, const int32_t* lengths, float scale, int window,
                            uint16_t* out, float* lse, void* ws, cudaStream_t stream);
+
+// Block tables and slot maps of a step (moe_kv_plan's arguments, checked).
+struct PlanArgs {
+  const int32_t *state, *new_tokens;
+  int batch, page_shift, pages, max_pages, axes, rows;
+  int64_t table_stride;
+  int32_t *table, *stack, *offsets, *slots, *positions, *state_out, *refused;
+};
+constexpr int kPlanMaxBatch = 4096;
+int launch_kv_plan(const PlanArgs& a, cudaStream_t stream);
+
+size_t prompt_attention_ws_bytes(int heads, int head_dim, int q_heads);
+int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int rows,
+                            int q_heads, const int32_t* offsets, const int32_t* lengths, int batch,
+                            float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
+                            void* ws, cudaStream_t stream);
 
 }  // namespace moe

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(
               static_cast<const uint8_t*>(which ? c.v : c.k) + at);
           raw[j][which].x = w.x;
           raw[j][which].y = w.y;
-          scale[j][which] = (which ? c.v_scale : c.k_scale)[row];
+          scale[j][which] = (which ? c.v_scale : c.k_scale)[row >> c.scale_shift];
         } else {
           raw[j][which] = *reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(which ? c.v : c.k) + at);

@@ -1,0 +1,220 @@
+// The key-value cache's write where a page has one scale for each head, behind the
+// rotation of the keys when there is one.
+//
+//   a = max |x| over the tokens that the call brings to the page,
+//   s(a) = 2^e, e the least integer >= -48 with a <= 448 * 2^e,
+//   scale' = s(a) when the call begins the page (writes its offset 0),
+//            max(scale, s(a)) when not; then a code q that stays becomes
+//            e4m3(q scale / scale'), and x is stored as e4m3(x / scale').
+//
+// Scales are powers of two, so that quotients by them are exact and a code has one
+// rounding; a code that stays is exact under a grown scale as long as it is not
+// subnormal there. e4m3 spans 2^-9 to 448, so that against a scale that brings the
+// largest element to 448 a power of two costs at most the lowest binade of those 18.
+//
+// A block takes the runs of tokens that begin in its part of the call, for one head of
+// k or v. A run is what the call brings to one page: tokens that follow one another
+// with slots of the same page. Its maximum has to be known before its first code, so
+// the first 4 units of a thread (64 tokens of 128 elements) stay in registers between,
+// and the rest are read twice. Bound by memory: 2 bytes an element in, 1 out.
+#include <algorithm>
+
+#include "attention.h"
+#include "common.cuh"
+#include "internal.h"
+#include "rotary.cuh"
+
+#include <cuda_fp16.h>
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kKept = 4;        // units of a thread in registers
+constexpr int kMostTokens = 64; // of a block's part
+constexpr float kLeastScale = 0x1p-48f;
+
+// 2^e, e the least integer >= -48 with amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ float page_scale(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int e = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return fmaxf(__uint_as_float((uint32_t)max(e, 1) << 23), kLeastScale);
+}
+
+__device__ __forceinline__ uint2 codes8(const float* v, float by) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = (uint32_t)f32x2_to_e4m3x2(v[4 * i] * by, v[4 * i + 1] * by) |
+           ((uint32_t)f32x2_to_e4m3x2(v[4 * i + 2] * by, v[4 * i + 3] * by) << 16);
+  return make_uint2(w[0], w[1]);
+}
+
+// Four codes times a power of two, as codes.
+__device__ __forceinline__ uint32_t scaled_codes(uint32_t w, float by) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    out |= (uint32_t)f32x2_to_e4m3x2(f.x * by, f.y * by) << (16 * i);
+  }
+  return out;
+}
+
+template <int PAIRS>
+__global__ void __launch_bounds__(kThreads) page_write_kernel(const RotaryArgs a, int part) {
+  __shared__ int32_t slots[kMostTokens + 1];   // of the part, and of the token before it
+  __shared__ int ends[kThreads / 32], begins[kThreads / 32];
+  __shared__ float maxima[kThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = blockIdx.x * part, here = min(part, a.T - t0);
+  const bool is_v = (blockIdx.y & 1) != 0;
+  const int head = blockIdx.y >> 1;
+  const int size = 1 << a.page_shift;
+  for (int i = threadIdx.x; i <= here; i += kThreads)
+    slots[i] = t0 + i > 0 ? a.slots[t0 + i - 1] : -1;
+  __syncthreads();
+  // the page of a slot (-1: none)
+  auto page_of = [&](int32_t slot) -> int {
+    return (uint32_t)slot < a.cache_slots ? slot >> a.page_shift : -1;
+  };
+
+  const int units = a.head_dim / kUnit, u = threadIdx.x % units;   // of a token
+  const int first = threadIdx.x / units, step = kThreads / units;  // tokens
+  const int rot_units = PAIRS == kNoPairs || is_v ? 0 : a.rot / kUnit;
+  const bool rotates = u < rot_units;
+  const int from = rotates || rot_units == 0 ? 0 : a.rot;
+  const int region = rot_units == 0 ? a.head_dim : rotates ? a.rot : a.head_dim - a.rot;
+  const int run0 = from + 8 * (rotates ? u : u - rot_units), run1 = run0 + region / 2;
+  const uint16_t* const src = (is_v ? a.v : a.k) + head * a.head_dim;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  auto load = [&](int t, float* x) {
+    unpack8(*reinterpret_cast<const uint4*>(src + t * stride + run0), x);
+    unpack8(*reinterpret_cast<const uint4*>(src + t * stride + run1), x + 8);
+    if (PAIRS != kNoPairs && rotates) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = pair_of<PAIRS>(u, j, a.rot);
+        const float2 cs = turn_of(a, t, a.turns[p], a.pair_axis[p]);
+        turn_pair(cs, PAIRS == kNeighbours ? x[2 * j] : x[j],
+                  PAIRS == kNeighbours ? x[2 * j + 1] : x[8 + j]);
+      }
+    }
+  };
+  auto largest = [&](const float* x) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) m = fmaxf(m, fabsf(x[j]));
+    return m;
+  };
+
+  for (int i = 0; i < here; ++i) {
+    const int page = page_of(slots[i + 1]);
+    if (page < 0 || page == page_of(slots[i])) continue;
+    // the run: tokens [t, t + n), and whether it begins the page
+    const int t = t0 + i;
+    int end = size, zero = size;   // (slots differ, so that a run has at most `size` tokens)
+    for (int j = threadIdx.x; j < size; j += kThreads) {
+      const int32_t slot = t + j < a.T ? a.slots[t + j] : -1;
+      if (page_of(slot) != page) {
+        end = j;
+        break;
+      }
+      if ((slot & (size - 1)) == 0) zero = min(zero, j);
+    }
+    end = __reduce_min_sync(0xffffffffu, end);
+    zero = __reduce_min_sync(0xffffffffu, zero);
+    if (lane == 0) {
+      ends[warp] = end;
+      begins[warp] = zero;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      end = min(end, ends[w]);
+      zero = min(zero, begins[w]);
+    }
+    const int n = end;
+    const bool begun = zero < n;
+    const int64_t block = (int64_t)page * a.k_heads + head;
+    float* const scale_at = (is_v ? a.v_scale : a.k_scale) + block;
+    const float was = begun ? 0.f : *scale_at;
+
+    float x[kKept][kUnit], top = 0.f;
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int j = first + k * step;
+      if (j < n) {
+        load(t + j, x[k]);
+        top = fmaxf(top, largest(x[k]));
+      }
+    }
+    for (int j = first + kKept * step; j < n; j += step) {
+      float y[kUnit];
+      load(t + j, y);
+      top = fmaxf(top, largest(y));
+    }
+    top = warp_max(top);
+    if (lane == 0) maxima[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, maxima[w]);
+    const float scale = fmaxf(was, page_scale(top)), by = __frcp_rn(scale);
+    uint8_t* const out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) +
+                         (block << a.page_shift) * a.head_dim;
+    if (!begun && scale > was) {   // the codes that stay (the run's are written over them)
+      const float down = was * by;
+      for (int c = threadIdx.x; c < size * a.head_dim / 16; c += kThreads) {
+        uint4 w = reinterpret_cast<uint4*>(out)[c];
+        w.x = scaled_codes(w.x, down);
+        w.y = scaled_codes(w.y, down);
+        w.z = scaled_codes(w.z, down);
+        w.w = scaled_codes(w.w, down);
+        reinterpret_cast<uint4*>(out)[c] = w;
+      }
+      __syncthreads();
+    }
+    auto store = [&](int t, const float* x) {
+      uint8_t* const row = out + (a.slots[t] & (size - 1)) * a.head_dim;
+      *reinterpret_cast<uint2*>(row + run0) = codes8(x, by);
+      *reinterpret_cast<uint2*>(row + run1) = codes8(x + 8, by);
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int j = first + k * step;
+      if (j < n) store(t + j, x[k]);
+    }
+    for (int j = first + kKept * step; j < n; j += step) {
+      float y[kUnit];
+      load(t + j, y);
+      store(t + j, y);
+    }
+    if (threadIdx.x == 0) *scale_at = scale;
+  }
+}
+
+}  // namespace
+
+int launch_page_write(const RotaryArgs& a, bool neighbours, cudaStream_t stream) {
+  if (a.q_heads > 0) {
+    RotaryArgs q = a;
+    q.k_heads = 0;
+    if (const int st = launch_rotary(q, 0, neighbours, stream)) return st;
+  }
+  // tokens of a block: so that there are enough blocks to fill the GPU
+  const int64_t work = (int64_t)a.T * 2 * a.k_heads;
+  const int part = (int)std::min<int64_t>(kMostTokens, std::max<int64_t>(1, work / 4096));
+  void (*kernel)(RotaryArgs, int) = a.rot == 0   ? page_write_kernel<kNoPairs>
+                                    : neighbours ? page_write_kernel<kNeighbours>
+                                                 : page_write_kernel<kHalves>;
+  const cudaError_t e = launch_kernel(true, dim3((a.T + part - 1) / part, 2 * a.k_heads),
+                                      dim3(kThreads), 0, stream, kernel, a, part);
+  return e == cudaSuccess ? 0 : -3;
+}
+
+}  // namespace moe

@@ -552,8 +552,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E4M3, D, M>::kCtas)
   auto ask_scales = [&](const Tokens k) {
     key_scale = value_scale = 1.f;
     if (E4M3 && ((k.here >> (lane & (S::kTile - 1))) & 1u)) {
-      key_scale = a.c.k_scale[k.row];
-      value_scale = a.c.v_scale[k.row];
+      key_scale = a.c.k_scale[k.row >> a.c.scale_shift];
+      value_scale = a.c.v_scale[k.row >> a.c.scale_shift];
     }
   };
   auto put_scales = [&](int n) {

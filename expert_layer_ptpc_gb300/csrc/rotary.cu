@@ -30,13 +30,13 @@
 #include "attention.h"
 #include "common.cuh"
 #include "internal.h"
+#include "rotary.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kUnit = 16;     // elements of a lane
 // Blocks of an SM: 32 warps of 64 registers a lane. A lane's units travel through
 // shared memory (cp.async, each lane reads back its own), so that more of them are
 // in flight than registers would hold. (GB300, 8192 tokens of 64 + 4 heads of 128, the
@@ -48,25 +48,6 @@ constexpr int kAhead = 3;     // units of a lane in flight
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void unpack8(const uint4& raw, float* v) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // v / s rounded to nearest, for many v and one s: with y = 1 / s rounded to
@@ -96,7 +77,6 @@ __device__ __forceinline__ uint2 codes8(const float* v, float s, float y) {
 }
 
 enum Sink { kSinkTensors = 0, kSinkE4m3 = 1, kSinkBf16 = 2 };
-enum Pairs { kNoPairs = 0, kHalves = 1, kNeighbours = 2 };
 
 // A token's heads are q's, then k's, then (with a cache) v's. Warp w of the grid
 // takes heads [part * per_warp, ...) of token w / parts, part = w % parts.
@@ -160,18 +140,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks)
   if (PAIRS != kNoPairs) {
     float2* const table = turns + (threadIdx.x >> 5) * (a.rot / 2);
     for (int p = lane; p < a.rot / 2; p += 32) {
-      const int axis = a.pair_axis[p];
-      const int32_t pos = axis < a.axes ? a.positions[(int64_t)axis * a.T + t] : 0;
-      const uint64_t f = (uint64_t)(int64_t)pos * a.turns[p];
-      float s, c;
-      sincospif((float)(int32_t)(f >> 32) * 0x1p-31f, &s, &c);
-      table[p] = make_float2(c, a.inverse ? -s : s);
+      table[p] = turn_of(a, t, a.turns[p], a.pair_axis[p]);
     }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      // pairs (i, i + rot / 2): run0[j] with run1[j]; neighbours: four in each run
-      const int p = NEIGHBOURS ? (j < 4 ? 4 * u + j : a.rot / 4 + 4 * u + j - 4) : 8 * u + j;
+      const int p = pair_of<PAIRS>(u, j, a.rot);
       cs[j] = rotates ? table[p] : make_float2(1.f, 0.f);
     }
   }
@@ -190,13 +164,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks)
     load(step + kAhead);
     if (PAIRS != kNoPairs && rotates && !is_v) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float& x1 = NEIGHBOURS ? x[2 * j] : x[j];
-        float& x2 = NEIGHBOURS ? x[2 * j + 1] : x[8 + j];
-        const float y1 = fmaf(x1, cs[j].x, -(x2 * cs[j].y));
-        x2 = fmaf(x2, cs[j].x, x1 * cs[j].y);
-        x1 = y1;
-      }
+      for (int j = 0; j < 8; ++j)
+        turn_pair(cs[j], NEIGHBOURS ? x[2 * j] : x[j], NEIGHBOURS ? x[2 * j + 1] : x[8 + j]);
     }
     const int o0 = is_v ? v_run0 : run0, o1 = is_v ? v_run1 : run1;
     uint16_t* dst = nullptr;

@@ -63,7 +63,8 @@ typedef enum moe_status {
 typedef enum moe_dtype {
   MOE_DTYPE_BF16 = 0,
   MOE_DTYPE_F32 = 1,
-  MOE_DTYPE_E4M3 = 2 /* key-value caches only */
+  MOE_DTYPE_E4M3 = 2,      /* key-value caches only: a scale per token and head */
+  MOE_DTYPE_E4M3_PAGE = 3  /* key-value caches only: a scale per page and head  */
 } moe_dtype;
 
 typedef enum moe_gemm_kind {
@@ -595,7 +596,8 @@ MOE_API int moe_grouped_gemm_scaled(int scale_kind, const uint8_t* A, const floa
 
 /*
  * Attention beside the MoE block: rotary positions with several axes, a
- * paged key-value cache and attention of one new token over it ("Ultimate
+ * paged key-value cache, attention of one or of many new tokens over it, and the
+ * block tables and slot maps of a step ("Ultimate
  * Latency Optimization of Qwen3 and Qwen3-VL on AMD MI300X Series": fused
  * MRoPE of q and k; the paged attention and FP8 cache types the pages name
  * beside the MoE path). No formulas on the pages; the definitions are here.
@@ -646,6 +648,8 @@ MOE_API int moe_rotary(const moe_rotary_plan* plan, const int32_t* positions, in
  *   one scale per token and head (the PTPC quantiser of moe_quant_ptpc on the
  *   head's row), value = code * scale. Scales are positive, as that quantiser
  *   makes them.
+ *   MOE_DTYPE_E4M3_PAGE: k_scale, v_scale [pages, heads] fp32, one scale per page and
+ *   head, powers of two (0 for a page that nothing was written to).
  * head_dim is 64, 128 or 256; page_size a power of two <= 1024; the whole
  * cache has fewer than 2^31 slots and fewer than 2^32 - 1 rows (pages *
  * heads * page_size). Entry points return MOE_ERR_INVALID_ARG for null,
@@ -660,7 +664,7 @@ typedef struct moe_kv_cache {
   int32_t heads;
   int32_t page_size;
   int32_t head_dim;
-  int32_t dtype;             /* MOE_DTYPE_BF16 or MOE_DTYPE_E4M3             */
+  int32_t dtype;             /* MOE_DTYPE_BF16, _E4M3 or _E4M3_PAGE          */
 } moe_kv_cache;
 
 /*
@@ -669,6 +673,16 @@ typedef struct moe_kv_cache {
  * v_stride elements between tokens; slots [T] int32. A token whose slot lies
  * outside [0, pages * page_size) is not written. Two tokens of
  * one call in the same slot are outside the contract.
+ *   MOE_DTYPE_E4M3_PAGE: with a the largest magnitude that the call brings to a page and
+ * head, and e the least integer >= -48 with a <= 448 * 2^e, the scale becomes
+ *   2^e               when the call writes the page's offset 0: what the page held
+ *                     before is void, as the page has a new owner;
+ *   max(scale, 2^e)   when not; where that is more than it was, the page's codes q
+ *                     become e4m3(q * scale / scale'), exact but for codes that are
+ *                     subnormal after it.
+ * The tokens that a call brings to one page must follow one another in the call
+ * (in any order, but without skipped tokens or other pages' between them), as the tokens of a request
+ * do; a page that comes twice in one call is outside the contract.
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
  *         pointers, bad strides, T < 0). T == 0 is a no-op.
  */
@@ -678,7 +692,7 @@ MOE_API int moe_kv_write(const moe_kv_cache* cache, const int32_t* slots, int T,
 
 /*
  * moe_rotary_kv_write - moe_rotary of q and k and moe_kv_write of the rotated
- * keys and the values in one launch: the keys go from fp32 to the cache with
+ * keys and the values in one call: the keys go from fp32 to the cache with
  * one rounding (to e4m3, or to bf16), without the bf16 rounding in between
  * that the two calls would add for an e4m3 cache. Every token's q is rotated,
  * whatever its slot.
@@ -754,6 +768,72 @@ MOE_API int moe_paged_attention(const moe_kv_cache* cache, const uint16_t* q,
                                 int max_pages, const int32_t* lengths, float scale,
                                 int window, uint16_t* out, float* lse, void* ws,
                                 size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_kv_plan - the block tables and slot maps of a step, from how many tokens the
+ * requests hold and get. Pages come from a stack of free ones and go back to it, all
+ * on the device.
+ *   state [batch + 1]: the tokens h_b that request b holds, then the number of
+ *   pages on the stack; new_tokens [batch]: n_b more tokens, or a negative number
+ *   for a request that leaves; block_table [batch, max_pages] with table_stride
+ *   entries between rows; stack [pages], the next page to be taken last.
+ *   1. The pages of the requests that leave (entries of their ceil(h_b / page_size)
+ *      first that lie in [0, pages)) go onto the stack, in order of request and
+ *      entry. F pages are then free.
+ *   2. Request b needs ceil((h_b + n_b) / page_size) - ceil(h_b / page_size) pages. It is
+ *      served when n_b >= 0, its tokens fit max_pages pages and an int32, and the pages
+ *      and the tokens of all such requests up to it are at most F and `rows`.
+ *   3. The k-th page that the served requests take, in order, is stack[F - 1 - k];
+ *      it becomes the next entry of its request's table.
+ *   offsets [batch + 1]: the rows of each request in the step; slots [rows] and positions
+ *   [axes, rows]: of each row's token (its place in the context on every axis); -1 and
+ *   0 for rows from offsets[batch] on. state_out [batch + 1]: h_b + n_b of a served
+ *   request, 0 of one that leaves, else h_b, then the free pages left. refused [1]:
+ *   requests with n_b > 0 that were not served. All int32.
+ *   block_table (entries of pages taken) and stack (from its end on) are written in
+ *   place, state is not: the call can be repeated. The outputs must not overlap the
+ *   inputs. Entries outside [0, pages) on the stack give slots of -1.
+ * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, batch, pages, page_size or
+ *         max_pages < 1, table_stride < max_pages, rows < 0, axes outside 1..8),
+ *         MOE_ERR_UNSUPPORTED (batch > 4096, page_size not a power of two <= 1024, 2^31
+ *         or more slots).
+ */
+MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int batch,
+                        int32_t* block_table, int64_t table_stride, int max_pages,
+                        int32_t* stack, int pages, int page_size, int rows, int axes,
+                        int32_t* offsets, int32_t* slots, int32_t* positions,
+                        int32_t* state_out, int32_t* refused, moe_stream_t stream);
+
+/*
+ * moe_prompt_attention - attention of many new tokens per context over its cached keys
+ * and values. Row r of context b (offsets[b] <= r < offsets[b + 1]) is token
+ *   i = lengths[b] - (offsets[b + 1] - r)
+ * of that context, and out and lse of its heads are those of moe_paged_attention for a
+ * context of i + 1 tokens: it sees its own token and those before it, with window > 0 the
+ * last `window` of them. A row with i < 0 sees nothing.
+ *   q [rows, q_heads, head_dim] bf16 with q_stride elements between tokens; offsets
+ *   [batch + 1] int32, ascending from 0, to at most `rows`; block_table and lengths as
+ *   for moe_paged_attention (the new tokens' keys and values are in the cache already
+ *   and counted); out like q with out_stride; lse [rows, q_heads] fp32 or NULL. Rows
+ *   from offsets[batch] on are left as they are.
+ *   Slots that no context covers have no influence, whatever they hold; a context's
+ *   keys and values from the first token on that any of its rows sees must be finite.
+ *   ws: device workspace of moe_prompt_attention_workspace_size bytes, as for
+ *   moe_paged_attention.
+ * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned pointers, q_heads
+ *         not a multiple of heads, bad strides, scale not finite, rows or batch < 0,
+ *         max_pages < 0, table_stride < max_pages, window < 0), MOE_ERR_UNSUPPORTED (batch
+ *         or q_heads > 65535, rows * q_heads >= 2^31), MOE_ERR_WORKSPACE. rows or batch
+ *         == 0 is a no-op.
+ */
+MOE_API size_t moe_prompt_attention_workspace_size(const moe_kv_cache* cache, int q_heads);
+MOE_API int moe_prompt_attention(const moe_kv_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, int rows, int q_heads,
+                                 const int32_t* offsets, const int32_t* block_table,
+                                 int64_t table_stride, int max_pages,
+                                 const int32_t* lengths, int batch, float scale, int window,
+                                 uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                 size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

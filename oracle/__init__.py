@@ -13,5 +13,6 @@ from .blockscale_ref import (BLOCK_K, BLOCK_N, SUBCHANNEL_K,  # noqa: F401
                              blockscale_matmul_ref, grouped_blockscale_ref,
                              quant_blocks_ref, quant_weight_blocks_ref,
                              subchannel_matmul_ref)
-from .attention_ref import (cache_rows_ref, kv_write_ref, paged_attention_ref,  # noqa: F401
-                            rotary_ref)
+from .attention_ref import (cache_rows_ref, kv_plan_ref, kv_write_page_ref,  # noqa: F401
+                            kv_write_ref, page_scale_ref, paged_attention_ref,
+                            prompt_attention_ref, rotary_ref)
