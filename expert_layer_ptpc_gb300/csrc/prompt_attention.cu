@@ -3,13 +3,44 @@
 //   s_ij = scale q_i . k_j for the tokens j that row i sees,
 //   out_i = sum_j softmax(s_i)_j v_j,  lse_i = ln sum_j exp(s_ij)
 //
-// A warp takes one query head of one new token, its lanes the head's elements, and
-// goes through the context with a running maximum and sum.
+// One pass over the tokens. The query heads of a kv head are rows of one matrix: row r of
+// a context is head r % group of its new token r / group, so that 128 rows are full
+// whatever the group. A CTA takes up to 256 rows (128 of 256 elements) against tiles of
+// 128 tokens (64):
+//   S = Q K^T (tcgen05, fp32 in TMEM);  x_j = s_j c,  w_j = 2^(x_j + F - M);
+//   l += 2^-F sum_j w_j;  O += W V' (tcgen05, W from TMEM), V' = 2^-F V;  out = O / l,
+// with c the factor of the row and tile, F the exponent that brings the tile's values
+// into fp16, and M near the largest x + F so far: it is set 7 below a tile's largest, and
+// moves only when a later one passes it by 15 (fp16 ends at 2^16), so that O is
+// rarely rescaled. A weight is off by up to 2^-11 of it in fp16, or 2^-32 of the largest
+// where that is more.
+//
+// What the tensor cores multiply: e4m3 codes in fp16, which holds them; a page's scale, a
+// power of two, goes into them as a power of two relative to the tile's largest (exact;
+// what is 2^-31 of the tile's largest becomes 0), a token's scale into the score's column
+// (keys) or, rounded to fp16, into the value. q in fp16, scaled by a power of two that
+// brings its head's largest element into [2^8, 2^9): exact down to 2^-25 of that, below
+// that off by up to 2^-33. A bf16 cache: q, k and v as they are, the weights rounded to
+// bf16 (8 bits): the values' own products have no more, and a second product for the
+// rest of a weight would cost half as much again.
+//
+// Roles of a CTA's 13 warps: 0-3 and 4-7 the softmax of 128 rows each, a row a thread; 8-11
+// fetch q, keys and values from the pages and lay them out for the tensor cores; 12
+// issues the products. While one half's softmax runs, the other half's products do; with
+// 128 rows or fewer the halves are two tiles of the same rows.
+//
+// The work is split over the CTAs by length: every item (a context's rows of one kv head)
+// is given a weight, and every CTA an equal run of the weights' sum, whatever the
+// lengths (they are read on the device). An item that several CTAs share leaves partial results,
+// which a second kernel joins.
 #include <algorithm>
+#include <atomic>
+#include <climits>
 
 #include "attention.h"
 #include "common.cuh"
 #include "internal.h"
+#include "tmem.cuh"
 
 #include <cuda_fp16.h>
 
@@ -17,94 +48,1150 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWorkers = 152;              // CTAs, one an SM
+constexpr int kSoftWarps = 8;
+constexpr int kLoadWarp0 = kSoftWarps;
+constexpr int kLoadWarps = 4;
+constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSides = 8;                  // tiles whose masks and factors are at hand
+constexpr int kRequests = 256;             // contexts whose places a CTA keeps at hand
+constexpr float kMostWeight = 15.0f;       // log2 of the largest weight let stand,
+constexpr float kNewWeight = 7.0f;         // and of a tile's largest when M is set by it
+// What an item costs beside its tiles, in tiles of 128 tokens, and the least that a
+// CTA is given.
+constexpr int kItemCost = 4;
+constexpr int kLeastWork = 8;
+
+constexpr int kLeastExponent = -64;        // scales below 2^-64 count as that (sums end at 2^128)
+
+enum Kind { kPageScales = 0, kTokenScales = 1, kBf16 = 2 };
 
 struct Args {
   CacheView c;
   const uint16_t* q;
   int64_t q_stride, out_stride;
-  int rows, q_heads, batch;
+  int rows, q_heads, batch, group;
   const int32_t *offsets, *lengths;
   float scale;
   int window;
   uint16_t* out;
   float* lse;
+  struct Record* records;   // [kWorkers]
+  float2* stats;            // [2 kWorkers][rows of an item] (M, l)
+  float* parts;             // [2 kWorkers][D / 4][rows of an item][4]
+  unsigned* err;
 };
 
-template <bool E4M3>
-__device__ __forceinline__ float element(const void* p, int64_t at) {
-  if (E4M3) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
-        : "=r"(h)
-        : "h"((uint16_t)static_cast<const uint8_t*>(p)[at]));
-    return __low2float(*reinterpret_cast<const __half2*>(&h));
-  }
-  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[at] << 16);
+// What a CTA left of items that it shares with others: of its first one, begun by an
+// earlier CTA (in slot 2 worker), and of its last one, which it began (slot 2 worker + 1).
+struct Record {
+  int4 head;                // context (-1: none), kv head, tile
+  int4 tail;
+  int token0, row0, rows;   // of the tail's rows: the first token of the context, first row, number
+  int some;                 // whether the CTA had anything to do
+};
+
+template <int KIND, int D>
+struct Shape {
+  static constexpr int kStreams = D == 256 ? 1 : 2;       // of 128 rows
+  static constexpr int kRows = 128 * kStreams;            // of an item
+  static constexpr int kTile = D == 256 ? 64 : 128;       // tokens of a tile
+  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kQBytes = 128 * D * 2;             // of a stream
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kSOut = 2 * kTile;                 // TMEM: two tiles of scores, then O
+  static constexpr int kCols = 512;
+  static constexpr int kSmemBytes = 1024 + kStreams * kQBytes + 2 * kStages * kTileBytes;
+  static_assert(kSOut + kStreams * D <= kCols, "tensor memory");
+};
+
+// A tile's masks and factors.
+struct Side {
+  uint32_t mask[4];      // which tokens are there: those of a loading warp each
+  float key_up;          // 2^E
+  float value_exp;       // F
+};
+
+struct Shared {
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t halves, maxed, drain;
+  uint32_t tmem;
+  int abort;
+  Side side[kSides];
+  float key_scale[kSides][128];      // token scales
+  float row_scale[2][256];
+  int maxima[2][kLoadWarps][2];
+  int2 request[kRequests + 1];       // (first row, length)
+  int64_t sums[kThreads / 32 + 1];
+  int place[2][4];                   // the run: first context, kv head, tile, unit; and its end
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {   // of the low two bytes
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  return h;
+}
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                            *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int exponent(float x) {
+  return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
 }
 
-template <bool E4M3, int D>
-__global__ void __launch_bounds__(kWarps * 32) prompt_attention_kernel(const Args a) {
-  constexpr int N = D / 32;
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared_16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// ---- the products ----
+// Instruction descriptor of kind::f16, fp32 accumulator, 128 x N, B from rows along N
+// (transposed) or along the contraction.
+__host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int n, bool b_rows_along_n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
+         ((b_rows_along_n ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+// Descriptor of an operand whose rows run along its outer dimension (values: a row of 64
+// elements of one token, 128 bytes, swizzled): groups of 8 tokens 1024 bytes apart, blocks
+// of 64 elements `block` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(block >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ---- the work ----
+// A context's rows: place of its first new token, rows and items of a kv head.
+struct Context {
+  int token0;      // row of q of its first new token
+  int place;       // that token's place in the context (negative: before it)
+  int rows;        // new tokens x group
+  int items;
+};
+// An item, or a part of one: units [u0, u1) of `units` tiles.
+struct Segment {
+  int b, kv, item;
+  int token0, place, row0, rows;   // rows [row0, row0 + rows) of the context
+  int begin, end, start;           // tokens that take part; the first tile's first
+  int u0, u1, units;
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
+};
+
+template <int ROWS>
+__device__ __forceinline__ Context context_of(const Args& a, int2 from, int to) {
+  Context c;
+  const int n = from.x >= 0 && to >= from.x && to <= a.rows ? to - from.x : 0;
+  c.token0 = from.x;
+  c.place = max(from.y, 0) - n;
+  c.rows = n * a.group;
+  c.items = (c.rows + ROWS - 1) / ROWS;
+  return c;
+}
+
+// Weights of a context's items, in (tiles of 128 tokens) x group: item i has
+//   min(a + s (i + 1), cap) + cost,  s the streams, a the tokens before its first new one.
+struct Weights {
+  int64_t a, cap, cost;
+  int s;
+  __device__ __forceinline__ int64_t of(int i) const {
+    return min(a + (int64_t)s * (i + 1), cap) + cost;
+  }
+  __device__ __forceinline__ int64_t before(int64_t i) const {   // of items 0 .. i - 1
+    const int64_t under = max((int64_t)0, min(i, (cap - a + s - 1) / s - 1));
+    return under * a + s * (under * (under + 1) / 2) + (i - under) * cap + i * cost;
+  }
+};
+template <int STREAMS>
+__device__ __forceinline__ Weights weights_of(const Args& a, const Context& c) {
+  Weights w;
+  const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
+  w.a = (min((int64_t)max(c.place, 0), room) * a.group) >> 7;
+  w.cap = a.window > 0 ? (((int64_t)a.window * a.group) >> 7) + STREAMS : (int64_t)1 << 60;
+  w.a = min(w.a, w.cap);
+  w.cost = (int64_t)kItemCost * a.group;
+  w.s = STREAMS;
+  return w;
+}
+
+template <int ROWS, int TILE>
+__device__ __forceinline__ Segment segment_of(const Args& a, const Context& c, int b, int kv,
+                                              int item) {
+  Segment s;
+  s.b = b;
+  s.kv = kv;
+  s.item = item;
+  s.token0 = c.token0;
+  s.place = c.place;
+  s.row0 = item * ROWS;
+  s.rows = min(ROWS, c.rows - s.row0);
+  const int64_t room = min((int64_t)a.c.max_pages << a.c.page_shift, (int64_t)INT_MAX);
+  const int first = s.row0 / a.group, last = (s.row0 + s.rows - 1) / a.group;
+  s.end = (int)max(min((int64_t)c.place + last + 1, room), (int64_t)0);
+  s.begin = a.window > 0 ? (int)max((int64_t)c.place + first + 1 - a.window, (int64_t)0) : 0;
+  s.begin = min(s.begin, s.end);
+  s.start = s.begin & ~(TILE - 1);
+  s.units = s.end > s.begin ? (int)(((int64_t)s.end - s.start + TILE - 1) / TILE) : 0;
+  s.u0 = 0;
+  s.u1 = s.units;
+  return s;
+}
+
+// Hands out a CTA's run of the work, segment by segment.
+template <int ROWS, int TILE>
+struct Walker {
+  int b, kv, item, unit;      // the next place
+  int end[4];
+  Context c;
+
+  __device__ __forceinline__ int2 request(const Args& a, const Shared& sh, int first, int i) const {
+    const int at = i - first;
+    if (at <= kRequests) return sh.request[at];
+    return make_int2(a.offsets[i], i < a.batch ? a.lengths[i] : 0);
+  }
+  __device__ __forceinline__ void look(const Args& a, const Shared& sh, int first) {
+    c = context_of<ROWS>(a, request(a, sh, first, b), request(a, sh, first, b + 1).x);
+  }
+  __device__ __forceinline__ void init(const Args& a, const Shared& sh) {
+    b = sh.place[0][0];
+    kv = sh.place[0][1];
+    item = sh.place[0][2];
+    unit = sh.place[0][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) end[i] = sh.place[1][i];
+    if (b < a.batch) look(a, sh, b);
+  }
+  __device__ __forceinline__ bool next(const Args& a, const Shared& sh, Segment& s) {
+    for (;;) {
+      if (b >= a.batch || (b == end[0] && kv == end[1] && item == end[2] && unit >= end[3]))
+        return false;
+      const bool last = b == end[0] && kv == end[1] && item == end[2];
+      s = segment_of<ROWS, TILE>(a, c, b, kv, item);
+      s.u0 = min(unit, s.units);
+      if (last) s.u1 = min(end[3], s.units);
+      unit = 0;
+      if (last) {
+        b = a.batch;
+      } else if (++item >= c.items) {
+        item = 0;
+        if (++kv == a.c.heads) {
+          kv = 0;
+          const int first = sh.place[0][0];
+          do {
+            if (++b >= a.batch) break;
+            look(a, sh, first);
+          } while (c.items == 0);
+        }
+      }
+      if (s.u1 > s.u0 || s.units == 0) return true;
+    }
+  }
+};
+
+// Bounded wait of a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared& sh,
+                                          unsigned* err, unsigned code) {
+  const uint32_t at = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+  const unsigned long long t0 = global_timer_ns();
+  for (uint32_t spin = 0;; ++spin) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    if ((spin & 63u) == 63u) {
+      bool bail = *reinterpret_cast<volatile int*>(&sh.abort) != 0;
+      if (!bail && global_timer_ns() - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+        atomicOr(err, code);
+        bail = true;
+      }
+      if (__any_sync(0xffffffffu, bail)) return false;
+    }
+  }
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(smem_u32(bar));
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Args a) {
+  using S = Shape<KIND, D>;
+  constexpr int kRows = S::kRows, kTile = S::kTile;
+  constexpr bool kIsBf16 = KIND == kBf16;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* const smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q_at = smem_u32(smem);
+  const uint32_t k_at = q_at + S::kStreams * S::kQBytes;
+  const uint32_t v_at = k_at + S::kStages * S::kTileBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_u32(&sh.k_full[i]), kLoadWarps);
+      mbar_init(smem_u32(&sh.k_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_full[i]), kLoadWarps);
+      mbar_init(smem_u32(&sh.v_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&sh.q_full), kLoadWarps);
+    mbar_init(smem_u32(&sh.q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.p_full[i]), 4);
+      mbar_init(smem_u32(&sh.o_full[i]), 1);
+      mbar_init(smem_u32(&sh.o_empty[i]), 4);
+    }
+    mbar_init(smem_u32(&sh.halves), kSoftWarps);
+    mbar_init(smem_u32(&sh.maxed), kLoadWarps);
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.abort = 0;
+    sh.place[0][0] = sh.place[1][0] = a.batch;   // nothing to do
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&sh.tmem), S::kCols);
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int row = (int)(w / a.q_heads), h = (int)(w - (int64_t)row * a.q_heads);
-  if (row >= a.rows || row >= a.offsets[a.batch]) return;
-  int lo = 0, hi = a.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.offsets[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int b = lo;
-  const int64_t at = (int64_t)a.lengths[b] - (a.offsets[b + 1] - row);   // the token's place
-  const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
-  const int64_t end = min(at + 1, room);
-  const int64_t begin = a.window > 0 ? max(at + 1 - a.window, (int64_t)0) : 0;
-  const int kv = h / (a.q_heads / a.c.heads);
-  float q[N], acc[N], m = -INFINITY, l = 0.f;
+
+  // ---- this CTA's run of the work ----
+  const int worker = blockIdx.x;
+  {
+    auto total_of = [&](int b) -> int64_t {
+      if (b >= a.batch) return 0;
+      const Context c = context_of<kRows>(a, make_int2(a.offsets[b], a.lengths[b]),
+                                          a.offsets[b + 1]);
+      return c.items == 0 ? 0 : weights_of<S::kStreams>(a, c).before(c.items) * a.c.heads;
+    };
+    // sum over the threads before this one, and over all
+    auto scan = [&](int64_t mine, int64_t& all) -> int64_t {
+      int64_t up = mine;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = element<false>(a.q, row * a.q_stride + h * D + lane + 32 * i);
-    acc[i] = 0.f;
-  }
-  for (int64_t j = begin; j < end; ++j) {
-    const int32_t entry = a.c.table[b * a.c.table_stride + (j >> a.c.page_shift)];
-    if ((uint32_t)entry >= (uint32_t)a.c.pages) continue;
-    const int64_t r = (((int64_t)entry * a.c.heads + kv) << a.c.page_shift) +
-                      (j & ((1 << a.c.page_shift) - 1));
-    const float ks = E4M3 ? a.c.k_scale[r >> a.c.scale_shift] : 1.f;
-    const float vs = E4M3 ? a.c.v_scale[r >> a.c.scale_shift] : 1.f;
-    float s = 0.f;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += v;
+      }
+      __syncthreads();
+      if (lane == 31) sh.sums[warp] = up;
+      __syncthreads();
+      all = 0;
+      int64_t before = up - mine;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sh.sums[w];
+        all += sh.sums[w];
+      }
+      return before;
+    };
+    int64_t total = 0, mine = total_of(threadIdx.x), before;
+    if (a.batch <= kThreads) {
+      before = scan(mine, total);
+    } else {
+      int64_t sum = 0;
+      for (int b = threadIdx.x; b < a.batch; b += kThreads) sum += total_of(b);
+      scan(sum, total);
+    }
+    const int64_t least = (int64_t)kLeastWork * a.group;
+    const int64_t workers = min((int64_t)gridDim.x, max((int64_t)1, total / least));
+    if (worker < workers && total > 0) {
+      const int64_t cut[2] = {total * worker / workers, total * (worker + 1) / workers};
+      int64_t done = 0;
+      for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+        int64_t all;
+        if (a.batch > kThreads) {
+          mine = total_of(b0 + threadIdx.x);
+          before = done + scan(mine, all);
+          done += all;
+        }
 #pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(q[i], element<E4M3>(a.c.k, r * D + lane + 32 * i), s);
-    s = warp_sum(s) * ks * a.scale;
-    const float top = fmaxf(m, s), was = __expf(m - top), p = __expf(s - top);
-    m = top;
-    l = fmaf(l, was, p);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      acc[i] = fmaf(acc[i], was, p * vs * element<E4M3>(a.c.v, r * D + lane + 32 * i));
+        for (int i = 0; i < 2; ++i) {
+          const int64_t past = cut[i] - before;
+          if (past < 0 || past >= mine) continue;
+          // place `past` of context b
+          const int b = b0 + threadIdx.x;
+          const Context c = context_of<kRows>(a, make_int2(a.offsets[b], a.lengths[b]),
+                                              a.offsets[b + 1]);
+          const Weights w = weights_of<S::kStreams>(a, c);
+          const int64_t each = w.before(c.items);
+          const int kv = (int)(past / each);
+          const int64_t in = past - kv * each;
+          int lo = 0, hi = c.items;     // before(lo) <= in < before(hi)
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (w.before(mid) <= in) lo = mid; else hi = mid;
+          }
+          const Segment s = segment_of<kRows, kTile>(a, c, b, kv, lo);
+          const int64_t rest = in - w.before(lo) - w.cost, span = w.of(lo) - w.cost;
+          sh.place[i][0] = b;
+          sh.place[i][1] = kv;
+          sh.place[i][2] = lo;
+          sh.place[i][3] = rest <= 0 ? 0 : (int)min(rest * s.units / span, (int64_t)s.units);
+        }
+      }
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const __nv_bfloat16 y = __float2bfloat16_rn(acc[i] * inv);
-    a.out[row * a.out_stride + h * D + lane + 32 * i] = *reinterpret_cast<const uint16_t*>(&y);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  for (int i = threadIdx.x; i <= kRequests; i += kThreads) {
+    const int b = sh.place[0][0] + i;
+    if (b <= a.batch)
+      sh.request[i] = make_int2(a.offsets[b], b < a.batch ? a.lengths[b] : 0);
   }
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[(int64_t)row * a.q_heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (threadIdx.x == 0) {
+    a.records[worker].head.x = -1;
+    a.records[worker].tail.x = -1;
+    a.records[worker].some = 0;
+  }
+  __syncthreads();
+  const uint32_t tmem = sh.tmem;
+  Walker<kRows, kTile> walk;
+  walk.init(a, sh);
+  Segment seg;
+  // halves of 128 rows that a segment works on together
+  auto streams_of = [&](const Segment& s) { return s.rows > 128 ? 2 : 1; };
+
+  if (warp < 4 * S::kStreams) {
+    // ---------------- softmax ----------------
+    const int me = warp >> 2;                 // the stream of two, and the half of TMEM
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // of TMEM
+    uint32_t s_phase[2] = {0u, 0u}, o_phase = 0u, halves_phase = 0u;
+    int tile = 0;                             // of all tiles (sides), at the segment's start
+    int parity = 0;                           // of the segment (row_scale)
+    bool ok = true;
+    while (ok && walk.next(a, sh, seg)) {
+      const int streams = streams_of(seg), tiles = seg.u1 - seg.u0;
+      const bool mine = me < streams;
+      const int r = seg.row0 + me * 128 + row;          // of the context
+      const bool live = mine && me * 128 + row < seg.rows;
+      const int token = r / a.group, head = seg.kv * a.group + (r - token * a.group);
+      // tokens [lo, hi) are seen (rows behind the last take anything; a warp of such rows
+      // only keeps step)
+      const bool works = __any_sync(0xffffffffu, live);
+      const int hi = live ? (int)min((int64_t)seg.place + token + 1, (int64_t)seg.end) : INT_MAX;
+      const int lo = live && a.window > 0
+                         ? (int)max((int64_t)seg.place + token + 1 - a.window, (int64_t)0) : 0;
+      float top = -INFINITY, sum = 0.f;
+      const uint32_t o_at = tmem + lanes + S::kSOut + me * D;
+      if (mine && tiles > 0) {
+        float factor = 0.f;
+        for (int i = 0; ok && i < tiles; ++i) {
+          const int slot = streams == 2 ? me : i & 1;
+          const uint32_t s_at = tmem + lanes + slot * kTile;
+          ok = warp_wait(&sh.s_full[slot], s_phase[slot], sh, a.err, kErrTimeoutEpilogue);
+          if (!ok) break;
+          s_phase[slot] ^= 1u;
+          if (!works) {
+            if (streams == 1 && i > 0)
+              ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
+            if (!ok) break;
+            warp_arrive(&sh.p_full[slot]);
+            o_phase ^= 1u;
+            continue;
+          }
+          tc_fence_after_sync();
+          if (i == 0) factor = sh.row_scale[parity][me * 128 + row];
+          const Side& side = sh.side[(tile + i) & (kSides - 1)];
+          // (above 0, so that it leaves the -inf of a token that is not seen as it is)
+          const float c = fmaxf(factor * side.key_up, 0x1p-120f), f = side.value_exp;
+          // what this row sees of the tile
+          const int first = seg.start + (seg.u0 + i) * kTile;
+          constexpr uint32_t kAll = kTile == 128 ? 0xffffffffu : 0xffffu;
+          const bool all_there = (side.mask[0] & side.mask[1] & side.mask[2] & side.mask[3]) == kAll;
+          const bool clear =
+              __all_sync(0xffffffffu, all_there && lo <= first && hi - first >= kTile);
+          // 64 scores at a time, read once for their maximum and again for the weights (128
+          // would not fit the registers)
+          float s[64];
+          auto get = [&](int h) {
+            tmem_load(s_at + 64 * h, s);
+            if (KIND == kTokenScales) {
+              const float4* const scales = reinterpret_cast<const float4*>(
+                  sh.key_scale[(tile + i) & (kSides - 1)] + 64 * h);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float4 v = scales[j];
+                s[4 * j] *= v.x;
+                s[4 * j + 1] *= v.y;
+                s[4 * j + 2] *= v.z;
+                s[4 * j + 3] *= v.w;
+              }
+            }
+            if (!clear) {
+              constexpr int kBits = kTile / kLoadWarps;   // tokens of a mask
+#pragma unroll
+              for (int w = 0; w < 64 / kBits; ++w) {
+                const int at = first + 64 * h + w * kBits;
+                const int from = min(max(lo - at, 0), kBits), to = min(max(hi - at, 0), kBits);
+                uint32_t bits = side.mask[h * (64 / kBits) + w];
+                bits &= to >= 32 ? 0xffffffffu : (1u << to) - 1u;
+                bits &= from >= 32 ? 0u : ~((1u << from) - 1u);
+#pragma unroll
+                for (int j = 0; j < kBits; ++j)
+                  if (!((bits >> j) & 1u)) s[w * kBits + j] = -INFINITY;
+              }
+            }
+          };
+          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = 0; h < kTile / 64; ++h) {
+            get(h);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) m[j & 3] = fmaxf(m[j & 3], s[j]);
+          }
+          const float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+          const float z = fmaf(high, c, f);
+          if (streams == 1 && i > 0) {
+            // the last tile's products, before O is touched and before the barrier can get
+            // a phase further (with two streams, these scores came after them)
+            ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
+            if (!ok) break;
+            tc_fence_after_sync();
+          }
+          if (__any_sync(0xffffffffu, z > top + kMostWeight)) {
+            const float next = fmaxf(top, z - kNewWeight);
+            const float down = top == -INFINITY ? 0.f : exp2_approx(top - next);
+            top = next;
+            sum *= down;
+            if (i > 0) {
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) {
+                float o[32];
+                tmem_load(o_at + 32 * j, o);
+                uint32_t w[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(o[k] * down);
+                tmem_store(o_at + 32 * j, w);
+              }
+            }
+          }
+          const float by = f - (top == -INFINITY ? 0.f : top);
+          float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < kTile / 64; ++h) {
+            if (kTile > 64) get(h);
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float w0 = exp2_approx(fmaf(s[2 * j], c, by));
+              const float w1 = exp2_approx(fmaf(s[2 * j + 1], c, by));
+              add[2 * (j & 1)] += w0;
+              add[2 * (j & 1) + 1] += w1;
+              p[j] = kIsBf16 ? pack_bf16(w0, w1) : pack_f16(w0, w1);
+            }
+            tmem_store(s_at + 32 * h, p);
+          }
+          sum = fmaf((add[0] + add[1]) + (add[2] + add[3]), exp2_approx(-f), sum);
+          tmem_store_wait();
+          tc_fence_before_sync();
+          warp_arrive(&sh.p_full[slot]);
+          o_phase ^= 1u;
+        }
+        if (!ok) break;
+        // the last products (o_phase has moved past them)
+        ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
+        if (!ok) break;
+        tc_fence_after_sync();
+      }
+      // the other half's tiles and segments, counted
+      if (tiles > 0) {
+        if (!mine || streams == 2) {
+          if (streams == 2) {
+            s_phase[me ^ 1] ^= tiles & 1;
+          } else {
+            s_phase[0] ^= (uint32_t)(((tiles + 1) >> 1) & 1);
+            s_phase[1] ^= (uint32_t)((tiles >> 1) & 1);
+          }
+        }
+        parity ^= 1;
+        tile += tiles;
+      }
+      if (S::kStreams == 2 && streams == 1 && tiles > 0) {
+        // the half without rows waits for the other: barriers it did not wait on have
+        // completed every phase of the segment before it counts on them again
+        warp_arrive(&sh.halves);
+        ok = warp_wait(&sh.halves, halves_phase, sh, a.err, kErrTimeoutEpilogue);
+        if (!ok) break;
+        halves_phase ^= 1u;
+      }
+      if (!mine) continue;
+      const bool whole = seg.whole();
+      const int64_t slot = 2 * worker + (seg.u0 == 0 ? 1 : 0);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int64_t to = (int64_t)(seg.token0 + token);
+      uint16_t* const out = a.out + to * a.out_stride + (int64_t)head * D;
+      float4* const part = reinterpret_cast<float4*>(a.parts) +
+                           slot * (kRows * D / 4) + me * 128 + row;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        float o[32];
+        __syncwarp();
+        if (tiles > 0) {
+          tmem_load(o_at + 32 * j, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (live && whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(out + 32 * j + 8 * k) =
+                make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv),
+                           pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                           pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                           pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        } else if (live) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            part[(8 * j + k) * kRows] =
+                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (tiles > 0) {
+        tc_fence_before_sync();
+        warp_arrive(&sh.o_empty[me]);
+      }
+      if (live) {
+        if (!whole) a.stats[slot * kRows + me * 128 + row] = make_float2(top, sum);
+        else if (a.lse != nullptr)
+          a.lse[to * a.q_heads + head] =
+              sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      }
+      if (threadIdx.x == 0) {
+        Record& rec = a.records[worker];
+        rec.some = 1;
+        if (whole) {
+        } else if (seg.u0 > 0) {
+          rec.head = make_int4(seg.b, seg.kv, seg.item, 0);
+        } else {
+          rec.tail = make_int4(seg.b, seg.kv, seg.item, 0);
+          rec.token0 = seg.token0;
+          rec.row0 = seg.row0;
+          rec.rows = seg.rows;
+        }
+      }
+    }
+  } else if (warp >= kLoadWarp0 && warp < kMmaWarp) {
+    // ---------------- q, keys and values ----------------
+    const int w = warp - kLoadWarp0;
+    constexpr int kMine = kTile / kLoadWarps;            // tokens of a warp
+    constexpr int kRowBytes = D * (kIsBf16 ? 2 : 1);
+    constexpr int kChunks = kRowBytes / 16;              // 16-byte pieces of a row
+    constexpr int kAtOnce = 32 / kChunks > 0 ? 32 / kChunks : 1;   // rows of one load
+    constexpr int kLoads = kMine * kChunks / 32;         // of a lane, of a tile
+    const int chunk = lane % kChunks, sub = lane / kChunks;
+    uint32_t k_phase = 1u, v_phase = 1u;   // (the stages are empty at first)
+    int stage = 0;
+    uint32_t q_phase = 1u;
+    int parity = 0, tile = 0;
+    bool ok = true;
+    // A tile's tokens, one a lane: its cache row and whether it is there.
+    struct Tokens {
+      uint32_t row;
+      bool here;
+    };
+    Segment next;          // the segment of the tile that is asked for
+    int at = 0;            // that tile in it
+    bool more = walk.next(a, sh, next);
+    while (more && next.u1 == next.u0) more = walk.next(a, sh, next);
+    auto look = [&]() -> int32_t {
+      const int64_t token = (int64_t)next.start + (int64_t)(next.u0 + at) * kTile + w * kMine + lane;
+      return more && lane < kMine && token >= next.begin && token < next.end
+                 ? a.c.table[next.b * a.c.table_stride + (token >> a.c.page_shift)]
+                 : -1;
+    };
+    auto tokens = [&](int32_t entry) -> Tokens {
+      const uint32_t token = (uint32_t)next.start + (uint32_t)(next.u0 + at) * kTile + w * kMine + lane;
+      Tokens t;
+      t.here = (uint32_t)entry < (uint32_t)a.c.pages;
+      t.row = t.here ? (((uint32_t)entry * a.c.heads + next.kv) << a.c.page_shift) +
+                           (token & ((1u << a.c.page_shift) - 1u))
+                     : 0u;
+      return t;
+    };
+    auto advance = [&]() {
+      if (++at >= next.u1 - next.u0) {
+        at = 0;
+        do more = walk.next(a, sh, next);
+        while (more && next.u1 == next.u0);
+      }
+    };
+    // place of 16-byte unit u of a row in an operand with `rows` rows: blocks of 128 bytes
+    auto place = [&](uint32_t base, int rows, int r, int u) -> uint32_t {
+      return base + (u >> 3) * (rows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+    };
+    uint4 kreg[kIsBf16 ? 1 : kLoads], vreg[kIsBf16 ? 1 : kLoads];
+    auto fetch = [&](const void* cache, const Tokens& t, uint4* reg) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kAtOnce + sub;
+        const uint32_t row = __shfl_sync(0xffffffffu, t.row, r);
+        const bool here = __shfl_sync(0xffffffffu, (int)t.here, r) != 0;
+        reg[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (here)
+          reg[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) +
+                                                   (uint64_t)row * kRowBytes + chunk * 16);
+      }
+    };
+    auto copy = [&](const void* cache, const Tokens& t, uint32_t base) {   // bf16: straight
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kAtOnce + sub;
+        const uint32_t row = __shfl_sync(0xffffffffu, t.row, r);
+        const bool here = __shfl_sync(0xffffffffu, (int)t.here, r) != 0;
+        cp_async_16(place(base, kTile, w * kMine + r, chunk),
+                    static_cast<const uint8_t*>(cache) + (uint64_t)row * kRowBytes + chunk * 16,
+                    here ? 16u : 0u);
+      }
+    };
+    // codes to fp16: `by` an fp16 pair (ROUNDED: an fp32 factor) of the lane's token
+    auto convert = [&](const uint4* reg, uint32_t by, uint32_t base, auto rounded) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kAtOnce + sub;
+        const uint32_t up = __shfl_sync(0xffffffffu, by, r);
+        const uint32_t in[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[j] = e4m3x2_to_f16(in[j >> 1] >> (16 * (j & 1)));
+          if (decltype(rounded)::value) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+            h[j] = pack_f16(f.x * __uint_as_float(up), f.y * __uint_as_float(up));
+          } else {
+            h[j] = mul_f16(h[j], up);
+          }
+        }
+        // (the lanes of the second 128 bytes put their units down in the other order: all
+        // banks are used)
+        const bool swap = ((2 * chunk) & 8) != 0;
+        const int row = w * kMine + r;
+        const uint32_t at0 = place(base, kTile, row, 2 * chunk + (swap ? 1 : 0));
+        const uint32_t at1 = place(base, kTile, row, 2 * chunk + (swap ? 0 : 1));
+        st_shared_16(at0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2],
+                     swap ? h[7] : h[3]);
+        st_shared_16(at1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6],
+                     swap ? h[3] : h[7]);
+      }
+    };
+    // q of a segment: a warp a quarter of the rows
+    auto load_q = [&](const Segment& s) {
+      constexpr int kLanes = D / 8, kQAtOnce = 32 / kLanes;   // lanes of a row, rows of a load
+      const int halves = streams_of(s);
+      const int lr = lane / kLanes, u = lane % kLanes;
+      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+      const float scale = fabsf(a.scale) * 1.4426950408889634f;
+      const int rows = halves * 32;
+#pragma unroll 8
+      for (int i = 0; i < rows / kQAtOnce; ++i) {
+        const int r = w * rows + i * kQAtOnce + lr;
+        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+        if (r < s.rows) {
+          const int flat = s.row0 + r, token = flat / a.group;
+          const int head = s.kv * a.group + flat - token * a.group;
+          raw = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.token0 + token) * a.q_stride +
+                                                (int64_t)head * D + u * 8);
+        }
+        uint32_t x[4] = {raw.x ^ flip, raw.y ^ flip, raw.z ^ flip, raw.w ^ flip};
+        float factor = scale;
+        if (!kIsBf16) {
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // a power of two brings the head's largest element into [2^8, 2^9)
+          const int e = min(max(exponent(top), -110), 126);
+          const float down = power(-e), up = power(8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[j] = pack_f16(bf16_lo(x[j]) * down * up, bf16_hi(x[j]) * down * up);
+          factor *= power(e - 8);
+        }
+        st_shared_16(place(q_at + (r >> 7) * S::kQBytes, 128, r & 127, u), x[0], x[1], x[2], x[3]);
+        if (u == 0) sh.row_scale[parity][r] = factor;
+      }
+    };
+
+    Tokens now{0u, false}, then{0u, false};
+    float ks = 0.f, vs = 0.f;                // scales of the lane's token of the next tile
+    auto ask_scales = [&](const Tokens& t) {
+      ks = vs = 0.f;
+      if (!kIsBf16 && t.here) {
+        ks = a.c.k_scale[t.row >> a.c.scale_shift];
+        vs = a.c.v_scale[t.row >> a.c.scale_shift];
+      }
+    };
+    Segment cur = next;
+    bool fresh = true, running = more;      // the current tile is the first of its segment
+    int32_t entry = -1;
+    if (running) {
+      now = tokens(look());
+      cur = next;
+      if (kIsBf16) {
+        // (nothing is asked for ahead: the stages are)
+      } else {
+        fetch(a.c.k, now, kreg);
+        fetch(a.c.v, now, vreg);
+        ask_scales(now);
+      }
+      advance();
+      entry = look();
+    }
+    bool pending = false;                   // bf16: a tile's copies are under way
+    int pending_stage = 0;
+    while (running && ok) {
+      if (fresh) {
+        if (kIsBf16 && pending) {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          fence_proxy_async_smem();
+          warp_arrive(&sh.v_full[pending_stage]);
+          pending = false;
+        }
+        ok = warp_wait(&sh.q_empty, q_phase, sh, a.err, kErrTimeoutProducer);
+        if (!ok) break;
+        load_q(cur);
+        fence_proxy_async_smem();
+        warp_arrive(&sh.q_full);
+        q_phase ^= 1u;
+        parity ^= 1;
+      }
+      // the tile's factors and masks
+      Side& side = sh.side[tile & (kSides - 1)];
+      const unsigned mask = __ballot_sync(0xffffffffu, now.here);
+      uint32_t kby = 0u, vby = 0u;
+      int e = 0, f = 0;
+      if (!kIsBf16) {
+        const int none = -1000;
+        int ke = now.here && ks > 0.f ? max(exponent(ks), kLeastExponent) : none;
+        int ve = now.here && vs > 0.f ? max(exponent(vs), kLeastExponent) : none;
+        const int ktop = __reduce_max_sync(0xffffffffu, ke);
+        const int vtop = __reduce_max_sync(0xffffffffu, ve);
+        if (lane == 0) {
+          sh.maxima[tile & 1][w][0] = ktop;
+          sh.maxima[tile & 1][w][1] = vtop;
+        }
+        warp_arrive(&sh.maxed);
+        ok = warp_wait(&sh.maxed, tile & 1, sh, a.err, kErrTimeoutProducer);
+        if (!ok) break;
+        e = f = none;
+#pragma unroll
+        for (int i = 0; i < kLoadWarps; ++i) {
+          e = max(e, sh.maxima[tile & 1][i][0]);
+          f = max(f, sh.maxima[tile & 1][i][1]);
+        }
+        // the largest codes (448) times what is left of the scales: below 2^15, or 2^16
+        e = e == none || KIND == kTokenScales ? 0 : e - 6;
+        f = f == none ? 0 : f - 6;
+        auto pair = [](int x) -> uint32_t {   // 2^x as an fp16 pair (0 below fp16)
+          if (x < -24) return 0u;
+          const __half h = __float2half_rn(power(x));
+          return (uint32_t)*reinterpret_cast<const uint16_t*>(&h) * 0x10001u;
+        };
+        kby = KIND == kTokenScales ? 0x3c003c00u : ke == none ? 0u : pair(ke - e);
+        if (KIND == kTokenScales)
+          vby = ve == none ? 0u : __float_as_uint(vs * power(-f));
+        else
+          vby = ve == none ? 0u : pair(ve - f);
+      }
+      if (lane == 0) {
+        side.mask[w] = mask;
+        if (w == 0) {
+          side.key_up = power(e);
+          side.value_exp = (float)f;
+        }
+      }
+      if (KIND == kTokenScales && lane < kMine)
+        sh.key_scale[tile & (kSides - 1)][w * kMine + lane] = now.here ? ks : 0.f;
+
+      const uint32_t k_to = k_at + stage * S::kTileBytes, v_to = v_at + stage * S::kTileBytes;
+      ok = warp_wait(&sh.k_empty[stage], k_phase, sh, a.err, kErrTimeoutProducer);
+      if (!ok) break;
+      if (kIsBf16) {
+        copy(a.c.k, now, k_to);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (pending) {   // the last tile's values have landed
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          fence_proxy_async_smem();
+          warp_arrive(&sh.v_full[pending_stage]);
+        }
+        ok = warp_wait(&sh.v_empty[stage], v_phase, sh, a.err, kErrTimeoutProducer);
+        if (!ok) break;
+        copy(a.c.v, now, v_to);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fence_proxy_async_smem();
+        warp_arrive(&sh.k_full[stage]);
+        pending = true;
+        pending_stage = stage;
+      } else {
+        convert(kreg, kby, k_to, std::false_type{});
+        fence_proxy_async_smem();
+        warp_arrive(&sh.k_full[stage]);
+      }
+      // the next tile
+      running = more;
+      fresh = at == 0;
+      if (more) {
+        then = tokens(entry);
+        cur = next;
+        if (!kIsBf16) {
+          fetch(a.c.k, then, kreg);
+          ask_scales(then);
+        }
+        advance();
+        entry = look();
+      }
+      if (!kIsBf16) {
+        ok = warp_wait(&sh.v_empty[stage], v_phase, sh, a.err, kErrTimeoutProducer);
+        if (!ok) break;
+        if (KIND == kTokenScales) convert(vreg, vby, v_to, std::true_type{});
+        else convert(vreg, vby, v_to, std::false_type{});
+        fence_proxy_async_smem();
+        warp_arrive(&sh.v_full[stage]);
+        if (running) fetch(a.c.v, then, vreg);
+      }
+      now = then;
+      ++tile;
+      if (++stage == S::kStages) {
+        stage = 0;
+        k_phase ^= 1u;
+        v_phase ^= 1u;
+      }
+    }
+    if (kIsBf16) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (ok && pending) {
+        fence_proxy_async_smem();
+        warp_arrive(&sh.v_full[pending_stage]);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- products ----------------
+    uint32_t k_phase = 0u, v_phase = 0u, q_phase = 0u, p_phase[2] = {0u, 0u};
+    uint32_t oe_phase[2] = {1u, 1u};        // (O is free at first)
+    int k_stage = 0, v_stage = 0;
+    bool ok = true;
+    constexpr uint32_t kQk = idesc_f16(kIsBf16, kTile, false), kPv = idesc_f16(kIsBf16, D, true);
+    while (ok && walk.next(a, sh, seg)) {
+      const int streams = streams_of(seg), tiles = seg.u1 - seg.u0;
+      if (tiles == 0) continue;
+      const int tasks = tiles * streams;
+      // task t: the scores, then the weights and products, of stream t % streams and tile
+      // t / streams, in half t % 2 of the scores' tensor memory
+      auto scores = [&](int t) -> bool {
+        const int stream = streams == 2 ? t & 1 : 0;
+        if (stream == 0 &&
+            !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
+          return false;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t d = tmem + (t & 1) * kTile;
+          const uint32_t qs = q_at + stream * S::kQBytes, ks = k_at + k_stage * S::kTileBytes;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            mma_f16_ss(d, smem_desc_k_sw128(qs + (i >> 2) * (128 * 128) + (i & 3) * 32),
+                       smem_desc_k_sw128(ks + (i >> 2) * (kTile * 128) + (i & 3) * 32), kQk,
+                       i > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&sh.s_full[t & 1]));
+          if (stream == streams - 1) mma_commit(smem_u32(&sh.k_empty[k_stage]));
+          if (t == tasks - 1) mma_commit(smem_u32(&sh.q_empty));
+        }
+        __syncwarp();
+        if (stream == streams - 1 && ++k_stage == S::kStages) {
+          k_stage = 0;
+          k_phase ^= 1u;
+        }
+        return true;
+      };
+      ok = warp_wait(&sh.q_full, q_phase, sh, a.err, kErrTimeoutMma);
+      q_phase ^= 1u;
+      if (ok) ok = scores(0);
+      if (ok && tasks > 1) ok = scores(1);
+      for (int t = 0; ok && t < tasks; ++t) {
+        const int stream = streams == 2 ? t & 1 : 0, slot = t & 1;
+        if (t < streams) {   // O: the last segment's has been read
+          ok = warp_wait(&sh.o_empty[stream], oe_phase[stream], sh, a.err, kErrTimeoutMma);
+          if (!ok) break;
+          oe_phase[stream] ^= 1u;
+        }
+        if (stream == 0) {
+          ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a.err, kErrTimeoutMma);
+          if (!ok) break;
+        }
+        ok = warp_wait(&sh.p_full[slot], p_phase[slot], sh, a.err, kErrTimeoutMma);
+        if (!ok) break;
+        p_phase[slot] ^= 1u;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t d = tmem + S::kSOut + stream * D, p = tmem + slot * kTile;
+          const uint32_t vs = v_at + v_stage * S::kTileBytes;
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_f16_ts(d, p + 8 * i, smem_desc_mn_sw128(vs + i * 2048, kTile * 128), kPv,
+                       t >= streams || i > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&sh.o_full[stream]));
+          if (stream == streams - 1) mma_commit(smem_u32(&sh.v_empty[v_stage]));
+        }
+        __syncwarp();
+        if (stream == streams - 1 && ++v_stage == S::kStages) {
+          v_stage = 0;
+          v_phase ^= 1u;
+        }
+        if (t + 2 < tasks) ok = scores(t + 2);
+      }
+    }
+    // every product has ended before tensor memory and shared memory are given back
+    if (lane == 0) mma_commit(smem_u32(&sh.drain));
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait_bounded(smem_u32(&sh.drain), 0, &no_abort, a.err, kErrTimeoutDrain);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, S::kCols);
 }
+
+// Joins the pieces of the items that several CTAs share: the one that CTA blockIdx.x
+// began, 32 of its rows a block, four elements of a row a thread at a time.
+constexpr int kJoinThreads = 256;
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a, int workers) {
+  constexpr int kRows = Shape<KIND, D>::kRows;
+  pdl_wait();
+  const int w = blockIdx.x;
+  const Record rec = a.records[w];
+  if (rec.tail.x < 0) return;
+  // the slots of the pieces: CTA w's, and those of the CTAs after it that went on (one
+  // between them can have got nothing)
+  __shared__ int slots[kWorkers];
+  __shared__ int count;
+  if (threadIdx.x == 0) {
+    int n = 0;
+    slots[n++] = 2 * w + 1;
+    for (int i = w + 1; i < workers; ++i) {
+      const int4 h = a.records[i].head;
+      if (h.x == rec.tail.x && h.y == rec.tail.y && h.z == rec.tail.z) slots[n++] = 2 * i;
+      else if (a.records[i].some != 0) break;
+    }
+    count = n;
+  }
+  __syncthreads();
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31);
+  if (row >= rec.rows) return;
+  float top = -INFINITY;
+  for (int i = 0; i < count; ++i) top = fmaxf(top, a.stats[slots[i] * kRows + row].x);
+  float sum = 0.f;
+  for (int i = 0; i < count; ++i) {
+    const float2 s = a.stats[slots[i] * kRows + row];
+    if (s.x != -INFINITY) sum = fmaf(s.y, exp2_approx(s.x - top), sum);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int r = rec.row0 + row, token = r / a.group;
+  const int head = rec.tail.y * a.group + (r - token * a.group);
+  const int64_t to = rec.token0 + token;
+  for (int d = threadIdx.x >> 5; d < D / 4; d += kJoinThreads / 32) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < count; ++i) {
+      const int64_t slot = slots[i];
+      const float m = a.stats[slot * kRows + row].x;
+      const float by = m == -INFINITY ? 0.f : exp2_approx(m - top);
+      const float4 v = reinterpret_cast<const float4*>(a.parts)[(slot * (D / 4) + d) * kRows + row];
+      o.x = fmaf(v.x, by, o.x);
+      o.y = fmaf(v.y, by, o.y);
+      o.z = fmaf(v.z, by, o.z);
+      o.w = fmaf(v.w, by, o.w);
+    }
+    *reinterpret_cast<uint2*>(a.out + to * a.out_stride + (int64_t)head * D + 4 * d) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  }
+  if (threadIdx.x < 32 && a.lse != nullptr)
+    a.lse[to * a.q_heads + head] =
+        sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int KIND, int D>
+int launch(const Args& a, cudaStream_t stream) {
+  using S = Shape<KIND, D>;
+  // the opt-in to more than 48 KB of shared memory, once per device
+  static std::atomic<uint64_t> opted{0};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return -3;
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if ((opted.load(std::memory_order_relaxed) & bit) == 0 || device >= 64) {
+    if (cudaFuncSetAttribute(prompt_attention_kernel<KIND, D>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::kSmemBytes) != cudaSuccess)
+      return -3;
+    opted.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaError_t e = launch_kernel(true, dim3(kWorkers), dim3(kThreads), S::kSmemBytes, stream,
+                                prompt_attention_kernel<KIND, D>, a);
+  if (e != cudaSuccess) return -3;
+  e = launch_kernel(true, dim3(kWorkers, S::kRows / 32), dim3(kJoinThreads), 0, stream,
+                    prompt_join_kernel<KIND, D>, a, kWorkers);
+  return e == cudaSuccess ? 0 : -3;
+}
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+size_t item_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 
 }  // namespace
 
-size_t prompt_attention_ws_bytes(int, int, int) { return 16; }
+size_t prompt_attention_ws_bytes(int, int head_dim, int) {
+  const size_t rows = 2 * kWorkers * item_rows(head_dim);
+  return align256(kWorkers * sizeof(Record)) + rows * sizeof(float2) +
+         rows * head_dim * sizeof(float);
+}
 
 int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int rows,
                             int q_heads, const int32_t* offsets, const int32_t* lengths, int batch,
                             float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
-                            void*, cudaStream_t stream) {
+                            void* ws, cudaStream_t stream) {
   Args a{};
   a.c = c;
   a.q = q;
@@ -113,25 +1200,33 @@ int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_str
   a.rows = rows;
   a.q_heads = q_heads;
   a.batch = batch;
+  a.group = q_heads / c.heads;
   a.offsets = offsets;
   a.lengths = lengths;
   a.scale = scale;
   a.window = window;
   a.out = out;
   a.lse = lse;
-  const int64_t blocks = ((int64_t)rows * q_heads + kWarps - 1) / kWarps;
-  void (*kernel)(Args) = nullptr;
-  if (c.e4m3)
-    kernel = c.head_dim == 64    ? prompt_attention_kernel<true, 64>
-             : c.head_dim == 128 ? prompt_attention_kernel<true, 128>
-                                 : prompt_attention_kernel<true, 256>;
-  else
-    kernel = c.head_dim == 64    ? prompt_attention_kernel<false, 64>
-             : c.head_dim == 128 ? prompt_attention_kernel<false, 128>
-                                 : prompt_attention_kernel<false, 256>;
-  const cudaError_t e =
-      launch_kernel(true, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, kernel, a);
-  return e == cudaSuccess ? 0 : -3;
+  uint8_t* const p = static_cast<uint8_t*>(ws);
+  const size_t records = align256(kWorkers * sizeof(Record));
+  a.records = reinterpret_cast<Record*>(p);
+  a.stats = reinterpret_cast<float2*>(p + records);
+  a.parts = reinterpret_cast<float*>(p + records +
+                                     2 * kWorkers * item_rows(c.head_dim) * sizeof(float2));
+  a.err = device_error_word();
+  if (a.err == nullptr) return -3;
+  const int kind = !c.e4m3 ? kBf16 : c.scale_shift > 0 ? kPageScales : kTokenScales;
+  if (c.head_dim == 64)
+    return kind == kBf16         ? launch<kBf16, 64>(a, stream)
+           : kind == kPageScales ? launch<kPageScales, 64>(a, stream)
+                                 : launch<kTokenScales, 64>(a, stream);
+  if (c.head_dim == 128)
+    return kind == kBf16         ? launch<kBf16, 128>(a, stream)
+           : kind == kPageScales ? launch<kPageScales, 128>(a, stream)
+                                 : launch<kTokenScales, 128>(a, stream);
+  return kind == kBf16         ? launch<kBf16, 256>(a, stream)
+         : kind == kPageScales ? launch<kPageScales, 256>(a, stream)
+                               : launch<kTokenScales, 256>(a, stream);
 }
 
 }  // namespace moe

@@ -128,13 +128,13 @@ def kv_write_page_ref(pages, scales, x, slots):
 
 def prompt_attention_ref(q, k_pages, v_pages, k_scale, v_scale, table, lengths, offsets, scale,
                          window=0):
-    """(out, lse, spread, reach) as of paged_attention_ref for the rows
-    offsets[b]..offsets[b + 1] of q [rows, Hq, D], the last tokens of context b; rows
-    behind the last are zeros."""
+    """(out, lse, spread, reach, mass): as of paged_attention_ref for the rows
+    offsets[b]..offsets[b + 1] of q [rows, Hq, D], the last tokens of context b, and
+    mass [rows, Hq, D] = max_j p_j sum_j |v_j|; rows behind the last are zeros."""
     q = np.asarray(q, np.float64)
     rows, hq, d = q.shape
     group = hq // k_pages.shape[1]
-    out, spread = np.zeros((rows, hq, d)), np.zeros((rows, hq, d))
+    out, spread, mass = (np.zeros((rows, hq, d)) for _ in range(3))
     lse, reach = np.full((rows, hq), -np.inf), np.zeros((rows, hq))
     for b, n in enumerate(lengths):
         s, e = int(offsets[b]), int(offsets[b + 1])
@@ -156,10 +156,11 @@ def prompt_attention_ref(q, k_pages, v_pages, k_scale, v_scale, table, lengths, 
             p = w / w.sum(-1, keepdims=True)
             at_rows = np.arange(s, e)[some]
             out[at_rows, h], spread[at_rows, h] = p @ vh, p @ np.abs(vh)
+            mass[at_rows, h] = p.max(-1, keepdims=True) * (seen[some] @ np.abs(vh))
             lse[at_rows, h] = m[some] + np.log(w.sum(-1))
             r = np.abs(scale) * (np.abs(q[s:e, h]) @ np.abs(kh).T)
             reach[s:e, h] = np.where(seen, r, 0.0).max(-1)
-    return out, lse, spread, reach
+    return out, lse, spread, reach, mass
 
 
 def kv_plan_ref(state, new, table, stack, page_size, rows):
