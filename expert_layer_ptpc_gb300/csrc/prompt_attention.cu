@@ -106,6 +106,29 @@ struct Shape {
   static_assert(kSOut + kStreams * D <= kCols, "tensor memory");
 };
 
+// A context's rows: place of its first new token, rows and items of a kv head.
+struct Context {
+  int token0;      // row of q of its first new token
+  int place;       // that token's place in the context (negative: before it)
+  int rows;        // new tokens x group
+  int items;
+};
+// An item, or a part of one: units [u0, u1) of `units` tiles.
+struct Segment {
+  int b, kv, item;
+  int token0, place, row0, rows;   // rows [row0, row0 + rows) of the context
+  int begin, end, start;           // tokens that take part; the first tile's first
+  int u0, u1, units;
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
+};
+
+// Where a warp is in its CTA's run: the next place, and the run's end.
+struct Walk {
+  int b, kv, item, unit;
+  int end[4];
+  Context c;         // of context b
+};
+
 // A tile's masks and factors.
 struct Side {
   uint32_t mask[4];      // which tokens are there: those of a loading warp each
@@ -115,17 +138,21 @@ struct Side {
 
 struct Shared {
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t halves, maxed, drain;
   uint32_t tmem;
   int abort;
   Side side[kSides];
   float key_scale[kSides][128];      // token scales
-  float row_scale[2][256];
+  float row_scale[256];
   int maxima[2][kLoadWarps][2];
   int2 request[kRequests + 1];       // (first row, length)
   int64_t sums[kThreads / 32 + 1];
-  int place[2][4];                   // the run: first context, kv head, tile, unit; and its end
+  int place[2][4];                   // the run: first context, kv head, item, unit; and its end
+  // each warp's walk, and the segments that it works on and looks ahead to (in shared
+  // memory: they are wanted once a segment, and registers are scarce)
+  Walk walk[kThreads / 32];
+  Segment segment[kThreads / 32][2];
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -203,22 +230,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
 }
 
 // ---- the work ----
-// A context's rows: place of its first new token, rows and items of a kv head.
-struct Context {
-  int token0;      // row of q of its first new token
-  int place;       // that token's place in the context (negative: before it)
-  int rows;        // new tokens x group
-  int items;
-};
-// An item, or a part of one: units [u0, u1) of `units` tiles.
-struct Segment {
-  int b, kv, item;
-  int token0, place, row0, rows;   // rows [row0, row0 + rows) of the context
-  int begin, end, start;           // tokens that take part; the first tile's first
-  int u0, u1, units;
-  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
-};
-
 template <int ROWS>
 __device__ __forceinline__ Context context_of(const Args& a, int2 from, int to) {
   Context c;
@@ -278,56 +289,41 @@ __device__ __forceinline__ Segment segment_of(const Args& a, const Context& c, i
   return s;
 }
 
-// Hands out a CTA's run of the work, segment by segment.
+// Hands out a CTA's run of the work to a warp, segment by segment.
 template <int ROWS, int TILE>
-struct Walker {
-  int b, kv, item, unit;      // the next place
-  int end[4];
-  Context c;
-
-  __device__ __forceinline__ int2 request(const Args& a, const Shared& sh, int first, int i) const {
-    const int at = i - first;
-    if (at <= kRequests) return sh.request[at];
-    return make_int2(a.offsets[i], i < a.batch ? a.lengths[i] : 0);
-  }
-  __device__ __forceinline__ void look(const Args& a, const Shared& sh, int first) {
-    c = context_of<ROWS>(a, request(a, sh, first, b), request(a, sh, first, b + 1).x);
-  }
-  __device__ __forceinline__ void init(const Args& a, const Shared& sh) {
-    b = sh.place[0][0];
-    kv = sh.place[0][1];
-    item = sh.place[0][2];
-    unit = sh.place[0][3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) end[i] = sh.place[1][i];
-    if (b < a.batch) look(a, sh, b);
-  }
-  __device__ __forceinline__ bool next(const Args& a, const Shared& sh, Segment& s) {
-    for (;;) {
-      if (b >= a.batch || (b == end[0] && kv == end[1] && item == end[2] && unit >= end[3]))
-        return false;
-      const bool last = b == end[0] && kv == end[1] && item == end[2];
-      s = segment_of<ROWS, TILE>(a, c, b, kv, item);
-      s.u0 = min(unit, s.units);
-      if (last) s.u1 = min(end[3], s.units);
-      unit = 0;
-      if (last) {
-        b = a.batch;
-      } else if (++item >= c.items) {
-        item = 0;
-        if (++kv == a.c.heads) {
-          kv = 0;
-          const int first = sh.place[0][0];
-          do {
-            if (++b >= a.batch) break;
-            look(a, sh, first);
-          } while (c.items == 0);
-        }
+__device__ __forceinline__ bool next_of(const Args& a, const Shared& sh, Walk& w, Segment& s) {
+  const int first = sh.place[0][0];
+  for (;;) {
+    const bool last = w.b == w.end[0] && w.kv == w.end[1] && w.item == w.end[2];
+    if (w.b >= a.batch || (last && w.unit >= w.end[3])) return false;
+    s = segment_of<ROWS, TILE>(a, w.c, w.b, w.kv, w.item);
+    s.u0 = min(w.unit, s.units);
+    if (last) s.u1 = min(w.end[3], s.units);
+    w.unit = 0;
+    if (last) {
+      w.b = a.batch;
+    } else if (++w.item >= w.c.items) {
+      w.item = 0;
+      if (++w.kv == a.c.heads) {
+        w.kv = 0;
+        do {
+          if (++w.b >= a.batch) break;
+          const int at = w.b - first;
+          int2 from, to;
+          if (at < kRequests) {
+            from = sh.request[at];
+            to = sh.request[at + 1];
+          } else {
+            from = make_int2(a.offsets[w.b], a.lengths[w.b]);
+            to.x = a.offsets[w.b + 1];
+          }
+          w.c = context_of<ROWS>(a, from, to.x);
+        } while (w.c.items == 0);
       }
-      if (s.u1 > s.u0 || s.units == 0) return true;
     }
+    if (s.u1 > s.u0 || s.units == 0) return true;
   }
-};
+}
 
 // Bounded wait of a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared& sh,
@@ -374,9 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       mbar_init(smem_u32(&sh.v_full[i]), kLoadWarps);
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
     }
-    mbar_init(smem_u32(&sh.q_full), kLoadWarps);
-    mbar_init(smem_u32(&sh.q_empty), 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.q_full[i]), 4);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
       mbar_init(smem_u32(&sh.p_full[i]), 4);
       mbar_init(smem_u32(&sh.o_full[i]), 1);
@@ -483,9 +478,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   }
   __syncthreads();
   const uint32_t tmem = sh.tmem;
-  Walker<kRows, kTile> walk;
-  walk.init(a, sh);
-  Segment seg;
+  if (lane == 0) {
+    Walk& w = sh.walk[warp];
+    w.b = sh.place[0][0];
+    w.kv = sh.place[0][1];
+    w.item = sh.place[0][2];
+    w.unit = sh.place[0][3];
+    for (int i = 0; i < 4; ++i) w.end[i] = sh.place[1][i];
+    if (w.b < a.batch) w.c = context_of<kRows>(a, sh.request[0], sh.request[1].x);
+  }
+  __syncwarp();
+  // the warp's next segment, put down as number `which` of its two
+  auto next_segment = [&](int which) -> bool {
+    Walk w = sh.walk[warp];
+    Segment s;
+    const bool got = next_of<kRows, kTile>(a, sh, w, s);
+    __syncwarp();
+    if (lane == 0) {
+      sh.walk[warp] = w;
+      sh.segment[warp][which] = s;
+    }
+    __syncwarp();
+    return got;
+  };
+  // place of 16-byte unit u of row r in an operand with `rows` rows: blocks of 128 bytes a
+  // row, swizzled
+  auto place = [](uint32_t base, int rows, int r, int u) -> uint32_t {
+    return base + (u >> 3) * (rows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+  };
   // halves of 128 rows that a segment works on together
   auto streams_of = [&](const Segment& s) { return s.rows > 128 ? 2 : 1; };
 
@@ -494,13 +514,74 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     const int me = warp >> 2;                 // the stream of two, and the half of TMEM
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // of TMEM
-    uint32_t s_phase[2] = {0u, 0u}, o_phase = 0u, halves_phase = 0u;
+    uint32_t s_phase = 0u;                    // of the two halves of the scores: bits 0, 1
+    uint32_t o_phase = 0u, halves_phase = 0u;
     int tile = 0;                             // of all tiles (sides), at the segment's start
-    int parity = 0;                           // of the segment (row_scale)
     bool ok = true;
-    while (ok && walk.next(a, sh, seg)) {
+    // This half's rows of q, a warp the rows of its threads; the factor of each.
+    auto load_q = [&](const Segment& s) {
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;   // lanes of a row, rows of a load
+      constexpr int kBatch = 8;                              // loads in flight
+      const int u = lane % kLanes;
+      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+      const float scale = fabsf(a.scale) * 1.4426950408889634f;
+      const int r0 = (warp & 3) * 32 + lane / kLanes;        // of the half
+      int token = (s.row0 + me * 128 + r0) / a.group;
+      int in = s.row0 + me * 128 + r0 - token * a.group;     // head of the group
+      for (int i0 = 0; i0 < 32; i0 += kBatch * kAtOnce) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (i * kAtOnce < 32 - i0) {
+            if (me * 128 + r0 + i0 + i * kAtOnce < s.rows)
+              raw[i] = *reinterpret_cast<const uint4*>(
+                  a.q + (int64_t)(s.token0 + token) * a.q_stride +
+                  (int64_t)(s.kv * a.group + in) * D + u * 8);
+            in += kAtOnce;
+            while (in >= a.group) {
+              in -= a.group;
+              ++token;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (i * kAtOnce >= 32 - i0) break;
+          const int r = r0 + i0 + i * kAtOnce;
+          uint32_t x[4] = {raw[i].x ^ flip, raw[i].y ^ flip, raw[i].z ^ flip, raw[i].w ^ flip};
+          float factor = scale;
+          if (!kIsBf16) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // a power of two brings the head's largest element into [2^8, 2^9)
+            const int e = min(max(exponent(top), -110), 126);
+            const float down = power(-e), up = power(8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[j] = pack_f16(bf16_lo(x[j]) * down * up, bf16_hi(x[j]) * down * up);
+            factor *= power(e - 8);
+          }
+          st_shared_16(place(q_at + me * S::kQBytes, 128, r, u), x[0], x[1], x[2], x[3]);
+          if (u == 0) sh.row_scale[me * 128 + r] = factor;
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&sh.q_full[me]);
+    };
+    auto has_q = [&](const Segment& s) { return s.u1 > s.u0 && me < streams_of(s); };
+    int which = 0;
+    bool running = next_segment(0);
+    if (running && has_q(sh.segment[warp][0])) load_q(sh.segment[warp][0]);
+    while (ok && running) {
+      const Segment& seg = sh.segment[warp][which];
       const int streams = streams_of(seg), tiles = seg.u1 - seg.u0;
-      const bool mine = me < streams;
+      const bool mine = me < streams, whole = seg.whole();
       const int r = seg.row0 + me * 128 + row;          // of the context
       const bool live = mine && me * 128 + row < seg.rows;
       const int token = r / a.group, head = seg.kv * a.group + (r - token * a.group);
@@ -513,13 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       float top = -INFINITY, sum = 0.f;
       const uint32_t o_at = tmem + lanes + S::kSOut + me * D;
       if (mine && tiles > 0) {
-        float factor = 0.f;
+        const float factor = sh.row_scale[me * 128 + row];
+        const int start = seg.start + seg.u0 * kTile;
         for (int i = 0; ok && i < tiles; ++i) {
           const int slot = streams == 2 ? me : i & 1;
           const uint32_t s_at = tmem + lanes + slot * kTile;
-          ok = warp_wait(&sh.s_full[slot], s_phase[slot], sh, a.err, kErrTimeoutEpilogue);
+          ok = warp_wait(&sh.s_full[slot], (s_phase >> slot) & 1u, sh, a.err, kErrTimeoutEpilogue);
           if (!ok) break;
-          s_phase[slot] ^= 1u;
+          s_phase ^= 1u << slot;
           if (!works) {
             if (streams == 1 && i > 0)
               ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
@@ -529,12 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             continue;
           }
           tc_fence_after_sync();
-          if (i == 0) factor = sh.row_scale[parity][me * 128 + row];
           const Side& side = sh.side[(tile + i) & (kSides - 1)];
           // (above 0, so that it leaves the -inf of a token that is not seen as it is)
           const float c = fmaxf(factor * side.key_up, 0x1p-120f), f = side.value_exp;
           // what this row sees of the tile
-          const int first = seg.start + (seg.u0 + i) * kTile;
+          const int first = start + i * kTile;
           constexpr uint32_t kAll = kTile == 128 ? 0xffffffffu : 0xffffu;
           const bool all_there = (side.mask[0] & side.mask[1] & side.mask[2] & side.mask[3]) == kAll;
           const bool clear =
@@ -627,6 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           o_phase ^= 1u;
         }
         if (!ok) break;
+      }
+      // q of the next segment, behind the last scores of this one
+      running = next_segment(which ^ 1);
+      if (running && has_q(sh.segment[warp][which ^ 1])) load_q(sh.segment[warp][which ^ 1]);
+      which ^= 1;
+      if (mine && tiles > 0) {
         // the last products (o_phase has moved past them)
         ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
         if (!ok) break;
@@ -634,15 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       }
       // the other half's tiles and segments, counted
       if (tiles > 0) {
-        if (!mine || streams == 2) {
-          if (streams == 2) {
-            s_phase[me ^ 1] ^= tiles & 1;
-          } else {
-            s_phase[0] ^= (uint32_t)(((tiles + 1) >> 1) & 1);
-            s_phase[1] ^= (uint32_t)((tiles >> 1) & 1);
-          }
-        }
-        parity ^= 1;
+        if (streams == 2)
+          s_phase ^= (uint32_t)(tiles & 1) << (me ^ 1);
+        else if (!mine)
+          s_phase ^= (uint32_t)(((tiles + 1) >> 1) & 1) | (uint32_t)((tiles >> 1) & 1) << 1;
         tile += tiles;
       }
       if (S::kStreams == 2 && streams == 1 && tiles > 0) {
@@ -654,7 +736,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         halves_phase ^= 1u;
       }
       if (!mine) continue;
-      const bool whole = seg.whole();
       const int64_t slot = 2 * worker + (seg.u0 == 0 ? 1 : 0);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const int64_t to = (int64_t)(seg.token0 + token);
@@ -718,69 +799,73 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     constexpr int kChunks = kRowBytes / 16;              // 16-byte pieces of a row
     constexpr int kAtOnce = 32 / kChunks > 0 ? 32 / kChunks : 1;   // rows of one load
     constexpr int kLoads = kMine * kChunks / 32;         // of a lane, of a tile
-    const int chunk = lane % kChunks, sub = lane / kChunks;
+    // The lane's piece of a row, and its row of those of one load. Codes become two pieces of
+    // fp16 each, and a row two or more blocks: eight neighbouring lanes take the same half of
+    // the pieces of a block in two rows, so that their stores use all banks.
+    constexpr int kQuads = kChunks / 4;
+    const int chunk = kIsBf16 ? lane % kChunks : (lane & 3) | ((lane >> 3) % kQuads) << 2;
+    const int sub = kIsBf16 ? lane / kChunks : ((lane >> 2) & 1) + 2 * ((lane >> 3) / kQuads);
     uint32_t k_phase = 1u, v_phase = 1u;   // (the stages are empty at first)
-    int stage = 0;
-    uint32_t q_phase = 1u;
-    int parity = 0, tile = 0;
+    int stage = 0, tile = 0;
     bool ok = true;
-    // A tile's tokens, one a lane: its cache row and whether it is there.
-    struct Tokens {
-      uint32_t row;
-      bool here;
+    // The next tile to ask for: its segment's context, kv head and tokens, the lane's token,
+    // and the tiles left of the segment.
+    const int32_t* row_of_table = nullptr;
+    int kv = 0, left = 0;
+    uint32_t begin = 0, end = 0, token = 0;
+    bool more = true;
+    auto open = [&]() {   // the next segment that has tiles
+      do {
+        if (!next_segment(0)) {
+          more = false;
+          return;
+        }
+        left = sh.segment[warp][0].u1 - sh.segment[warp][0].u0;
+      } while (left == 0);
+      const Segment& s = sh.segment[warp][0];
+      row_of_table = a.c.table + s.b * a.c.table_stride;
+      kv = s.kv;
+      begin = s.begin;
+      end = s.end;
+      token = (uint32_t)s.start + (uint32_t)s.u0 * kTile + w * kMine + lane;
     };
-    Segment next;          // the segment of the tile that is asked for
-    int at = 0;            // that tile in it
-    bool more = walk.next(a, sh, next);
-    while (more && next.u1 == next.u0) more = walk.next(a, sh, next);
     auto look = [&]() -> int32_t {
-      const int64_t token = (int64_t)next.start + (int64_t)(next.u0 + at) * kTile + w * kMine + lane;
-      return more && lane < kMine && token >= next.begin && token < next.end
-                 ? a.c.table[next.b * a.c.table_stride + (token >> a.c.page_shift)]
+      return more && lane < kMine && token >= begin && token < end
+                 ? row_of_table[token >> a.c.page_shift]
                  : -1;
     };
-    auto tokens = [&](int32_t entry) -> Tokens {
-      const uint32_t token = (uint32_t)next.start + (uint32_t)(next.u0 + at) * kTile + w * kMine + lane;
-      Tokens t;
-      t.here = (uint32_t)entry < (uint32_t)a.c.pages;
-      t.row = t.here ? (((uint32_t)entry * a.c.heads + next.kv) << a.c.page_shift) +
-                           (token & ((1u << a.c.page_shift) - 1u))
-                     : 0u;
-      return t;
+    // the lane's cache row, all ones for none
+    constexpr uint32_t kNoRow = 0xffffffffu;
+    auto row_of = [&](int32_t entry) -> uint32_t {
+      return (uint32_t)entry < (uint32_t)a.c.pages
+                 ? (((uint32_t)entry * a.c.heads + kv) << a.c.page_shift) +
+                       (token & ((1u << a.c.page_shift) - 1u))
+                 : kNoRow;
     };
     auto advance = [&]() {
-      if (++at >= next.u1 - next.u0) {
-        at = 0;
-        do more = walk.next(a, sh, next);
-        while (more && next.u1 == next.u0);
-      }
-    };
-    // place of 16-byte unit u of a row in an operand with `rows` rows: blocks of 128 bytes
-    auto place = [&](uint32_t base, int rows, int r, int u) -> uint32_t {
-      return base + (u >> 3) * (rows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+      token += kTile;
+      if (--left == 0) open();
     };
     uint4 kreg[kIsBf16 ? 1 : kLoads], vreg[kIsBf16 ? 1 : kLoads];
-    auto fetch = [&](const void* cache, const Tokens& t, uint4* reg) {
+    auto fetch = [&](const void* cache, uint32_t rows, uint4* reg) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = i * kAtOnce + sub;
-        const uint32_t row = __shfl_sync(0xffffffffu, t.row, r);
-        const bool here = __shfl_sync(0xffffffffu, (int)t.here, r) != 0;
+        const uint32_t row = __shfl_sync(0xffffffffu, rows, i * kAtOnce + sub);
         reg[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (here)
+        if (row != kNoRow)
           reg[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) +
                                                    (uint64_t)row * kRowBytes + chunk * 16);
       }
     };
-    auto copy = [&](const void* cache, const Tokens& t, uint32_t base) {   // bf16: straight
+    auto copy = [&](const void* cache, uint32_t rows, uint32_t base) {   // bf16: straight
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = i * kAtOnce + sub;
-        const uint32_t row = __shfl_sync(0xffffffffu, t.row, r);
-        const bool here = __shfl_sync(0xffffffffu, (int)t.here, r) != 0;
+        const uint32_t row = __shfl_sync(0xffffffffu, rows, r);
         cp_async_16(place(base, kTile, w * kMine + r, chunk),
-                    static_cast<const uint8_t*>(cache) + (uint64_t)row * kRowBytes + chunk * 16,
-                    here ? 16u : 0u);
+                    static_cast<const uint8_t*>(cache) +
+                        (row == kNoRow ? 0 : (uint64_t)row * kRowBytes + chunk * 16),
+                    row == kNoRow ? 0u : 16u);
       }
     };
     // codes to fp16: `by` an fp16 pair (ROUNDED: an fp32 factor) of the lane's token
@@ -801,111 +886,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             h[j] = mul_f16(h[j], up);
           }
         }
-        // (the lanes of the second 128 bytes put their units down in the other order: all
-        // banks are used)
-        const bool swap = ((2 * chunk) & 8) != 0;
         const int row = w * kMine + r;
-        const uint32_t at0 = place(base, kTile, row, 2 * chunk + (swap ? 1 : 0));
-        const uint32_t at1 = place(base, kTile, row, 2 * chunk + (swap ? 0 : 1));
-        st_shared_16(at0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2],
-                     swap ? h[7] : h[3]);
-        st_shared_16(at1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6],
-                     swap ? h[3] : h[7]);
+        st_shared_16(place(base, kTile, row, 2 * chunk), h[0], h[1], h[2], h[3]);
+        st_shared_16(place(base, kTile, row, 2 * chunk + 1), h[4], h[5], h[6], h[7]);
       }
     };
-    // q of a segment: a warp a quarter of the rows
-    auto load_q = [&](const Segment& s) {
-      constexpr int kLanes = D / 8, kQAtOnce = 32 / kLanes;   // lanes of a row, rows of a load
-      const int halves = streams_of(s);
-      const int lr = lane / kLanes, u = lane % kLanes;
-      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-      const float scale = fabsf(a.scale) * 1.4426950408889634f;
-      const int rows = halves * 32;
-#pragma unroll 8
-      for (int i = 0; i < rows / kQAtOnce; ++i) {
-        const int r = w * rows + i * kQAtOnce + lr;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (r < s.rows) {
-          const int flat = s.row0 + r, token = flat / a.group;
-          const int head = s.kv * a.group + flat - token * a.group;
-          raw = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.token0 + token) * a.q_stride +
-                                                (int64_t)head * D + u * 8);
-        }
-        uint32_t x[4] = {raw.x ^ flip, raw.y ^ flip, raw.z ^ flip, raw.w ^ flip};
-        float factor = scale;
-        if (!kIsBf16) {
-          float top = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // a power of two brings the head's largest element into [2^8, 2^9)
-          const int e = min(max(exponent(top), -110), 126);
-          const float down = power(-e), up = power(8);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            x[j] = pack_f16(bf16_lo(x[j]) * down * up, bf16_hi(x[j]) * down * up);
-          factor *= power(e - 8);
-        }
-        st_shared_16(place(q_at + (r >> 7) * S::kQBytes, 128, r & 127, u), x[0], x[1], x[2], x[3]);
-        if (u == 0) sh.row_scale[parity][r] = factor;
-      }
-    };
-
-    Tokens now{0u, false}, then{0u, false};
-    float ks = 0.f, vs = 0.f;                // scales of the lane's token of the next tile
-    auto ask_scales = [&](const Tokens& t) {
+    uint32_t now = kNoRow, then = kNoRow;   // the lane's rows of this tile and the next
+    float ks = 0.f, vs = 0.f;               // and its scales of the next tile
+    auto ask_scales = [&](uint32_t row) {
       ks = vs = 0.f;
-      if (!kIsBf16 && t.here) {
-        ks = a.c.k_scale[t.row >> a.c.scale_shift];
-        vs = a.c.v_scale[t.row >> a.c.scale_shift];
+      if (!kIsBf16 && row != kNoRow) {
+        ks = a.c.k_scale[row >> a.c.scale_shift];
+        vs = a.c.v_scale[row >> a.c.scale_shift];
       }
     };
-    Segment cur = next;
-    bool fresh = true, running = more;      // the current tile is the first of its segment
-    int32_t entry = -1;
+    open();
+    int32_t entry = look();
+    bool running = more;
     if (running) {
-      now = tokens(look());
-      cur = next;
-      if (kIsBf16) {
-        // (nothing is asked for ahead: the stages are)
-      } else {
+      now = row_of(entry);
+      if (!kIsBf16) {   // (bf16 rows go straight to the stages)
         fetch(a.c.k, now, kreg);
-        fetch(a.c.v, now, vreg);
         ask_scales(now);
+        fetch(a.c.v, now, vreg);
       }
       advance();
       entry = look();
     }
-    bool pending = false;                   // bf16: a tile's copies are under way
+    bool pending = false;                   // bf16: a tile's values are under way
     int pending_stage = 0;
     while (running && ok) {
-      if (fresh) {
-        if (kIsBf16 && pending) {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-          fence_proxy_async_smem();
-          warp_arrive(&sh.v_full[pending_stage]);
-          pending = false;
-        }
-        ok = warp_wait(&sh.q_empty, q_phase, sh, a.err, kErrTimeoutProducer);
-        if (!ok) break;
-        load_q(cur);
-        fence_proxy_async_smem();
-        warp_arrive(&sh.q_full);
-        q_phase ^= 1u;
-        parity ^= 1;
-      }
       // the tile's factors and masks
       Side& side = sh.side[tile & (kSides - 1)];
-      const unsigned mask = __ballot_sync(0xffffffffu, now.here);
+      const unsigned mask = __ballot_sync(0xffffffffu, now != kNoRow);
       uint32_t kby = 0u, vby = 0u;
       int e = 0, f = 0;
       if (!kIsBf16) {
         const int none = -1000;
-        int ke = now.here && ks > 0.f ? max(exponent(ks), kLeastExponent) : none;
-        int ve = now.here && vs > 0.f ? max(exponent(vs), kLeastExponent) : none;
+        int ke = now != kNoRow && ks > 0.f ? max(exponent(ks), kLeastExponent) : none;
+        int ve = now != kNoRow && vs > 0.f ? max(exponent(vs), kLeastExponent) : none;
         const int ktop = __reduce_max_sync(0xffffffffu, ke);
         const int vtop = __reduce_max_sync(0xffffffffu, ve);
         if (lane == 0) {
@@ -943,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         }
       }
       if (KIND == kTokenScales && lane < kMine)
-        sh.key_scale[tile & (kSides - 1)][w * kMine + lane] = now.here ? ks : 0.f;
+        sh.key_scale[tile & (kSides - 1)][w * kMine + lane] = now != kNoRow ? ks : 0.f;
 
       const uint32_t k_to = k_at + stage * S::kTileBytes, v_to = v_at + stage * S::kTileBytes;
       ok = warp_wait(&sh.k_empty[stage], k_phase, sh, a.err, kErrTimeoutProducer);
@@ -972,10 +991,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       }
       // the next tile
       running = more;
-      fresh = at == 0;
-      if (more) {
-        then = tokens(entry);
-        cur = next;
+      if (running) {
+        then = row_of(entry);
         if (!kIsBf16) {
           fetch(a.c.k, then, kreg);
           ask_scales(then);
@@ -1009,19 +1026,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     }
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
-    uint32_t k_phase = 0u, v_phase = 0u, q_phase = 0u, p_phase[2] = {0u, 0u};
-    uint32_t oe_phase[2] = {1u, 1u};        // (O is free at first)
+    uint32_t k_phase = 0u, v_phase = 0u;
+    uint32_t q_phase = 0u, p_phase = 0u, oe_phase = 3u;   // bits 0, 1 (O is free at first)
     int k_stage = 0, v_stage = 0;
     bool ok = true;
     constexpr uint32_t kQk = idesc_f16(kIsBf16, kTile, false), kPv = idesc_f16(kIsBf16, D, true);
-    while (ok && walk.next(a, sh, seg)) {
-      const int streams = streams_of(seg), tiles = seg.u1 - seg.u0;
+    while (ok && next_segment(0)) {
+      const int streams = streams_of(sh.segment[warp][0]);
+      const int tiles = sh.segment[warp][0].u1 - sh.segment[warp][0].u0;
       if (tiles == 0) continue;
       const int tasks = tiles * streams;
       // task t: the scores, then the weights and products, of stream t % streams and tile
       // t / streams, in half t % 2 of the scores' tensor memory
       auto scores = [&](int t) -> bool {
         const int stream = streams == 2 ? t & 1 : 0;
+        if (t < streams) {   // the stream's rows of q
+          if (!warp_wait(&sh.q_full[stream], (q_phase >> stream) & 1u, sh, a.err, kErrTimeoutMma))
+            return false;
+          q_phase ^= 1u << stream;
+        }
         if (stream == 0 &&
             !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
           return false;
@@ -1036,7 +1059,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
                        i > 0 ? 1u : 0u);
           mma_commit(smem_u32(&sh.s_full[t & 1]));
           if (stream == streams - 1) mma_commit(smem_u32(&sh.k_empty[k_stage]));
-          if (t == tasks - 1) mma_commit(smem_u32(&sh.q_empty));
         }
         __syncwarp();
         if (stream == streams - 1 && ++k_stage == S::kStages) {
@@ -1045,24 +1067,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         }
         return true;
       };
-      ok = warp_wait(&sh.q_full, q_phase, sh, a.err, kErrTimeoutMma);
-      q_phase ^= 1u;
-      if (ok) ok = scores(0);
+      ok = scores(0);
       if (ok && tasks > 1) ok = scores(1);
       for (int t = 0; ok && t < tasks; ++t) {
         const int stream = streams == 2 ? t & 1 : 0, slot = t & 1;
         if (t < streams) {   // O: the last segment's has been read
-          ok = warp_wait(&sh.o_empty[stream], oe_phase[stream], sh, a.err, kErrTimeoutMma);
+          ok = warp_wait(&sh.o_empty[stream], (oe_phase >> stream) & 1u, sh, a.err, kErrTimeoutMma);
           if (!ok) break;
-          oe_phase[stream] ^= 1u;
+          oe_phase ^= 1u << stream;
         }
         if (stream == 0) {
           ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a.err, kErrTimeoutMma);
           if (!ok) break;
         }
-        ok = warp_wait(&sh.p_full[slot], p_phase[slot], sh, a.err, kErrTimeoutMma);
+        ok = warp_wait(&sh.p_full[slot], (p_phase >> slot) & 1u, sh, a.err, kErrTimeoutMma);
         if (!ok) break;
-        p_phase[slot] ^= 1u;
+        p_phase ^= 1u << slot;
         tc_fence_after_sync();
         if (lane == 0) {
           const uint32_t d = tmem + S::kSOut + stream * D, p = tmem + slot * kTile;

@@ -31,15 +31,14 @@ class Model:
         ring = range(stages)
         self.k_full, self.v_full = ([Barrier(LOADERS) for _ in ring] for _ in range(2))
         self.k_empty, self.v_empty = ([Barrier(1) for _ in ring] for _ in range(2))
-        self.q_full, self.q_empty = Barrier(LOADERS), Barrier(1)
+        self.q_full = [Barrier(4) for _ in range(2)]
         self.s_full, self.o_full = ([Barrier(1) for _ in range(2)] for _ in range(2))
         self.p_full, self.o_empty = ([Barrier(4) for _ in range(2)] for _ in range(2))
         self.both, self.maxed = Barrier(8), Barrier(LOADERS)
         self.queue = []                 # products and commits under way, in order
         self.k_holds, self.v_holds = [None] * stages, [None] * stages
-        self.q_holds = [None] * LOADERS
+        self.q_holds = [[None] * 4 for _ in range(2)]
         self.side = [[None] * LOADERS for _ in range(SIDES)]
-        self.row_scale = [[None] * LOADERS for _ in range(2)]
         self.s_holds, self.o_holds = [None, None], [[], []]
         self.out = []
 
@@ -58,14 +57,10 @@ class Model:
             yield
 
     def loader(self, w):
-        stage = use = seg = tile = 0
+        stage = use = tile = 0
         for n, (rows, tiles) in enumerate(self.segments):
             if tiles == 0:
                 continue
-            yield from self.wait(self.q_empty, seg - 1)
-            self.q_holds[w] = self.row_scale[seg & 1][w] = n
-            self.q_full.arrive()
-            seg += 1
             for i in range(tiles):
                 self.side[tile % SIDES][w] = (n, i)
                 self.maxed.arrive()
@@ -84,8 +79,8 @@ class Model:
                 yield
 
     def issuer(self):
-        k = v = seg = 0                 # tiles used
-        p, oe = [0, 0], [0, 0]
+        k = v = 0                       # tiles used
+        p, oe, q = [0, 0], [0, 0], [0, 0]
         for n, (rows, tiles) in enumerate(self.segments):
             if tiles == 0:
                 continue
@@ -96,6 +91,9 @@ class Model:
                 nonlocal k
                 stream = t % streams
                 stage = k % self.stages
+                if t < streams:
+                    yield from self.wait(self.q_full[stream], q[stream])
+                    q[stream] += 1
                 if stream == 0:
                     yield from self.wait(self.k_full[stage], k // self.stages)
                 self.queue.append(("s", t & 1, (n, t // streams, stream), stage))
@@ -103,11 +101,7 @@ class Model:
                 if stream == streams - 1:
                     self.queue.append(self.k_empty[stage])
                     k += 1
-                if t == tasks - 1:
-                    self.queue.append(self.q_empty)
 
-            yield from self.wait(self.q_full, seg)
-            seg += 1
             yield from scores(0)
             if tasks > 1:
                 yield from scores(1)
@@ -130,7 +124,15 @@ class Model:
                 yield
 
     def softmax(self, me, w):
-        s, o, q, both, tile = [0, 0], 0, 0, 0, 0
+        s, o, both, tile = [0, 0], 0, 0, 0
+
+        def load_q(n):
+            if n < len(self.segments) and self.segments[n][1] and \
+                    me < self.streams(self.segments[n][0]):
+                self.q_holds[me][w] = n
+                self.q_full[me].arrive()
+
+        load_q(0)
         for n, (rows, tiles) in enumerate(self.segments):
             streams = self.streams(rows)
             mine = me < streams
@@ -140,8 +142,6 @@ class Model:
                     yield from self.wait(self.s_full[slot], s[slot])
                     s[slot] += 1
                     assert self.s_holds[slot] == (n, i, me)
-                    if i == 0:
-                        assert self.row_scale[q & 1] == [n] * LOADERS
                     yield
                     if i > 0 and streams == 1:
                         yield from self.wait(self.o_full[me], o - 1)
@@ -153,6 +153,8 @@ class Model:
                     self.p_full[slot].arrive()
                     o += 1
                     yield
+            load_q(n + 1)
+            if mine and tiles:
                 yield from self.wait(self.o_full[me], o - 1)
                 assert self.o_holds[me] == [(n, i, me) for i in range(tiles)]
             if tiles:
@@ -161,7 +163,6 @@ class Model:
                 elif not mine:
                     s[0] += (tiles + 1) // 2
                     s[1] += tiles // 2
-                q += 1
                 tile += tiles
                 if streams == 1 and self.halves == 2:
                     self.both.arrive()
@@ -183,7 +184,7 @@ class Model:
         kind, slot, task, stage = x
         n, i, stream = task
         if kind == "s":
-            assert self.k_holds[stage] == (n, i) and self.q_holds == [n] * LOADERS
+            assert self.k_holds[stage] == (n, i) and self.q_holds[stream] == [n] * 4
             self.s_holds[slot] = task
         else:
             assert self.v_holds[stage] == (n, i) and self.s_holds[slot] == task
