@@ -24,9 +24,10 @@
 // bf16 (8 bits): the values' own products have no more, and a second product for the
 // rest of a weight would cost half as much again.
 //
-// Roles of a CTA's 13 warps: 0-3 and 4-7 the softmax of 128 rows each, a row a thread; 8-11
-// fetch q, keys and values from the pages and lay them out for the tensor cores; 12
-// issues the products. While one half's softmax runs, the other half's products do; with
+// Roles of a CTA's warps: 0-3 and 4-7 the softmax of 128 rows each, a row a thread, and
+// the rows' q; 8-11 fetch keys from the pages and lay them out for the tensor cores, 12-15
+// values; 16 issues the products, 17
+// hands out the work. While one half's softmax runs, the other half's products do; with
 // 128 rows or fewer the halves are two tiles of the same rows.
 //
 // The work is split over the CTAs by length: every item (a context's rows of one kv head)
@@ -51,9 +52,14 @@ namespace {
 constexpr int kWorkers = 152;              // CTAs, one an SM
 constexpr int kSoftWarps = 8;
 constexpr int kLoadWarp0 = kSoftWarps;
-constexpr int kLoadWarps = 4;
-constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kLoadWarps = 4;              // of keys, and of values
+constexpr int kMmaWarp = kLoadWarp0 + 2 * kLoadWarps;
+constexpr int kPlanWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 4);
+// Registers of a thread, by role (640 threads are launched with 96 each: 61440).
+constexpr int kSoftRegs = 128, kLoadRegs = 88, kMmaRegs = 48;
+static_assert(256 * kSoftRegs + 256 * kLoadRegs + 128 * kMmaRegs <= 96 * kThreads, "registers");
+constexpr int kRing = 8;                   // segments handed out at a time
 constexpr int kSides = 8;                  // tiles whose masks and factors are at hand
 constexpr int kRequests = 256;             // contexts whose places a CTA keeps at hand
 constexpr float kMostWeight = 15.0f;       // log2 of the largest weight let stand,
@@ -101,6 +107,7 @@ struct Shape {
   static constexpr int kQBytes = 128 * D * 2;             // of a stream
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kSOut = 2 * kTile;                 // TMEM: two tiles of scores, then O
+  static constexpr int kPOut = kTile - kTile / 2;         // the weights in a tile of scores
   static constexpr int kCols = 512;
   static constexpr int kSmemBytes = 1024 + kStreams * kQBytes + 2 * kStages * kTileBytes;
   static_assert(kSOut + kStreams * D <= kCols, "tensor memory");
@@ -139,26 +146,46 @@ struct Side {
 struct Shared {
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t halves, maxed, drain;
+  uint64_t halves, maxed[2], drain, seg_full[kRing], seg_empty[kRing];
   uint32_t tmem;
   int abort;
   Side side[kSides];
-  float key_scale[kSides][128];      // token scales
+  alignas(16) float key_scale[kSides][128];   // token scales, read as float4
   float row_scale[256];
-  int maxima[2][kLoadWarps][2];
+  int maxima[2][2][kLoadWarps][2];   // of keys' loaders and values'
   int2 request[kRequests + 1];       // (first row, length)
   int64_t sums[kThreads / 32 + 1];
   int place[2][4];                   // the run: first context, kv head, item, unit; and its end
-  // each warp's walk, and the segments that it works on and looks ahead to (in shared
-  // memory: they are wanted once a segment, and registers are scarce)
-  Walk walk[kThreads / 32];
-  Segment segment[kThreads / 32][2];
+  Segment ring[kRing];               // handed out and not yet done with; units < 0: no more
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -378,7 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       mbar_init(smem_u32(&sh.o_empty[i]), 4);
     }
     mbar_init(smem_u32(&sh.halves), kSoftWarps);
-    mbar_init(smem_u32(&sh.maxed), kLoadWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.maxed[i]), kLoadWarps);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(smem_u32(&sh.seg_full[i]), 1);
+      mbar_init(smem_u32(&sh.seg_empty[i]), 4 * S::kStreams + 2 * kLoadWarps + 1);
+    }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.place[0][0] = sh.place[1][0] = a.batch;   // nothing to do
@@ -478,29 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   }
   __syncthreads();
   const uint32_t tmem = sh.tmem;
-  if (lane == 0) {
-    Walk& w = sh.walk[warp];
-    w.b = sh.place[0][0];
-    w.kv = sh.place[0][1];
-    w.item = sh.place[0][2];
-    w.unit = sh.place[0][3];
-    for (int i = 0; i < 4; ++i) w.end[i] = sh.place[1][i];
-    if (w.b < a.batch) w.c = context_of<kRows>(a, sh.request[0], sh.request[1].x);
-  }
-  __syncwarp();
-  // the warp's next segment, put down as number `which` of its two
-  auto next_segment = [&](int which) -> bool {
-    Walk w = sh.walk[warp];
-    Segment s;
-    const bool got = next_of<kRows, kTile>(a, sh, w, s);
-    __syncwarp();
-    if (lane == 0) {
-      sh.walk[warp] = w;
-      sh.segment[warp][which] = s;
-    }
-    __syncwarp();
-    return got;
+  // The segments, from the warp that hands them out: number n is there (false: the run has
+  // ended, or a wait has run out) and, when a role is done with it, free.
+  auto take = [&](int n) -> bool {
+    return warp_wait(&sh.seg_full[n % kRing], (n / kRing) & 1, sh, a.err, kErrTimeoutSched) &&
+           sh.ring[n % kRing].units >= 0;
   };
+  auto release = [&](int n) { warp_arrive(&sh.seg_empty[n % kRing]); };
   // place of 16-byte unit u of row r in an operand with `rows` rows: blocks of 128 bytes a
   // row, swizzled
   auto place = [](uint32_t base, int rows, int r, int u) -> uint32_t {
@@ -509,8 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   // halves of 128 rows that a segment works on together
   auto streams_of = [&](const Segment& s) { return s.rows > 128 ? 2 : 1; };
 
-  if (warp < 4 * S::kStreams) {
+  if (warp < kSoftWarps) {
     // ---------------- softmax ----------------
+    more_registers<kSoftRegs>();
     const int me = warp >> 2;                 // the stream of two, and the half of TMEM
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // of TMEM
@@ -575,11 +591,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       warp_arrive(&sh.q_full[me]);
     };
     auto has_q = [&](const Segment& s) { return s.u1 > s.u0 && me < streams_of(s); };
-    int which = 0;
-    bool running = next_segment(0);
-    if (running && has_q(sh.segment[warp][0])) load_q(sh.segment[warp][0]);
-    while (ok && running) {
-      const Segment& seg = sh.segment[warp][which];
+    int number = 0;
+    bool running = me < S::kStreams && take(0);
+    if (running && has_q(sh.ring[0])) load_q(sh.ring[0]);
+    for (; ok && running; release(number++)) {
+      const Segment& seg = sh.ring[number % kRing];
       const int streams = streams_of(seg), tiles = seg.u1 - seg.u0;
       const bool mine = me < streams, whole = seg.whole();
       const int r = seg.row0 + me * 128 + row;          // of the context
@@ -620,46 +636,52 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           const bool all_there = (side.mask[0] & side.mask[1] & side.mask[2] & side.mask[3]) == kAll;
           const bool clear =
               __all_sync(0xffffffffu, all_there && lo <= first && hi - first >= kTile);
-          // 64 scores at a time, read once for their maximum and again for the weights (128
-          // would not fit the registers)
-          float s[64];
-          auto get = [&](int h) {
-            tmem_load(s_at + 64 * h, s);
-            if (KIND == kTokenScales) {
-              const float4* const scales = reinterpret_cast<const float4*>(
-                  sh.key_scale[(tile + i) & (kSides - 1)] + 64 * h);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float4 v = scales[j];
-                s[4 * j] *= v.x;
-                s[4 * j + 1] *= v.y;
-                s[4 * j + 2] *= v.z;
-                s[4 * j + 3] *= v.w;
-              }
-            }
-            if (!clear) {
-              constexpr int kBits = kTile / kLoadWarps;   // tokens of a mask
-#pragma unroll
-              for (int w = 0; w < 64 / kBits; ++w) {
-                const int at = first + 64 * h + w * kBits;
-                const int from = min(max(lo - at, 0), kBits), to = min(max(hi - at, 0), kBits);
-                uint32_t bits = side.mask[h * (64 / kBits) + w];
-                bits &= to >= 32 ? 0xffffffffu : (1u << to) - 1u;
-                bits &= from >= 32 ? 0u : ~((1u << from) - 1u);
-#pragma unroll
-                for (int j = 0; j < kBits; ++j)
-                  if (!((bits >> j) & 1u)) s[w * kBits + j] = -INFINITY;
-              }
-            }
-          };
-          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+          // 64 scores at a time: all for their maximum, the last of them kept, and then the
+          // others again for the weights (128 would not fit the registers). What a row does not
+          // see is put back as -inf, keys' own scales with them. (The loops stay
+          // rolled: five roles' code has to fit the instruction caches.)
+          float s[64], high = -INFINITY;
+#pragma unroll 1
           for (int h = 0; h < kTile / 64; ++h) {
-            get(h);
+            float m = tmem_load_max(s_at + 64 * h, s);
+            if (KIND == kTokenScales || !clear) {
+              if (KIND == kTokenScales) {
+                const float4* const scales = reinterpret_cast<const float4*>(
+                    sh.key_scale[(tile + i) & (kSides - 1)] + 64 * h);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) m[j & 3] = fmaxf(m[j & 3], s[j]);
+                for (int j = 0; j < 16; ++j) {
+                  const float4 v = scales[j];
+                  s[4 * j] *= v.x;
+                  s[4 * j + 1] *= v.y;
+                  s[4 * j + 2] *= v.z;
+                  s[4 * j + 3] *= v.w;
+                }
+              }
+              if (!clear) {
+                constexpr int kBits = kTile / kLoadWarps;   // tokens of a mask
+#pragma unroll
+                for (int w = 0; w < 64 / kBits; ++w) {
+                  const int at = first + 64 * h + w * kBits;
+                  const int from = min(max(lo - at, 0), kBits), to = min(max(hi - at, 0), kBits);
+                  uint32_t bits = side.mask[h * (64 / kBits) + w];
+                  bits &= to >= 32 ? 0xffffffffu : (1u << to) - 1u;
+                  bits &= from >= 32 ? 0u : ~((1u << from) - 1u);
+#pragma unroll
+                  for (int j = 0; j < kBits; ++j)
+                    if (!((bits >> j) & 1u)) s[w * kBits + j] = -INFINITY;
+                }
+              }
+              float top4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+              for (int j = 4; j < 64; ++j) top4[j & 3] = fmaxf(top4[j & 3], s[j]);
+              m = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+              if (kTile > 64 && h == 0) {
+                tmem_store(s_at, s);
+                tmem_store_wait();
+              }
+            }
+            high = fmaxf(high, m);
           }
-          const float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
           const float z = fmaf(high, c, f);
           if (streams == 1 && i > 0) {
             // the last tile's products, before O is touched and before the barrier can get
@@ -674,34 +696,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             top = next;
             sum *= down;
             if (i > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int j = 0; j < D / 32; ++j) {
                 float o[32];
                 tmem_load(o_at + 32 * j, o);
-                uint32_t w[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(o[k] * down);
-                tmem_store(o_at + 32 * j, w);
+                for (int k = 0; k < 32; ++k) o[k] *= down;
+                tmem_store(o_at + 32 * j, o);
               }
             }
           }
           const float by = f - (top == -INFINITY ? 0.f : top);
-          float add[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < kTile / 64; ++h) {
-            if (kTile > 64) get(h);
+          const float2 c2 = make_float2(c, c), by2 = make_float2(by, by);
+          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int h = kTile / 64 - 1; h >= 0; --h) {
+            if (h < kTile / 64 - 1) tmem_load(s_at, s);
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const float w0 = exp2_approx(fmaf(s[2 * j], c, by));
-              const float w1 = exp2_approx(fmaf(s[2 * j + 1], c, by));
-              add[2 * (j & 1)] += w0;
-              add[2 * (j & 1) + 1] += w1;
-              p[j] = kIsBf16 ? pack_bf16(w0, w1) : pack_f16(w0, w1);
+              const float2 x = fma2(make_float2(s[2 * j], s[2 * j + 1]), c2, by2);
+              const float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+              add[j & 1] = add2(add[j & 1], w);
+              p[j] = kIsBf16 ? pack_bf16(w.x, w.y) : pack_f16(w.x, w.y);
             }
-            tmem_store(s_at + 32 * h, p);
+            // (behind the scores that are still to be read)
+            tmem_store(s_at + S::kPOut + 32 * h, p);
           }
-          sum = fmaf((add[0] + add[1]) + (add[2] + add[3]), exp2_approx(-f), sum);
+          sum = fmaf((add[0].x + add[1].x) + (add[0].y + add[1].y), exp2_approx(-f), sum);
           tmem_store_wait();
           tc_fence_before_sync();
           warp_arrive(&sh.p_full[slot]);
@@ -710,9 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         if (!ok) break;
       }
       // q of the next segment, behind the last scores of this one
-      running = next_segment(which ^ 1);
-      if (running && has_q(sh.segment[warp][which ^ 1])) load_q(sh.segment[warp][which ^ 1]);
-      which ^= 1;
+      running = take(number + 1);
+      if (running && has_q(sh.ring[(number + 1) % kRing])) load_q(sh.ring[(number + 1) % kRing]);
       if (mine && tiles > 0) {
         // the last products (o_phase has moved past them)
         ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
@@ -742,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       uint16_t* const out = a.out + to * a.out_stride + (int64_t)head * D;
       float4* const part = reinterpret_cast<float4*>(a.parts) +
                            slot * (kRows * D / 4) + me * 128 + row;
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < D / 32; ++j) {
         float o[32];
         __syncwarp();
@@ -791,13 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         }
       }
     }
-  } else if (warp >= kLoadWarp0 && warp < kMmaWarp) {
-    // ---------------- q, keys and values ----------------
-    const int w = warp - kLoadWarp0;
+  } else if (warp < kMmaWarp) {
+    // ---------------- keys, or values ----------------
+    fewer_registers<kLoadRegs>();
+    const bool keys = warp < kLoadWarp0 + kLoadWarps;
+    const int w = (warp - kLoadWarp0) & (kLoadWarps - 1);
     constexpr int kMine = kTile / kLoadWarps;            // tokens of a warp
     constexpr int kRowBytes = D * (kIsBf16 ? 2 : 1);
     constexpr int kChunks = kRowBytes / 16;              // 16-byte pieces of a row
-    constexpr int kAtOnce = 32 / kChunks > 0 ? 32 / kChunks : 1;   // rows of one load
+    constexpr int kAtOnce = 32 / kChunks;                // rows of one load
     constexpr int kLoads = kMine * kChunks / 32;         // of a lane, of a tile
     // The lane's piece of a row, and its row of those of one load. Codes become two pieces of
     // fp16 each, and a row two or more blocks: eight neighbouring lanes take the same half of
@@ -805,29 +828,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     constexpr int kQuads = kChunks / 4;
     const int chunk = kIsBf16 ? lane % kChunks : (lane & 3) | ((lane >> 3) % kQuads) << 2;
     const int sub = kIsBf16 ? lane / kChunks : ((lane >> 2) & 1) + 2 * ((lane >> 3) / kQuads);
-    uint32_t k_phase = 1u, v_phase = 1u;   // (the stages are empty at first)
+    const uint8_t* const cache = static_cast<const uint8_t*>(keys ? a.c.k : a.c.v) + chunk * 16;
+    uint64_t* const full = keys ? sh.k_full : sh.v_full;
+    uint64_t* const empty = keys ? sh.k_empty : sh.v_empty;
+    const uint32_t stages = keys ? k_at : v_at;
+    uint32_t phase = 1u;                                 // (the stages are empty at first)
     int stage = 0, tile = 0;
-    bool ok = true;
     // The next tile to ask for: its segment's context, kv head and tokens, the lane's token,
     // and the tiles left of the segment.
     const int32_t* row_of_table = nullptr;
     int kv = 0, left = 0;
     uint32_t begin = 0, end = 0, token = 0;
     bool more = true;
+    int number = 0;
     auto open = [&]() {   // the next segment that has tiles
       do {
-        if (!next_segment(0)) {
-          more = false;
-          return;
-        }
-        left = sh.segment[warp][0].u1 - sh.segment[warp][0].u0;
+        more = take(number);
+        if (!more) return;
+        const Segment& s = sh.ring[number % kRing];
+        left = s.u1 - s.u0;
+        row_of_table = a.c.table + s.b * a.c.table_stride;
+        kv = s.kv;
+        begin = s.begin;
+        end = s.end;
+        token = (uint32_t)s.start + (uint32_t)s.u0 * kTile + w * kMine + lane;
+        release(number++);
       } while (left == 0);
-      const Segment& s = sh.segment[warp][0];
-      row_of_table = a.c.table + s.b * a.c.table_stride;
-      kv = s.kv;
-      begin = s.begin;
-      end = s.end;
-      token = (uint32_t)s.start + (uint32_t)s.u0 * kTile + w * kMine + lane;
     };
     auto look = [&]() -> int32_t {
       return more && lane < kMine && token >= begin && token < end
@@ -846,99 +872,63 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       token += kTile;
       if (--left == 0) open();
     };
-    uint4 kreg[kIsBf16 ? 1 : kLoads], vreg[kIsBf16 ? 1 : kLoads];
-    auto fetch = [&](const void* cache, uint32_t rows, uint4* reg) {
+    uint4 reg[kIsBf16 ? 1 : kLoads];
+    auto fetch = [&](uint32_t rows, uint4* to) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t row = __shfl_sync(0xffffffffu, rows, i * kAtOnce + sub);
-        reg[i] = make_uint4(0u, 0u, 0u, 0u);
+        to[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row != kNoRow)
-          reg[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) +
-                                                   (uint64_t)row * kRowBytes + chunk * 16);
+          to[i] = *reinterpret_cast<const uint4*>(cache + (uint64_t)row * kRowBytes);
       }
     };
-    auto copy = [&](const void* cache, uint32_t rows, uint32_t base) {   // bf16: straight
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int r = i * kAtOnce + sub;
-        const uint32_t row = __shfl_sync(0xffffffffu, rows, r);
-        cp_async_16(place(base, kTile, w * kMine + r, chunk),
-                    static_cast<const uint8_t*>(cache) +
-                        (row == kNoRow ? 0 : (uint64_t)row * kRowBytes + chunk * 16),
-                    row == kNoRow ? 0u : 16u);
-      }
-    };
-    // codes to fp16: `by` an fp16 pair (ROUNDED: an fp32 factor) of the lane's token
-    auto convert = [&](const uint4* reg, uint32_t by, uint32_t base, auto rounded) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int r = i * kAtOnce + sub;
-        const uint32_t up = __shfl_sync(0xffffffffu, by, r);
-        const uint32_t in[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[j] = e4m3x2_to_f16(in[j >> 1] >> (16 * (j & 1)));
-          if (decltype(rounded)::value) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-            h[j] = pack_f16(f.x * __uint_as_float(up), f.y * __uint_as_float(up));
-          } else {
-            h[j] = mul_f16(h[j], up);
-          }
-        }
-        const int row = w * kMine + r;
-        st_shared_16(place(base, kTile, row, 2 * chunk), h[0], h[1], h[2], h[3]);
-        st_shared_16(place(base, kTile, row, 2 * chunk + 1), h[4], h[5], h[6], h[7]);
-      }
-    };
-    uint32_t now = kNoRow, then = kNoRow;   // the lane's rows of this tile and the next
-    float ks = 0.f, vs = 0.f;               // and its scales of the next tile
+    // scales of the lane's token: the keys' loaders need both (they tell the softmax)
+    float ks = 0.f, vs = 0.f;
     auto ask_scales = [&](uint32_t row) {
       ks = vs = 0.f;
       if (!kIsBf16 && row != kNoRow) {
-        ks = a.c.k_scale[row >> a.c.scale_shift];
+        if (keys) ks = a.c.k_scale[row >> a.c.scale_shift];
         vs = a.c.v_scale[row >> a.c.scale_shift];
       }
     };
     open();
     int32_t entry = look();
-    bool running = more;
+    bool running = more, ok = true;
+    uint32_t now = kNoRow;                  // the lane's row of this tile
     if (running) {
       now = row_of(entry);
       if (!kIsBf16) {   // (bf16 rows go straight to the stages)
-        fetch(a.c.k, now, kreg);
+        fetch(now, reg);
         ask_scales(now);
-        fetch(a.c.v, now, vreg);
       }
       advance();
       entry = look();
     }
-    bool pending = false;                   // bf16: a tile's values are under way
-    int pending_stage = 0;
-    while (running && ok) {
+    while (running) {
       // the tile's factors and masks
-      Side& side = sh.side[tile & (kSides - 1)];
       const unsigned mask = __ballot_sync(0xffffffffu, now != kNoRow);
-      uint32_t kby = 0u, vby = 0u;
+      uint32_t factor = 0u;
       int e = 0, f = 0;
       if (!kIsBf16) {
         const int none = -1000;
-        int ke = now != kNoRow && ks > 0.f ? max(exponent(ks), kLeastExponent) : none;
-        int ve = now != kNoRow && vs > 0.f ? max(exponent(vs), kLeastExponent) : none;
+        const int ke = ks > 0.f ? max(exponent(ks), kLeastExponent) : none;
+        const int ve = vs > 0.f ? max(exponent(vs), kLeastExponent) : none;
         const int ktop = __reduce_max_sync(0xffffffffu, ke);
         const int vtop = __reduce_max_sync(0xffffffffu, ve);
+        int(&maxima)[kLoadWarps][2] = sh.maxima[keys ? 0 : 1][tile & 1];
         if (lane == 0) {
-          sh.maxima[tile & 1][w][0] = ktop;
-          sh.maxima[tile & 1][w][1] = vtop;
+          maxima[w][0] = ktop;
+          maxima[w][1] = vtop;
         }
-        warp_arrive(&sh.maxed);
-        ok = warp_wait(&sh.maxed, tile & 1, sh, a.err, kErrTimeoutProducer);
+        uint64_t* const maxed = &sh.maxed[keys ? 0 : 1];
+        warp_arrive(maxed);
+        ok = warp_wait(maxed, tile & 1, sh, a.err, kErrTimeoutProducer);
         if (!ok) break;
         e = f = none;
 #pragma unroll
         for (int i = 0; i < kLoadWarps; ++i) {
-          e = max(e, sh.maxima[tile & 1][i][0]);
-          f = max(f, sh.maxima[tile & 1][i][1]);
+          e = max(e, maxima[i][0]);
+          f = max(f, maxima[i][1]);
         }
         // the largest codes (448) times what is left of the scales: below 2^15, or 2^16
         e = e == none || KIND == kTokenScales ? 0 : e - 6;
@@ -948,92 +938,96 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           const __half h = __float2half_rn(power(x));
           return (uint32_t)*reinterpret_cast<const uint16_t*>(&h) * 0x10001u;
         };
-        kby = KIND == kTokenScales ? 0x3c003c00u : ke == none ? 0u : pair(ke - e);
         if (KIND == kTokenScales)
-          vby = ve == none ? 0u : __float_as_uint(vs * power(-f));
+          factor = __float_as_uint(keys ? 1.f : ve == none ? 0.f : vs * power(-f));
+        else if (keys)
+          factor = ke == none ? 0u : pair(ke - e);
         else
-          vby = ve == none ? 0u : pair(ve - f);
+          factor = ve == none ? 0u : pair(ve - f);
       }
-      if (lane == 0) {
-        side.mask[w] = mask;
-        if (w == 0) {
-          side.key_up = power(e);
-          side.value_exp = (float)f;
+      if (keys) {
+        Side& side = sh.side[tile & (kSides - 1)];
+        if (lane == 0) {
+          side.mask[w] = mask;
+          if (w == 0) {
+            side.key_up = power(e);
+            side.value_exp = (float)f;
+          }
         }
+        if (KIND == kTokenScales && lane < kMine)
+          sh.key_scale[tile & (kSides - 1)][w * kMine + lane] = ks;
       }
-      if (KIND == kTokenScales && lane < kMine)
-        sh.key_scale[tile & (kSides - 1)][w * kMine + lane] = now != kNoRow ? ks : 0.f;
 
-      const uint32_t k_to = k_at + stage * S::kTileBytes, v_to = v_at + stage * S::kTileBytes;
-      ok = warp_wait(&sh.k_empty[stage], k_phase, sh, a.err, kErrTimeoutProducer);
-      if (!ok) break;
-      if (kIsBf16) {
-        copy(a.c.k, now, k_to);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (pending) {   // the last tile's values have landed
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          fence_proxy_async_smem();
-          warp_arrive(&sh.v_full[pending_stage]);
-        }
-        ok = warp_wait(&sh.v_empty[stage], v_phase, sh, a.err, kErrTimeoutProducer);
-        if (!ok) break;
-        copy(a.c.v, now, v_to);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        fence_proxy_async_smem();
-        warp_arrive(&sh.k_full[stage]);
-        pending = true;
-        pending_stage = stage;
-      } else {
-        convert(kreg, kby, k_to, std::false_type{});
-        fence_proxy_async_smem();
-        warp_arrive(&sh.k_full[stage]);
-      }
-      // the next tile
+      const uint32_t to = stages + stage * S::kTileBytes;
+      uint4 next[kIsBf16 ? 1 : kLoads];
+      const uint32_t mine = now;
       running = more;
       if (running) {
-        then = row_of(entry);
+        now = row_of(entry);
         if (!kIsBf16) {
-          fetch(a.c.k, then, kreg);
-          ask_scales(then);
+          fetch(now, next);
+          ask_scales(now);
         }
         advance();
         entry = look();
       }
-      if (!kIsBf16) {
-        ok = warp_wait(&sh.v_empty[stage], v_phase, sh, a.err, kErrTimeoutProducer);
-        if (!ok) break;
-        if (KIND == kTokenScales) convert(vreg, vby, v_to, std::true_type{});
-        else convert(vreg, vby, v_to, std::false_type{});
-        fence_proxy_async_smem();
-        warp_arrive(&sh.v_full[stage]);
-        if (running) fetch(a.c.v, then, vreg);
+      ok = warp_wait(&empty[stage], phase, sh, a.err, kErrTimeoutProducer);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kAtOnce + sub, row = w * kMine + r;
+        if (kIsBf16) {
+          const uint32_t from = __shfl_sync(0xffffffffu, mine, r);
+          cp_async_16(place(to, kTile, row, chunk),
+                      cache + (from == kNoRow ? 0 : (uint64_t)from * kRowBytes),
+                      from == kNoRow ? 0u : 16u);
+        } else {
+          const uint32_t up = __shfl_sync(0xffffffffu, factor, r);
+          const uint32_t in[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h[j] = e4m3x2_to_f16(in[j >> 1] >> (16 * (j & 1)));
+            if (KIND == kTokenScales) {
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+              h[j] = pack_f16(v.x * __uint_as_float(up), v.y * __uint_as_float(up));
+            } else {
+              h[j] = mul_f16(h[j], up);
+            }
+          }
+          st_shared_16(place(to, kTile, row, 2 * chunk), h[0], h[1], h[2], h[3]);
+          st_shared_16(place(to, kTile, row, 2 * chunk + 1), h[4], h[5], h[6], h[7]);
+        }
       }
-      now = then;
+      if (kIsBf16) {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&full[stage]);
+      if (!kIsBf16) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) reg[i] = next[i];
+      }
       ++tile;
       if (++stage == S::kStages) {
         stage = 0;
-        k_phase ^= 1u;
-        v_phase ^= 1u;
+        phase ^= 1u;
       }
     }
-    if (kIsBf16) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      if (ok && pending) {
-        fence_proxy_async_smem();
-        warp_arrive(&sh.v_full[pending_stage]);
-      }
-    }
-  } else if (warp == kMmaWarp) {
+  } else {
+    fewer_registers<kMmaRegs>();
+    if (warp == kMmaWarp) {
     // ---------------- products ----------------
     uint32_t k_phase = 0u, v_phase = 0u;
     uint32_t q_phase = 0u, p_phase = 0u, oe_phase = 3u;   // bits 0, 1 (O is free at first)
     int k_stage = 0, v_stage = 0;
     bool ok = true;
     constexpr uint32_t kQk = idesc_f16(kIsBf16, kTile, false), kPv = idesc_f16(kIsBf16, D, true);
-    while (ok && next_segment(0)) {
-      const int streams = streams_of(sh.segment[warp][0]);
-      const int tiles = sh.segment[warp][0].u1 - sh.segment[warp][0].u0;
+    for (int number = 0; ok && take(number); ++number) {
+      const int streams = streams_of(sh.ring[number % kRing]);
+      const int tiles = sh.ring[number % kRing].u1 - sh.ring[number % kRing].u0;
+      release(number);
       if (tiles == 0) continue;
       const int tasks = tiles * streams;
       // task t: the scores, then the weights and products, of stream t % streams and tile
@@ -1085,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         p_phase ^= 1u << slot;
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t d = tmem + S::kSOut + stream * D, p = tmem + slot * kTile;
+          const uint32_t d = tmem + S::kSOut + stream * D, p = tmem + slot * kTile + S::kPOut;
           const uint32_t vs = v_at + v_stage * S::kTileBytes;
 #pragma unroll
           for (int i = 0; i < kTile / 16; ++i)
@@ -1107,6 +1101,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     __syncwarp();
     volatile int no_abort = 0;
     mbar_wait_bounded(smem_u32(&sh.drain), 0, &no_abort, a.err, kErrTimeoutDrain);
+    } else if (warp == kPlanWarp) {
+      // ---------------- the work, segment by segment ----------------
+      Walk walk;
+      walk.b = sh.place[0][0];
+      walk.kv = sh.place[0][1];
+      walk.item = sh.place[0][2];
+      walk.unit = sh.place[0][3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) walk.end[i] = sh.place[1][i];
+      if (walk.b < a.batch) walk.c = context_of<kRows>(a, sh.request[0], sh.request[1].x);
+      bool more = true;
+      for (int n = 0; more; ++n) {
+        Segment s;
+        more = next_of<kRows, kTile>(a, sh, walk, s);
+        if (!more) s.units = -1;
+        if (!warp_wait(&sh.seg_empty[n % kRing], ((n / kRing) & 1) ^ 1, sh, a.err,
+                       kErrTimeoutSched))
+          break;
+        if (lane == 0) sh.ring[n % kRing] = s;
+        warp_arrive(&sh.seg_full[n % kRing]);
+      }
+    }
   }
   __syncwarp();
   tc_fence_before_sync();
