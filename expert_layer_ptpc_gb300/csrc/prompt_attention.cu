@@ -230,30 +230,49 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int n, bool b_rows_a
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
          ((b_rows_along_n ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-// Descriptor of an operand whose rows run along its outer dimension (values: a row of 64
-// elements of one token, 128 bytes, swizzled): groups of 8 tokens 1024 bytes apart, blocks
-// of 64 elements `block` bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(block >> 4) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Operand descriptors (smem_desc_k_sw128's fields) as a low word that counts with the address,
+// and a constant high one: 8-row groups 1024 bytes apart, 128-byte swizzle. Rows along the
+// contraction; or along the outer dimension (values: a row is 64 elements of one token), with
+// the blocks of 64 elements `block` bytes apart.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t block) {
+  return saddr >> 4 | (block >> 4) << 16;
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
+}
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+// The same value in every lane, so that the compiler knows it.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // ---- the work ----
@@ -1043,14 +1062,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
           return false;
         tc_fence_after_sync();
-        if (lane == 0) {
-          const uint32_t d = tmem + (t & 1) * kTile;
-          const uint32_t qs = q_at + stream * S::kQBytes, ks = k_at + k_stage * S::kTileBytes;
+        const uint32_t d = uniform(tmem + (t & 1) * kTile);
+        const uint32_t qs = uniform(desc_k(q_at + stream * S::kQBytes));
+        const uint32_t ks = uniform(desc_k(k_at + k_stage * S::kTileBytes));
+        if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
-            mma_f16_ss(d, smem_desc_k_sw128(qs + (i >> 2) * (128 * 128) + (i & 3) * 32),
-                       smem_desc_k_sw128(ks + (i >> 2) * (kTile * 128) + (i & 3) * 32), kQk,
-                       i > 0 ? 1u : 0u);
+            mma_f16_ss(d, qs + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
+                       ks + ((i >> 2) * (kTile * 128) + (i & 3) * 32) / 16, kQk, i > 0 ? 1u : 0u);
           mma_commit(smem_u32(&sh.s_full[t & 1]));
           if (stream == streams - 1) mma_commit(smem_u32(&sh.k_empty[k_stage]));
         }
@@ -1078,13 +1097,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         if (!ok) break;
         p_phase ^= 1u << slot;
         tc_fence_after_sync();
-        if (lane == 0) {
-          const uint32_t d = tmem + S::kSOut + stream * D, p = tmem + slot * kTile + S::kPOut;
-          const uint32_t vs = v_at + v_stage * S::kTileBytes;
+        const uint32_t d = uniform(tmem + S::kSOut + stream * D);
+        const uint32_t p = uniform(tmem + slot * kTile + S::kPOut);
+        const uint32_t vs = uniform(desc_mn(v_at + v_stage * S::kTileBytes, kTile * 128));
+        const uint32_t more = uniform(t >= streams ? 1u : 0u);
+        if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kTile / 16; ++i)
-            mma_f16_ts(d, p + 8 * i, smem_desc_mn_sw128(vs + i * 2048, kTile * 128), kPv,
-                       t >= streams || i > 0 ? 1u : 0u);
+            mma_f16_ts(d, p + 8 * i, vs + i * (2048 / 16), kPv, i > 0 ? 1u : more);
           mma_commit(smem_u32(&sh.o_full[stream]));
           if (stream == streams - 1) mma_commit(smem_u32(&sh.v_empty[v_stage]));
         }
