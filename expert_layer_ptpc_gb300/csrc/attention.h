@@ -26,6 +26,9 @@ struct RotaryArgs {
   float *k_scale, *v_scale;
   uint32_t cache_slots;
   int page_shift;
+  // Whether the launch runs beside the one before it, of whose results it needs none: it
+  // begins with that one, and lets the next begin only when both have ended.
+  bool beside;
 };
 int launch_rotary(const RotaryArgs& a, int sink, bool neighbours, cudaStream_t stream);
 

@@ -12,11 +12,13 @@
 // subnormal there. e4m3 spans 2^-9 to 448, so that against a scale that brings the
 // largest element to 448 a power of two costs at most the lowest binade of those 18.
 //
-// A block takes the runs of tokens that begin in its part of the call, for one head of
-// k or v. A run is what the call brings to one page: tokens that follow one another
-// with slots of the same page. Its maximum has to be known before its first code, so
-// the first 4 units of a thread (64 tokens of 128 elements) stay in registers between,
-// and the rest are read twice. Bound by memory: 2 bytes an element in, 1 out.
+// A team of one or four warps takes the runs of tokens that begin in its part of the call,
+// for one head of k or v. A run is what the call brings to one page: tokens that follow
+// one another with slots of the same page. Its maximum has to be known before its first
+// code, so the first 4 units of a thread stay in registers between, and the rest are read
+// twice: one warp for pages of up to 16 tokens of 128 elements, four for larger ones. Bound by
+// memory: 2 bytes an element in, 1 out. q is rotated by a launch of its own, which runs
+// beside this one.
 #include <algorithm>
 
 #include "attention.h"
@@ -30,9 +32,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;       // of a block
 constexpr int kKept = 4;        // units of a thread in registers
-constexpr int kMostTokens = 64; // of a block's part
+constexpr int kMostTokens = 64; // of a team's part
 constexpr float kLeastScale = 0x1p-48f;
 
 // 2^e, e the least integer >= -48 with amax <= 448 * 2^e (448 = 1.75 * 2^8).
@@ -64,28 +66,37 @@ __device__ __forceinline__ uint32_t scaled_codes(uint32_t w, float by) {
   return out;
 }
 
-template <int PAIRS>
-__global__ void __launch_bounds__(kThreads) page_write_kernel(const RotaryArgs a, int part) {
-  __shared__ int32_t slots[kMostTokens + 1];   // of the part, and of the token before it
-  __shared__ int ends[kThreads / 32], begins[kThreads / 32];
-  __shared__ float maxima[kThreads / 32];
+// TEAM: warps of a team.
+template <int PAIRS, int TEAM>
+__global__ void __launch_bounds__(32 * kWarps) page_write_kernel(const RotaryArgs a, int part) {
+  constexpr int kThreads = 32 * TEAM;
+  // of each team: the slots of its part and of the token before it; its warps' findings
+  __shared__ int32_t all_slots[kWarps / TEAM][kMostTokens + 1];
+  __shared__ int ends[TEAM], begins[TEAM];
+  __shared__ float maxima[TEAM];
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * part, here = min(part, a.T - t0);
+  const int lane = threadIdx.x & 31, team = threadIdx.x / kThreads, me = threadIdx.x % kThreads;
+  const int warp = me >> 5;
+  const int64_t t_begin = ((int64_t)blockIdx.x * (kWarps / TEAM) + team) * part;
+  if (TEAM == 1 && t_begin >= a.T) return;
+  const int t0 = (int)t_begin, here = min(part, a.T - t0);
   const bool is_v = (blockIdx.y & 1) != 0;
   const int head = blockIdx.y >> 1;
   const int size = 1 << a.page_shift;
-  for (int i = threadIdx.x; i <= here; i += kThreads)
-    slots[i] = t0 + i > 0 ? a.slots[t0 + i - 1] : -1;
-  __syncthreads();
+  int32_t* const slots = all_slots[team];
+  auto sync = [&]() {
+    if (TEAM == 1) __syncwarp(); else __syncthreads();
+  };
+  for (int i = me; i <= here; i += kThreads) slots[i] = t0 + i > 0 ? a.slots[t0 + i - 1] : -1;
+  sync();
   // the page of a slot (-1: none)
   auto page_of = [&](int32_t slot) -> int {
     return (uint32_t)slot < a.cache_slots ? slot >> a.page_shift : -1;
   };
 
-  const int units = a.head_dim / kUnit, u = threadIdx.x % units;   // of a token
-  const int first = threadIdx.x / units, step = kThreads / units;  // tokens
+  const int units = a.head_dim / kUnit, u = me % units;   // of a token
+  const int first = me / units, step = kThreads / units;  // tokens
   const int rot_units = PAIRS == kNoPairs || is_v ? 0 : a.rot / kUnit;
   const bool rotates = u < rot_units;
   const int from = rotates || rot_units == 0 ? 0 : a.rot;
@@ -119,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(const RotaryArgs a
     // the run: tokens [t, t + n), and whether it begins the page
     const int t = t0 + i;
     int end = size, zero = size;   // (slots differ, so that a run has at most `size` tokens)
-    for (int j = threadIdx.x; j < size; j += kThreads) {
+    for (int j = me; j < size; j += kThreads) {
       const int32_t slot = t + j < a.T ? a.slots[t + j] : -1;
       if (page_of(slot) != page) {
         end = j;
@@ -129,15 +140,17 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(const RotaryArgs a
     }
     end = __reduce_min_sync(0xffffffffu, end);
     zero = __reduce_min_sync(0xffffffffu, zero);
-    if (lane == 0) {
-      ends[warp] = end;
-      begins[warp] = zero;
-    }
-    __syncthreads();
+    if (TEAM > 1) {
+      if (lane == 0) {
+        ends[warp] = end;
+        begins[warp] = zero;
+      }
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      end = min(end, ends[w]);
-      zero = min(zero, begins[w]);
+      for (int w = 0; w < TEAM; ++w) {
+        end = min(end, ends[w]);
+        zero = min(zero, begins[w]);
+      }
     }
     const int n = end;
     const bool begun = zero < n;
@@ -160,16 +173,18 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(const RotaryArgs a
       top = fmaxf(top, largest(y));
     }
     top = warp_max(top);
-    if (lane == 0) maxima[warp] = top;
-    __syncthreads();
+    if (TEAM > 1) {
+      if (lane == 0) maxima[warp] = top;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, maxima[w]);
+      for (int w = 0; w < TEAM; ++w) top = fmaxf(top, maxima[w]);
+    }
     const float scale = fmaxf(was, page_scale(top)), by = __frcp_rn(scale);
     uint8_t* const out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) +
                          (block << a.page_shift) * a.head_dim;
     if (!begun && scale > was) {   // the codes that stay (the run's are written over them)
       const float down = was * by;
-      for (int c = threadIdx.x; c < size * a.head_dim / 16; c += kThreads) {
+      for (int c = me; c < size * a.head_dim / 16; c += kThreads) {
         uint4 w = reinterpret_cast<uint4*>(out)[c];
         w.x = scaled_codes(w.x, down);
         w.y = scaled_codes(w.y, down);
@@ -177,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(const RotaryArgs a
         w.w = scaled_codes(w.w, down);
         reinterpret_cast<uint4*>(out)[c] = w;
       }
-      __syncthreads();
+      sync();
     }
     auto store = [&](int t, const float* x) {
       uint8_t* const row = out + (a.slots[t] & (size - 1)) * a.head_dim;
@@ -194,27 +209,37 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(const RotaryArgs a
       load(t + j, y);
       store(t + j, y);
     }
-    if (threadIdx.x == 0) *scale_at = scale;
+    // (every lane has read the scale that was)
+    if (TEAM == 1) __syncwarp();
+    if (me == 0) *scale_at = scale;
   }
+}
+
+template <int TEAM>
+cudaError_t launch(const RotaryArgs& a, bool neighbours, cudaStream_t stream) {
+  // tokens of a team: so that there are enough teams to fill the GPU
+  const int64_t work = (int64_t)a.T * 2 * a.k_heads, teams = 16384 / TEAM;
+  const int part = (int)std::min<int64_t>(kMostTokens, std::max<int64_t>(1, work / teams));
+  void (*kernel)(RotaryArgs, int) = a.rot == 0   ? page_write_kernel<kNoPairs, TEAM>
+                                    : neighbours ? page_write_kernel<kNeighbours, TEAM>
+                                                 : page_write_kernel<kHalves, TEAM>;
+  const int64_t of_block = (int64_t)part * (kWarps / TEAM);   // tokens
+  return launch_kernel(true, dim3((unsigned)((a.T + of_block - 1) / of_block), 2 * a.k_heads),
+                       dim3(32 * kWarps), 0, stream, kernel, a, part);
 }
 
 }  // namespace
 
 int launch_page_write(const RotaryArgs& a, bool neighbours, cudaStream_t stream) {
-  if (a.q_heads > 0) {
-    RotaryArgs q = a;
-    q.k_heads = 0;
-    if (const int st = launch_rotary(q, 0, neighbours, stream)) return st;
-  }
-  // tokens of a block: so that there are enough blocks to fill the GPU
-  const int64_t work = (int64_t)a.T * 2 * a.k_heads;
-  const int part = (int)std::min<int64_t>(kMostTokens, std::max<int64_t>(1, work / 4096));
-  void (*kernel)(RotaryArgs, int) = a.rot == 0   ? page_write_kernel<kNoPairs>
-                                    : neighbours ? page_write_kernel<kNeighbours>
-                                                 : page_write_kernel<kHalves>;
-  const cudaError_t e = launch_kernel(true, dim3((a.T + part - 1) / part, 2 * a.k_heads),
-                                      dim3(kThreads), 0, stream, kernel, a, part);
-  return e == cudaSuccess ? 0 : -3;
+  const int units = a.head_dim / kUnit << a.page_shift;   // of a full page
+  const cudaError_t e =
+      units <= 32 * kKept ? launch<1>(a, neighbours, stream) : launch<4>(a, neighbours, stream);
+  if (e != cudaSuccess) return -3;
+  if (a.q_heads == 0) return 0;
+  RotaryArgs q = a;
+  q.k_heads = 0;
+  q.beside = true;
+  return launch_rotary(q, 0, neighbours, stream);
 }
 
 }  // namespace moe

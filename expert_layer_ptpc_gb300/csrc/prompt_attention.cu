@@ -879,17 +879,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
                  ? row_of_table[token >> a.c.page_shift]
                  : -1;
     };
-    // the lane's cache row, all ones for none
-    constexpr uint32_t kNoRow = 0xffffffffu;
-    auto row_of = [&](int32_t entry) -> uint32_t {
-      return (uint32_t)entry < (uint32_t)a.c.pages
-                 ? (((uint32_t)entry * a.c.heads + kv) << a.c.page_shift) +
-                       (token & ((1u << a.c.page_shift) - 1u))
-                 : kNoRow;
-    };
     auto advance = [&]() {
       token += kTile;
       if (--left == 0) open();
+    };
+    // What is known of the tiles ahead: the table entry of one that is looked up, and the
+    // lane's cache row (all ones for none) of the one before it, whose lines are
+    // on their way to L2.
+    constexpr uint32_t kNoRow = 0xffffffffu;
+    int32_t entry = -1;
+    uint32_t spot = 0;
+    bool asked = false;
+    auto ask = [&]() {
+      asked = more;
+      entry = look();
+      spot = ((uint32_t)kv << a.c.page_shift) + (token & ((1u << a.c.page_shift) - 1u));
+      if (more) advance();
+    };
+    auto resolve = [&]() -> uint32_t {
+      if ((uint32_t)entry >= (uint32_t)a.c.pages) return kNoRow;
+      const uint32_t row = (((uint32_t)entry * a.c.heads) << a.c.page_shift) + spot;
+#pragma unroll
+      for (int i = 0; i < (kRowBytes + 127) / 128; ++i)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(cache - chunk * 16 +
+                                                      (uint64_t)row * kRowBytes + 128 * i));
+      return row;
     };
     uint4 reg[kIsBf16 ? 1 : kLoads];
     auto fetch = [&](uint32_t rows, uint4* to) {
@@ -911,17 +925,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       }
     };
     open();
-    int32_t entry = look();
-    bool running = more, ok = true;
-    uint32_t now = kNoRow;                  // the lane's row of this tile
-    if (running) {
-      now = row_of(entry);
-      if (!kIsBf16) {   // (bf16 rows go straight to the stages)
-        fetch(now, reg);
-        ask_scales(now);
-      }
-      advance();
-      entry = look();
+    ask();
+    bool running = asked, ok = true;
+    uint32_t now = resolve();               // the lane's row of this tile
+    ask();
+    bool follows = asked;
+    uint32_t then = resolve();              // and of the next
+    ask();
+    if (running && !kIsBf16) {              // (bf16 rows go straight to the stages)
+      fetch(now, reg);
+      ask_scales(now);
     }
     while (running) {
       // the tile's factors and masks
@@ -980,16 +993,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       const uint32_t to = stages + stage * S::kTileBytes;
       uint4 next[kIsBf16 ? 1 : kLoads];
       const uint32_t mine = now;
-      running = more;
-      if (running) {
-        now = row_of(entry);
-        if (!kIsBf16) {
-          fetch(now, next);
-          ask_scales(now);
-        }
-        advance();
-        entry = look();
+      running = follows;
+      now = then;
+      if (running && !kIsBf16) {
+        fetch(now, next);
+        ask_scales(now);
       }
+      follows = asked;
+      then = resolve();
+      ask();
       ok = warp_wait(&empty[stage], phase, sh, a.err, kErrTimeoutProducer);
       if (!ok) break;
 #pragma unroll

@@ -88,8 +88,14 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks)
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* const flight = smem + (threadIdx.x >> 5) * (kAhead * 1024);
   float2* const turns = reinterpret_cast<float2*>(smem + kWarps * kAhead * 1024);
-  pdl_wait();
-  pdl_launch_dependents();
+  if (!a.beside) {
+    pdl_wait();
+    pdl_launch_dependents();
+  } else if (blockIdx.x == gridDim.x - 1) {
+    // (what q depends on had ended when the launch before this one began; the last block
+    // sees that launch out, and without a word to the next that waits for all of this one)
+    pdl_wait();
+  }
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int t = (int)(w / parts);
