@@ -59,7 +59,7 @@ constexpr int kThreads = 32 * (kMmaWarp + 4);
 // Registers of a thread, by role (640 threads are launched with 96 each: 61440).
 constexpr int kSoftRegs = 128, kLoadRegs = 88, kMmaRegs = 48;
 static_assert(256 * kSoftRegs + 256 * kLoadRegs + 128 * kMmaRegs <= 96 * kThreads, "registers");
-constexpr int kRing = 8;                   // segments handed out at a time
+constexpr int kRing = 16;                  // segments handed out at a time
 constexpr int kSides = 8;                  // tiles whose masks and factors are at hand
 constexpr int kRequests = 256;             // contexts whose places a CTA keeps at hand
 constexpr float kMostWeight = 15.0f;       // log2 of the largest weight let stand,
@@ -106,8 +106,11 @@ struct Shape {
   static constexpr int kStages = D == 64 ? 3 : 2;
   static constexpr int kQBytes = 128 * D * 2;             // of a stream
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kSOut = 2 * kTile;                 // TMEM: two tiles of scores, then O
-  static constexpr int kPOut = kTile - kTile / 2;         // the weights in a tile of scores
+  // TMEM: tiles of scores, one a stream, or two in turn where there is one stream; then O. A
+  // tile's weights lie in the second half of its scores.
+  static constexpr int kSlots = 2 / kStreams;
+  static constexpr int kSOut = 2 * kTile;
+  static constexpr int kPOut = kTile / 2;
   static constexpr int kCols = 512;
   static constexpr int kSmemBytes = 1024 + kStreams * kQBytes + 2 * kStages * kTileBytes;
   static_assert(kSOut + kStreams * D <= kCols, "tensor memory");
@@ -146,7 +149,7 @@ struct Side {
 struct Shared {
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t halves, maxed[2], drain, seg_full[kRing], seg_empty[kRing];
+  uint64_t maxed[2], drain, seg_full[kRing], seg_empty[kRing];
   uint32_t tmem;
   int abort;
   Side side[kSides];
@@ -163,6 +166,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -417,19 +425,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.q_full[i]), 4);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
       mbar_init(smem_u32(&sh.p_full[i]), 4);
+      mbar_init(smem_u32(&sh.q_full[i]), 4);
       mbar_init(smem_u32(&sh.o_full[i]), 1);
       mbar_init(smem_u32(&sh.o_empty[i]), 4);
     }
-    mbar_init(smem_u32(&sh.halves), kSoftWarps);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.maxed[i]), kLoadWarps);
+    mbar_init(smem_u32(&sh.drain), 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&sh.seg_full[i]), 1);
       mbar_init(smem_u32(&sh.seg_empty[i]), 4 * S::kStreams + 2 * kLoadWarps + 1);
     }
-    mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.place[0][0] = sh.place[1][0] = a.batch;   // nothing to do
     fence_barrier_init();
@@ -549,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     const int me = warp >> 2;                 // the stream of two, and the half of TMEM
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // of TMEM
-    uint32_t s_phase = 0u;                    // of the two halves of the scores: bits 0, 1
-    uint32_t o_phase = 0u, halves_phase = 0u;
+    uint32_t s_phase = 0u;                    // of the stream's tiles of scores: bits 0, 1
+    uint32_t o_phase = 0u;
     int tile = 0;                             // of all tiles (sides), at the segment's start
     bool ok = true;
     // This half's rows of q, a warp the rows of its threads; the factor of each.
@@ -609,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       fence_proxy_async_smem();
       warp_arrive(&sh.q_full[me]);
     };
-    auto has_q = [&](const Segment& s) { return s.u1 > s.u0 && me < streams_of(s); };
+    auto has_q = [&](const Segment& s) { return me < streams_of(s); };
     int number = 0;
     bool running = me < S::kStreams && take(0);
     if (running && has_q(sh.ring[0])) load_q(sh.ring[0]);
@@ -628,21 +635,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
                          ? (int)max((int64_t)seg.place + token + 1 - a.window, (int64_t)0) : 0;
       float top = -INFINITY, sum = 0.f;
       const uint32_t o_at = tmem + lanes + S::kSOut + me * D;
-      if (mine && tiles > 0) {
+      if (mine) {
         const float factor = sh.row_scale[me * 128 + row];
         const int start = seg.start + seg.u0 * kTile;
         for (int i = 0; ok && i < tiles; ++i) {
-          const int slot = streams == 2 ? me : i & 1;
+          const int turn = S::kSlots == 2 ? i & 1 : 0, slot = me + turn;
           const uint32_t s_at = tmem + lanes + slot * kTile;
-          ok = warp_wait(&sh.s_full[slot], (s_phase >> slot) & 1u, sh, a.err, kErrTimeoutEpilogue);
+          ok = warp_wait(&sh.s_full[slot], (s_phase >> turn) & 1u, sh, a.err,
+                         kErrTimeoutEpilogue);
           if (!ok) break;
-          s_phase ^= 1u << slot;
+          s_phase ^= 1u << turn;
+          // The last tile's products. With one tile of scores in TMEM, these came after them;
+          // with two, they are waited for before O is touched, and before the barrier can get a
+          // phase further.
+          auto last_products = [&]() -> bool {
+            return S::kSlots == 1 || i == 0 ||
+                   warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
+          };
           if (!works) {
-            if (streams == 1 && i > 0)
-              ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
+            ok = last_products();
             if (!ok) break;
             warp_arrive(&sh.p_full[slot]);
-            o_phase ^= 1u;
+            if (S::kSlots == 2 || i == tiles - 1) o_phase ^= 1u;
             continue;
           }
           tc_fence_after_sync();
@@ -651,19 +665,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           const float c = fmaxf(factor * side.key_up, 0x1p-120f), f = side.value_exp;
           // what this row sees of the tile
           const int first = start + i * kTile;
-          constexpr uint32_t kAll = kTile == 128 ? 0xffffffffu : 0xffffu;
-          const bool all_there = (side.mask[0] & side.mask[1] & side.mask[2] & side.mask[3]) == kAll;
+          constexpr int kBits = kTile / kLoadWarps;   // tokens of a mask
+          constexpr uint32_t kAll = kBits == 32 ? 0xffffffffu : 0xffffu;
+          const uint32_t there = side.mask[0] & side.mask[1] & side.mask[2] & side.mask[3];
           const bool clear =
-              __all_sync(0xffffffffu, all_there && lo <= first && hi - first >= kTile);
+              __all_sync(0xffffffffu, there == kAll && lo <= first && hi - first >= kTile);
           // 64 scores at a time: all for their maximum, the last of them kept, and then the
           // others again for the weights (128 would not fit the registers). What a row does not
           // see is put back as -inf, keys' own scales with them. (The loops stay
-          // rolled: five roles' code has to fit the instruction caches.)
+          // rolled: the roles' code has to fit the instruction caches.)
           float s[64], high = -INFINITY;
 #pragma unroll 1
           for (int h = 0; h < kTile / 64; ++h) {
             float m = tmem_load_max(s_at + 64 * h, s);
-            if (KIND == kTokenScales || !clear) {
+            if (KIND == kTokenScales || __builtin_expect(!clear, 0)) {
               if (KIND == kTokenScales) {
                 const float4* const scales = reinterpret_cast<const float4*>(
                     sh.key_scale[(tile + i) & (kSides - 1)] + 64 * h);
@@ -677,7 +692,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
                 }
               }
               if (!clear) {
-                constexpr int kBits = kTile / kLoadWarps;   // tokens of a mask
 #pragma unroll
                 for (int w = 0; w < 64 / kBits; ++w) {
                   const int at = first + 64 * h + w * kBits;
@@ -690,11 +704,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
                     if (!((bits >> j) & 1u)) s[w * kBits + j] = -INFINITY;
                 }
               }
-              float top4[4] = {s[0], s[1], s[2], s[3]};
+              float t[2] = {s[0], s[1]};
 #pragma unroll
-              for (int j = 4; j < 64; ++j) top4[j & 3] = fmaxf(top4[j & 3], s[j]);
-              m = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-              if (kTile > 64 && h == 0) {
+              for (int j = 2; j < 62; j += 4) {
+                t[0] = max3(t[0], s[j], s[j + 1]);
+                t[1] = max3(t[1], s[j + 2], s[j + 3]);
+              }
+              m = max3(fmaxf(t[0], t[1]), s[62], s[63]);
+              if (h < kTile / 64 - 1) {
                 tmem_store(s_at, s);
                 tmem_store_wait();
               }
@@ -702,19 +719,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             high = fmaxf(high, m);
           }
           const float z = fmaf(high, c, f);
-          if (streams == 1 && i > 0) {
-            // the last tile's products, before O is touched and before the barrier can get
-            // a phase further (with two streams, these scores came after them)
-            ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
-            if (!ok) break;
-            tc_fence_after_sync();
-          }
-          if (__any_sync(0xffffffffu, z > top + kMostWeight)) {
+          bool waited = false;
+          if (__builtin_expect(__any_sync(0xffffffffu, z > top + kMostWeight), 0)) {
             const float next = fmaxf(top, z - kNewWeight);
             const float down = top == -INFINITY ? 0.f : exp2_approx(top - next);
             top = next;
             sum *= down;
             if (i > 0) {
+              ok = last_products();
+              if (!ok) break;
+              waited = true;
+              tc_fence_after_sync();
 #pragma unroll 1
               for (int j = 0; j < D / 32; ++j) {
                 float o[32];
@@ -745,36 +760,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           sum = fmaf((add[0].x + add[1].x) + (add[0].y + add[1].y), exp2_approx(-f), sum);
           tmem_store_wait();
           tc_fence_before_sync();
+          if (!waited) {
+            ok = last_products();
+            if (!ok) break;
+          }
           warp_arrive(&sh.p_full[slot]);
-          o_phase ^= 1u;
+          if (S::kSlots == 2 || i == tiles - 1) o_phase ^= 1u;   // (commits on o_full)
         }
         if (!ok) break;
       }
       // q of the next segment, behind the last scores of this one
       running = take(number + 1);
       if (running && has_q(sh.ring[(number + 1) % kRing])) load_q(sh.ring[(number + 1) % kRing]);
-      if (mine && tiles > 0) {
+      if (mine) {
         // the last products (o_phase has moved past them)
         ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
         if (!ok) break;
         tc_fence_after_sync();
       }
-      // the other half's tiles and segments, counted
-      if (tiles > 0) {
-        if (streams == 2)
-          s_phase ^= (uint32_t)(tiles & 1) << (me ^ 1);
-        else if (!mine)
-          s_phase ^= (uint32_t)(((tiles + 1) >> 1) & 1) | (uint32_t)((tiles >> 1) & 1) << 1;
-        tile += tiles;
-      }
-      if (S::kStreams == 2 && streams == 1 && tiles > 0) {
-        // the half without rows waits for the other: barriers it did not wait on have
-        // completed every phase of the segment before it counts on them again
-        warp_arrive(&sh.halves);
-        ok = warp_wait(&sh.halves, halves_phase, sh, a.err, kErrTimeoutEpilogue);
-        if (!ok) break;
-        halves_phase ^= 1u;
-      }
+      tile += tiles;
       if (!mine) continue;
       const int64_t slot = 2 * worker + (seg.u0 == 0 ? 1 : 0);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -786,12 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       for (int j = 0; j < D / 32; ++j) {
         float o[32];
         __syncwarp();
-        if (tiles > 0) {
-          tmem_load(o_at + 32 * j, o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
-        }
+        tmem_load(o_at + 32 * j, o);
         if (live && whole) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -807,10 +806,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      if (tiles > 0) {
-        tc_fence_before_sync();
-        warp_arrive(&sh.o_empty[me]);
-      }
+      tc_fence_before_sync();
+      warp_arrive(&sh.o_empty[me]);
       if (live) {
         if (!whole) a.stats[slot * kRows + me * 128 + row] = make_float2(top, sum);
         else if (a.lse != nullptr)
@@ -860,19 +857,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     uint32_t begin = 0, end = 0, token = 0;
     bool more = true;
     int number = 0;
-    auto open = [&]() {   // the next segment that has tiles
-      do {
-        more = take(number);
-        if (!more) return;
-        const Segment& s = sh.ring[number % kRing];
-        left = s.u1 - s.u0;
-        row_of_table = a.c.table + s.b * a.c.table_stride;
-        kv = s.kv;
-        begin = s.begin;
-        end = s.end;
-        token = (uint32_t)s.start + (uint32_t)s.u0 * kTile + w * kMine + lane;
-        release(number++);
-      } while (left == 0);
+    auto open = [&]() {   // the next segment
+      more = take(number);
+      if (!more) return;
+      const Segment& s = sh.ring[number % kRing];
+      left = s.u1 - s.u0;
+      row_of_table = a.c.table + s.b * a.c.table_stride;
+      kv = s.kv;
+      begin = s.begin;
+      end = s.end;
+      token = (uint32_t)s.start + (uint32_t)s.u0 * kTile + w * kMine + lane;
+      release(number++);
     };
     auto look = [&]() -> int32_t {
       return more && lane < kMine && token >= begin && token < end
@@ -1049,90 +1044,92 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   } else {
     fewer_registers<kMmaRegs>();
     if (warp == kMmaWarp) {
-    // ---------------- products ----------------
-    uint32_t k_phase = 0u, v_phase = 0u;
-    uint32_t q_phase = 0u, p_phase = 0u, oe_phase = 3u;   // bits 0, 1 (O is free at first)
-    int k_stage = 0, v_stage = 0;
-    bool ok = true;
-    constexpr uint32_t kQk = idesc_f16(kIsBf16, kTile, false), kPv = idesc_f16(kIsBf16, D, true);
-    for (int number = 0; ok && take(number); ++number) {
-      const int streams = streams_of(sh.ring[number % kRing]);
-      const int tiles = sh.ring[number % kRing].u1 - sh.ring[number % kRing].u0;
-      release(number);
-      if (tiles == 0) continue;
-      const int tasks = tiles * streams;
-      // task t: the scores, then the weights and products, of stream t % streams and tile
-      // t / streams, in half t % 2 of the scores' tensor memory
-      auto scores = [&](int t) -> bool {
-        const int stream = streams == 2 ? t & 1 : 0;
-        if (t < streams) {   // the stream's rows of q
-          if (!warp_wait(&sh.q_full[stream], (q_phase >> stream) & 1u, sh, a.err, kErrTimeoutMma))
+      // ---------------- products ----------------
+      // (One thread issues a product in about 50 cycles, whatever its size, and a wait or a
+      // commit in 100 or so more: what it issues is kept to the least.)
+      uint32_t k_phase = 0u, v_phase = 0u;
+      uint32_t q_phase = 0u, p_phase = 0u, oe_phase = 3u;   // bits 0, 1 (O is free at first)
+      int k_stage = 0, v_stage = 0;
+      bool ok = true;
+      constexpr uint32_t kQk = idesc_f16(kIsBf16, kTile, false), kPv = idesc_f16(kIsBf16, D, true);
+      for (int number = 0; ok && take(number); ++number) {
+        const int streams = streams_of(sh.ring[number % kRing]);
+        const int tiles = sh.ring[number % kRing].u1 - sh.ring[number % kRing].u0;
+        release(number);
+        // the scores of tile i of a stream
+        auto scores = [&](int stream, int i) -> bool {
+          if (i == 0) {   // the stream's rows of q
+            if (!warp_wait(&sh.q_full[stream], (q_phase >> stream) & 1u, sh, a.err,
+                           kErrTimeoutMma))
+              return false;
+            q_phase ^= 1u << stream;
+          }
+          if (stream == 0 && !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
             return false;
-          q_phase ^= 1u << stream;
-        }
-        if (stream == 0 &&
-            !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
-          return false;
-        tc_fence_after_sync();
-        const uint32_t d = uniform(tmem + (t & 1) * kTile);
-        const uint32_t qs = uniform(desc_k(q_at + stream * S::kQBytes));
-        const uint32_t ks = uniform(desc_k(k_at + k_stage * S::kTileBytes));
-        if (elect_one()) {
+          tc_fence_after_sync();
+          const int slot = stream + (S::kSlots == 2 ? i & 1 : 0);
+          const uint32_t d = uniform(tmem + slot * kTile);
+          const uint32_t qs = uniform(desc_k(q_at + stream * S::kQBytes));
+          const uint32_t ks = uniform(desc_k(k_at + k_stage * S::kTileBytes));
+          if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            mma_f16_ss(d, qs + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
-                       ks + ((i >> 2) * (kTile * 128) + (i & 3) * 32) / 16, kQk, i > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&sh.s_full[t & 1]));
-          if (stream == streams - 1) mma_commit(smem_u32(&sh.k_empty[k_stage]));
-        }
-        __syncwarp();
-        if (stream == streams - 1 && ++k_stage == S::kStages) {
-          k_stage = 0;
-          k_phase ^= 1u;
-        }
-        return true;
-      };
-      ok = scores(0);
-      if (ok && tasks > 1) ok = scores(1);
-      for (int t = 0; ok && t < tasks; ++t) {
-        const int stream = streams == 2 ? t & 1 : 0, slot = t & 1;
-        if (t < streams) {   // O: the last segment's has been read
-          ok = warp_wait(&sh.o_empty[stream], (oe_phase >> stream) & 1u, sh, a.err, kErrTimeoutMma);
-          if (!ok) break;
-          oe_phase ^= 1u << stream;
-        }
-        if (stream == 0) {
-          ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a.err, kErrTimeoutMma);
-          if (!ok) break;
-        }
-        ok = warp_wait(&sh.p_full[slot], (p_phase >> slot) & 1u, sh, a.err, kErrTimeoutMma);
-        if (!ok) break;
-        p_phase ^= 1u << slot;
-        tc_fence_after_sync();
-        const uint32_t d = uniform(tmem + S::kSOut + stream * D);
-        const uint32_t p = uniform(tmem + slot * kTile + S::kPOut);
-        const uint32_t vs = uniform(desc_mn(v_at + v_stage * S::kTileBytes, kTile * 128));
-        const uint32_t more = uniform(t >= streams ? 1u : 0u);
-        if (elect_one()) {
+            for (int j = 0; j < D / 16; ++j)
+              mma_f16_ss(d, qs + ((j >> 2) * (128 * 128) + (j & 3) * 32) / 16,
+                         ks + ((j >> 2) * (kTile * 128) + (j & 3) * 32) / 16, kQk, j > 0 ? 1u : 0u);
+            mma_commit(smem_u32(&sh.s_full[slot]));
+            if (stream == streams - 1) mma_commit(smem_u32(&sh.k_empty[k_stage]));
+          }
+          __syncwarp();
+          if (stream == streams - 1 && ++k_stage == S::kStages) {
+            k_stage = 0;
+            k_phase ^= 1u;
+          }
+          return true;
+        };
+        for (int i = 0; ok && i < min(tiles, S::kSlots); ++i)
+          for (int stream = 0; ok && stream < streams; ++stream) ok = scores(stream, i);
+        for (int i = 0; ok && i < tiles; ++i) {
+          for (int stream = 0; ok && stream < streams; ++stream) {
+            const int turn = S::kSlots == 2 ? i & 1 : 0, slot = stream + turn;
+            if (i == 0) {   // O: the last segment's has been read
+              ok = warp_wait(&sh.o_empty[stream], (oe_phase >> stream) & 1u, sh, a.err,
+                             kErrTimeoutMma);
+              if (!ok) break;
+              oe_phase ^= 1u << stream;
+            }
+            if (stream == 0) {
+              ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a.err, kErrTimeoutMma);
+              if (!ok) break;
+            }
+            ok = warp_wait(&sh.p_full[slot], (p_phase >> slot) & 1u, sh, a.err, kErrTimeoutMma);
+            if (!ok) break;
+            p_phase ^= 1u << slot;
+            tc_fence_after_sync();
+            const uint32_t d = uniform(tmem + S::kSOut + stream * D);
+            const uint32_t p = uniform(tmem + slot * kTile + S::kPOut);
+            const uint32_t vs = uniform(desc_mn(v_at + v_stage * S::kTileBytes, kTile * 128));
+            const uint32_t more = uniform(i > 0 ? 1u : 0u);
+            if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_f16_ts(d, p + 8 * i, vs + i * (2048 / 16), kPv, i > 0 ? 1u : more);
-          mma_commit(smem_u32(&sh.o_full[stream]));
-          if (stream == streams - 1) mma_commit(smem_u32(&sh.v_empty[v_stage]));
+              for (int j = 0; j < kTile / 16; ++j)
+                mma_f16_ts(d, p + 8 * j, vs + j * (2048 / 16), kPv, j > 0 ? 1u : more);
+              if (S::kSlots == 2 || i == tiles - 1) mma_commit(smem_u32(&sh.o_full[stream]));
+              if (stream == streams - 1) mma_commit(smem_u32(&sh.v_empty[v_stage]));
+            }
+            __syncwarp();
+            if (stream == streams - 1 && ++v_stage == S::kStages) {
+              v_stage = 0;
+              v_phase ^= 1u;
+            }
+            if (i + S::kSlots < tiles) ok = scores(stream, i + S::kSlots);
+          }
         }
-        __syncwarp();
-        if (stream == streams - 1 && ++v_stage == S::kStages) {
-          v_stage = 0;
-          v_phase ^= 1u;
-        }
-        if (t + 2 < tasks) ok = scores(t + 2);
       }
-    }
-    // every product has ended before tensor memory and shared memory are given back
-    if (lane == 0) mma_commit(smem_u32(&sh.drain));
-    __syncwarp();
-    volatile int no_abort = 0;
-    mbar_wait_bounded(smem_u32(&sh.drain), 0, &no_abort, a.err, kErrTimeoutDrain);
+      // every product has ended before tensor memory and shared memory are given back
+      if (elect_one()) mma_commit(smem_u32(&sh.drain));
+      __syncwarp();
+      volatile int no_abort = 0;
+      mbar_wait_bounded(smem_u32(&sh.drain), 0, &no_abort, a.err, kErrTimeoutDrain);
     } else if (warp == kPlanWarp) {
       // ---------------- the work, segment by segment ----------------
       Walk walk;
@@ -1146,7 +1143,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       bool more = true;
       for (int n = 0; more; ++n) {
         Segment s;
-        more = next_of<kRows, kTile>(a, sh, walk, s);
+        while ((more = next_of<kRows, kTile>(a, sh, walk, s)) && s.units == 0) {
+          // rows that see nothing (the others get segments with tiles only: the loading warps
+          // look some tiles ahead, and must find them within the ring)
+          for (int r = s.row0; r < s.row0 + s.rows; ++r) {
+            const int token = r / a.group, head = s.kv * a.group + r - token * a.group;
+            const int64_t to = (int64_t)(s.token0 + token);
+            if (lane < D / 8)
+              *reinterpret_cast<uint4*>(a.out + to * a.out_stride + (int64_t)head * D + 8 * lane) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            if (lane == 0 && a.lse != nullptr) a.lse[to * a.q_heads + head] = -INFINITY;
+          }
+        }
         if (!more) s.units = -1;
         if (!warp_wait(&sh.seg_empty[n % kRing], ((n / kRing) & 1) ^ 1, sh, a.err,
                        kErrTimeoutSched))
