@@ -57,7 +57,7 @@ constexpr int kMmaWarp = kLoadWarp0 + 2 * kLoadWarps;
 constexpr int kPlanWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 4);
 // Registers of a thread, by role (640 threads are launched with 96 each: 61440).
-constexpr int kSoftRegs = 128, kLoadRegs = 88, kMmaRegs = 48;
+constexpr int kSoftRegs = 136, kLoadRegs = 80, kMmaRegs = 48;
 static_assert(256 * kSoftRegs + 256 * kLoadRegs + 128 * kMmaRegs <= 96 * kThreads, "registers");
 constexpr int kRing = 16;                  // segments handed out at a time
 constexpr int kSides = 8;                  // tiles whose masks and factors are at hand
@@ -900,15 +900,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
                                                       (uint64_t)row * kRowBytes + 128 * i));
       return row;
     };
+    // the lane's pieces of the next tile to lay out, asked for as those before are laid out
     uint4 reg[kIsBf16 ? 1 : kLoads];
-    auto fetch = [&](uint32_t rows, uint4* to) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const uint32_t row = __shfl_sync(0xffffffffu, rows, i * kAtOnce + sub);
-        to[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row != kNoRow)
-          to[i] = *reinterpret_cast<const uint4*>(cache + (uint64_t)row * kRowBytes);
-      }
+    auto fetch = [&](uint32_t rows, int i) -> uint4 {
+      const uint32_t row = __shfl_sync(0xffffffffu, rows, i * kAtOnce + sub);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row != kNoRow) v = *reinterpret_cast<const uint4*>(cache + (uint64_t)row * kRowBytes);
+      return v;
     };
     // scales of the lane's token: the keys' loaders need both (they tell the softmax)
     float ks = 0.f, vs = 0.f;
@@ -928,7 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     uint32_t then = resolve();              // and of the next
     ask();
     if (running && !kIsBf16) {              // (bf16 rows go straight to the stages)
-      fetch(now, reg);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) reg[i] = fetch(now, i);
       ask_scales(now);
     }
     while (running) {
@@ -986,14 +985,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       }
 
       const uint32_t to = stages + stage * S::kTileBytes;
-      uint4 next[kIsBf16 ? 1 : kLoads];
       const uint32_t mine = now;
       running = follows;
       now = then;
-      if (running && !kIsBf16) {
-        fetch(now, next);
-        ask_scales(now);
-      }
+      if (!kIsBf16) ask_scales(now);
       follows = asked;
       then = resolve();
       ask();
@@ -1023,6 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           }
           st_shared_16(place(to, kTile, row, 2 * chunk), h[0], h[1], h[2], h[3]);
           st_shared_16(place(to, kTile, row, 2 * chunk + 1), h[4], h[5], h[6], h[7]);
+          reg[i] = fetch(now, i);
         }
       }
       if (kIsBf16) {
@@ -1031,10 +1027,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       }
       fence_proxy_async_smem();
       warp_arrive(&full[stage]);
-      if (!kIsBf16) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) reg[i] = next[i];
-      }
       ++tile;
       if (++stage == S::kStages) {
         stage = 0;
