@@ -248,12 +248,15 @@ class StepPlan:
     last), `refused` [1], the number of requests that wait for pages or rows, and
     `state`, the pool's after the step."""
 
-    __slots__ = ("offsets", "lengths", "slots", "positions", "state", "refused")
+    __slots__ = ("offsets", "slots", "positions", "state", "refused")
 
     def __init__(self, offsets, slots, positions, state, refused):
         self.offsets, self.slots, self.positions = offsets, slots, positions
         self.state, self.refused = state, refused
-        self.lengths = state[:-1]
+
+    @property
+    def lengths(self):
+        return self.state[:-1]
 
 
 class PagePool:

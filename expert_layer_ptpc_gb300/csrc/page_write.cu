@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t scaled_codes(uint32_t w, float by) {
 
 // TEAM: warps of a team.
 template <int PAIRS, int TEAM>
-__global__ void __launch_bounds__(32 * kWarps) page_write_kernel(const RotaryArgs a, int part) {
+__global__ void __launch_bounds__(32 * kWarps, PAIRS == kNoPairs ? 8 : 4) page_write_kernel(const RotaryArgs a, int part) {
   constexpr int kThreads = 32 * TEAM;
   // of each team: the slots of its part and of the token before it; its warps' findings
   __shared__ int32_t all_slots[kWarps / TEAM][kMostTokens + 1];
@@ -104,9 +104,17 @@ __global__ void __launch_bounds__(32 * kWarps) page_write_kernel(const RotaryArg
   const int run0 = from + 8 * (rotates ? u : u - rot_units), run1 = run0 + region / 2;
   const uint16_t* const src = (is_v ? a.v : a.k) + head * a.head_dim;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  auto load = [&](int t, float* x) {
-    unpack8(*reinterpret_cast<const uint4*>(src + t * stride + run0), x);
-    unpack8(*reinterpret_cast<const uint4*>(src + t * stride + run1), x + 8);
+  // a unit as it comes, and its elements (rotated)
+  struct Raw {
+    uint4 a, b;
+  };
+  auto ask = [&](int t) -> Raw {
+    return {*reinterpret_cast<const uint4*>(src + t * stride + run0),
+            *reinterpret_cast<const uint4*>(src + t * stride + run1)};
+  };
+  auto elements = [&](const Raw& raw, int t, float* x) {
+    unpack8(raw.a, x);
+    unpack8(raw.b, x + 8);
     if (PAIRS != kNoPairs && rotates) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -158,18 +166,26 @@ __global__ void __launch_bounds__(32 * kWarps) page_write_kernel(const RotaryArg
     float* const scale_at = (is_v ? a.v_scale : a.k_scale) + block;
     const float was = begun ? 0.f : *scale_at;
 
-    float x[kKept][kUnit], top = 0.f;
+    // (rotated units are kept as they are wanted, others as they come)
+    Raw raw[PAIRS == kNoPairs ? kKept : 1];
+    float x[PAIRS == kNoPairs ? 1 : kKept][kUnit], top = 0.f;
+    if (PAIRS == kNoPairs) {
+#pragma unroll
+      for (int k = 0; k < kKept; ++k)
+        if (first + k * step < n) raw[PAIRS == kNoPairs ? k : 0] = ask(t + first + k * step);
+    }
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
       const int j = first + k * step;
       if (j < n) {
-        load(t + j, x[k]);
-        top = fmaxf(top, largest(x[k]));
+        float* const y = x[PAIRS == kNoPairs ? 0 : k];
+        elements(PAIRS == kNoPairs ? raw[PAIRS == kNoPairs ? k : 0] : ask(t + j), t + j, y);
+        top = fmaxf(top, largest(y));
       }
     }
     for (int j = first + kKept * step; j < n; j += step) {
       float y[kUnit];
-      load(t + j, y);
+      elements(ask(t + j), t + j, y);
       top = fmaxf(top, largest(y));
     }
     top = warp_max(top);
@@ -202,11 +218,14 @@ __global__ void __launch_bounds__(32 * kWarps) page_write_kernel(const RotaryArg
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
       const int j = first + k * step;
-      if (j < n) store(t + j, x[k]);
+      if (j < n) {
+        if (PAIRS == kNoPairs) elements(raw[PAIRS == kNoPairs ? k : 0], t + j, x[0]);
+        store(t + j, x[PAIRS == kNoPairs ? 0 : k]);
+      }
     }
     for (int j = first + kKept * step; j < n; j += step) {
       float y[kUnit];
-      load(t + j, y);
+      elements(ask(t + j), t + j, y);
       store(t + j, y);
     }
     // (every lane has read the scale that was)

@@ -67,7 +67,7 @@ constexpr float kNewWeight = 7.0f;         // and of a tile's largest when M is 
 // What an item costs beside its tiles, in tiles of 128 tokens, and the least that a
 // CTA is given.
 constexpr int kItemCost = 4;
-constexpr int kLeastWork = 8;
+constexpr int kLeastWork = 4;
 
 constexpr int kLeastExponent = -64;        // scales below 2^-64 count as that (sums end at 2^128)
 
@@ -158,6 +158,7 @@ struct Shared {
   int maxima[2][2][kLoadWarps][2];   // of keys' loaders and values'
   int2 request[kRequests + 1];       // (first row, length)
   int64_t sums[kThreads / 32 + 1];
+  int first;                         // the context of request[0]
   int place[2][4];                   // the run: first context, kv head, item, unit; and its end
   Segment ring[kRing];               // handed out and not yet done with; units < 0: no more
 };
@@ -346,7 +347,7 @@ __device__ __forceinline__ Segment segment_of(const Args& a, const Context& c, i
 // Hands out a CTA's run of the work to a warp, segment by segment.
 template <int ROWS, int TILE>
 __device__ __forceinline__ bool next_of(const Args& a, const Shared& sh, Walk& w, Segment& s) {
-  const int first = sh.place[0][0];
+  const int first = sh.first;
   for (;;) {
     const bool last = w.b == w.end[0] && w.kv == w.end[1] && w.item == w.end[2];
     if (w.b >= a.batch || (last && w.unit >= w.end[3])) return false;
@@ -448,10 +449,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   // ---- this CTA's run of the work ----
   const int worker = blockIdx.x;
   {
+    // (contexts that fit are read once, the others where they are wanted)
+    const bool few = a.batch <= kRequests;
+    if (few) {
+      for (int i = threadIdx.x; i <= a.batch; i += kThreads)
+        sh.request[i] = make_int2(a.offsets[i], i < a.batch ? a.lengths[i] : 0);
+      __syncthreads();
+    }
+    auto context = [&](int b) -> Context {
+      if (few) return context_of<kRows>(a, sh.request[b], sh.request[b + 1].x);
+      return context_of<kRows>(a, make_int2(a.offsets[b], a.lengths[b]), a.offsets[b + 1]);
+    };
     auto total_of = [&](int b) -> int64_t {
       if (b >= a.batch) return 0;
-      const Context c = context_of<kRows>(a, make_int2(a.offsets[b], a.lengths[b]),
-                                          a.offsets[b + 1]);
+      const Context c = context(b);
       return c.items == 0 ? 0 : weights_of<S::kStreams>(a, c).before(c.items) * a.c.heads;
     };
     // sum over the threads before this one, and over all
@@ -499,8 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           if (past < 0 || past >= mine) continue;
           // place `past` of context b
           const int b = b0 + threadIdx.x;
-          const Context c = context_of<kRows>(a, make_int2(a.offsets[b], a.lengths[b]),
-                                              a.offsets[b + 1]);
+          const Context c = context(b);
           const Weights w = weights_of<S::kStreams>(a, c);
           const int64_t each = w.before(c.items);
           const int kv = (int)(past / each);
@@ -523,15 +533,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  for (int i = threadIdx.x; i <= kRequests; i += kThreads) {
-    const int b = sh.place[0][0] + i;
-    if (b <= a.batch)
-      sh.request[i] = make_int2(a.offsets[b], b < a.batch ? a.lengths[b] : 0);
+  if (a.batch > kRequests) {
+    for (int i = threadIdx.x; i <= kRequests; i += kThreads) {
+      const int b = sh.place[0][0] + i;
+      if (b <= a.batch)
+        sh.request[i] = make_int2(a.offsets[b], b < a.batch ? a.lengths[b] : 0);
+    }
   }
   if (threadIdx.x == 0) {
     a.records[worker].head.x = -1;
     a.records[worker].tail.x = -1;
     a.records[worker].some = 0;
+    sh.first = a.batch > kRequests ? sh.place[0][0] : 0;
   }
   __syncthreads();
   const uint32_t tmem = sh.tmem;
@@ -1131,7 +1144,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       walk.unit = sh.place[0][3];
 #pragma unroll
       for (int i = 0; i < 4; ++i) walk.end[i] = sh.place[1][i];
-      if (walk.b < a.batch) walk.c = context_of<kRows>(a, sh.request[0], sh.request[1].x);
+      if (walk.b < a.batch)
+        walk.c = context_of<kRows>(a, sh.request[walk.b - sh.first],
+                                   sh.request[walk.b - sh.first + 1].x);
       bool more = true;
       for (int n = 0; more; ++n) {
         Segment s;
@@ -1178,48 +1193,84 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
   // between them can have got nothing)
   __shared__ int slots[kWorkers];
   __shared__ int count;
-  if (threadIdx.x == 0) {
-    int n = 0;
-    slots[n++] = 2 * w + 1;
-    for (int i = w + 1; i < workers; ++i) {
-      const int4 h = a.records[i].head;
-      if (h.x == rec.tail.x && h.y == rec.tail.y && h.z == rec.tail.z) slots[n++] = 2 * i;
-      else if (a.records[i].some != 0) break;
+  __shared__ float weight[kWorkers][32];   // of a piece's row, over the joined sum
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int n = 1;
+    bool more = true;
+    if (lane == 0) slots[0] = 2 * w + 1;
+    for (int i0 = w + 1; more && i0 < workers; i0 += 32) {
+      int4 h = make_int4(-1, 0, 0, 0);
+      int some = 1;
+      if (i0 + lane < workers) {
+        h = a.records[i0 + lane].head;
+        some = a.records[i0 + lane].some;
+      }
+      const bool piece = h.x == rec.tail.x && h.y == rec.tail.y && h.z == rec.tail.z;
+      // those up to the first CTA that did something else
+      const unsigned other = __ballot_sync(0xffffffffu, !piece && some != 0);
+      const unsigned upto = other ? (1u << (__ffs(other) - 1)) - 1u : 0xffffffffu;
+      const unsigned pieces = __ballot_sync(0xffffffffu, piece) & upto;
+      if ((pieces >> lane) & 1u) slots[n + __popc(pieces & lanemask_lt())] = 2 * (i0 + lane);
+      n += __popc(pieces);
+      more = other == 0;
     }
-    count = n;
+    if (lane == 0) count = n;
   }
   __syncthreads();
   const int row = blockIdx.y * 32 + (threadIdx.x & 31);
-  if (row >= rec.rows) return;
-  float top = -INFINITY;
-  for (int i = 0; i < count; ++i) top = fmaxf(top, a.stats[slots[i] * kRows + row].x);
-  float sum = 0.f;
-  for (int i = 0; i < count; ++i) {
-    const float2 s = a.stats[slots[i] * kRows + row];
-    if (s.x != -INFINITY) sum = fmaf(s.y, exp2_approx(s.x - top), sum);
+  if (threadIdx.x < 32) {
+    float top = -INFINITY, sum = 0.f;
+    for (int i = 0; i < count; ++i) {
+      const float2 s = a.stats[slots[i] * kRows + row];
+      weight[i][threadIdx.x] = s.x;
+      const float next = fmaxf(top, s.x);
+      if (next != -INFINITY)
+        sum = sum * (top == -INFINITY ? 0.f : exp2_approx(top - next)) +
+              (s.x == -INFINITY ? 0.f : s.y * exp2_approx(s.x - next));
+      top = next;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    for (int i = 0; i < count; ++i) {
+      const float m = weight[i][threadIdx.x];
+      weight[i][threadIdx.x] = m == -INFINITY ? 0.f : exp2_approx(m - top) * inv;
+    }
+    if (row < rec.rows && a.lse != nullptr) {
+      const int r = rec.row0 + row, token = r / a.group;
+      const int head = rec.tail.y * a.group + (r - token * a.group);
+      a.lse[(int64_t)(rec.token0 + token) * a.q_heads + head] =
+          sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  __syncthreads();
+  if (row >= rec.rows) return;
   const int r = rec.row0 + row, token = r / a.group;
   const int head = rec.tail.y * a.group + (r - token * a.group);
-  const int64_t to = rec.token0 + token;
-  for (int d = threadIdx.x >> 5; d < D / 4; d += kJoinThreads / 32) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < count; ++i) {
-      const int64_t slot = slots[i];
-      const float m = a.stats[slot * kRows + row].x;
-      const float by = m == -INFINITY ? 0.f : exp2_approx(m - top);
-      const float4 v = reinterpret_cast<const float4*>(a.parts)[(slot * (D / 4) + d) * kRows + row];
-      o.x = fmaf(v.x, by, o.x);
-      o.y = fmaf(v.y, by, o.y);
-      o.z = fmaf(v.z, by, o.z);
-      o.w = fmaf(v.w, by, o.w);
+  uint16_t* const out = a.out + (int64_t)(rec.token0 + token) * a.out_stride + (int64_t)head * D;
+  const float4* const parts = reinterpret_cast<const float4*>(a.parts);
+  constexpr int kSteps = D / 4 / (kJoinThreads / 32);   // of a thread
+  float4 o[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < count; ++i) {
+    const float by = weight[i][threadIdx.x & 31];
+    const int64_t slot = slots[i];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int d = (threadIdx.x >> 5) + k * (kJoinThreads / 32);
+      const float4 v = parts[(slot * (D / 4) + d) * kRows + row];
+      o[k].x = fmaf(v.x, by, o[k].x);
+      o[k].y = fmaf(v.y, by, o[k].y);
+      o[k].z = fmaf(v.z, by, o[k].z);
+      o[k].w = fmaf(v.w, by, o[k].w);
     }
-    *reinterpret_cast<uint2*>(a.out + to * a.out_stride + (int64_t)head * D + 4 * d) =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   }
-  if (threadIdx.x < 32 && a.lse != nullptr)
-    a.lse[to * a.q_heads + head] =
-        sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int d = (threadIdx.x >> 5) + k * (kJoinThreads / 32);
+    *reinterpret_cast<uint2*>(out + 4 * d) =
+        make_uint2(pack_bf16(o[k].x, o[k].y), pack_bf16(o[k].z, o[k].w));
+  }
 }
 
 template <int KIND, int D>
