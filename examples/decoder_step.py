@@ -1,18 +1,20 @@
 """One decoder layer served step by step: attention over a paged key-value cache,
 then the MoE block.
 
-    python examples/decoder_step.py [--steps N] [--cache bf16]
+    python examples/decoder_step.py [--steps N] [--cache e4m3_page|bf16]
 
-A batch of requests has its prompts written to the cache in one call, and then
-takes one token a step:
+A batch of requests has its prompts written to the cache and attended to in one
+call each, and then takes one token a step:
 
-    qkv = x Wqkv                              (library matrix product)
-    q   = cache.write_rotary(q, k, v)         rotation, quantised cache write
-    o   = cache.attend(q)                     paged attention, one token a request
-    x   = MoELayer.forward(o Wo, residual=x)  add + RMSNorm, routing, experts
+    plan = pool.plan(new tokens)              pages, slots and positions, on the GPU
+    qkv  = x Wqkv                             (library matrix product)
+    q    = cache.write_rotary(q, k, v)        rotation, quantised cache write
+    o    = cache.attend(q)                    paged attention, one token a request
+           (a prompt: cache.attend_prompt(q))
+    x    = MoELayer.forward(o Wo, residual=x) add + RMSNorm, routing, experts
 
-Weights and inputs are random; every step's attention is compared with a dense
-evaluation over the keys and values read back from the cache.
+Weights and inputs are random; every step's attention, the prompts' too, is compared
+with a dense evaluation over the keys and values read back from the cache.
 """
 
 import argparse
@@ -25,8 +27,8 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import torch  # noqa: E402
 
 from expert_layer_ptpc_gb300 import synthetic as syn  # noqa: E402
-from expert_layer_ptpc_gb300.attention import (PagedKVCache, Rotary, frequencies,  # noqa: E402
-                                               pair_axes)
+from expert_layer_ptpc_gb300.attention import (PagedKVCache, PagePool, Rotary,  # noqa: E402
+                                               frequencies, pair_axes)
 from expert_layer_ptpc_gb300.layer import MoELayer  # noqa: E402
 
 
@@ -58,10 +60,11 @@ class DecoderLayer:
         qkv = (x @ self.w_qkv).unflatten(1, (-1, self.head_dim))
         return qkv.split([self.q_heads, self.kv_heads, self.kv_heads], 1)
 
-    def prompt(self, x, positions, slots):
-        """Write the keys and values of prompt tokens x [T, D] to the cache;
-        returns their rotated q."""
-        return self.cache.write_rotary(self.rotary, positions, *self.heads(x), slots)
+    def prompt(self, x, plan, table):
+        """Attention of prompt tokens x [T, D], whose keys and values go to the cache
+        first. Returns (the attention's output, the rotated q)."""
+        q = self.cache.write_rotary(self.rotary, plan.positions, *self.heads(x), plan.slots)
+        return self.cache.attend_prompt(q, plan.offsets, table, plan.lengths), q
 
     def step(self, x, positions, slots, table, lengths):
         """One new token a request, x [batch, D]. Returns (the layer's output,
@@ -77,20 +80,24 @@ class DecoderLayer:
         return out, residual, o, q
 
 
-def dense_attention(layer, q, table, lengths):
-    """Attention over the contexts read back from the cache, in fp64."""
+def dense_attention(layer, q, table, lengths, rows):
+    """Attention over the contexts read back from the cache, in fp64: the last rows[b]
+    tokens of each."""
     offsets = torch.zeros(len(lengths) + 1, dtype=torch.int32, device="cuda")
     offsets[1:] = torch.cumsum(lengths, 0)
     ends = offsets.tolist()
     k, v = layer.cache.read(table, offsets, ends[-1])
     group = layer.q_heads // layer.kv_heads
-    outs = []
-    for b, (s, e) in enumerate(zip(ends, ends[1:])):
+    outs, at = [], 0
+    for s, e, n in zip(ends, ends[1:], rows):
         kb = k[s:e].double().repeat_interleave(group, 1)
         vb = v[s:e].double().repeat_interleave(group, 1)
-        scores = torch.einsum("hd,nhd->hn", q[b].double(), kb) / math.sqrt(layer.head_dim)
-        outs.append(torch.einsum("hn,nhd->hd", torch.softmax(scores, -1), vb))
-    return torch.stack(outs)
+        scores = torch.einsum("rhd,nhd->hrn", q[at:at + n].double(), kb)
+        future = torch.ones((n, e - s), dtype=torch.bool, device="cuda").triu(e - s - n + 1)
+        scores = (scores / math.sqrt(layer.head_dim)).masked_fill(future, float("-inf"))
+        outs.append(torch.einsum("hrn,nhd->rhd", torch.softmax(scores, -1), vb))
+        at += n
+    return torch.cat(outs)
 
 
 def main(argv=None):
@@ -99,40 +106,35 @@ def main(argv=None):
     ap.add_argument("--steps", type=int, default=4)
     ap.add_argument("--batch", type=int, default=8)
     ap.add_argument("--prompt", type=int, default=200, help="longest prompt")
-    ap.add_argument("--cache", choices=("e4m3", "bf16"), default="e4m3")
+    ap.add_argument("--cache", choices=("e4m3", "e4m3_page", "bf16"), default="e4m3")
     a = ap.parse_args(argv)
     page = 16
     cfg = syn.LayerConfig("decoder", a.batch, 1024, 16, 4, 256, False, "normal")
     each = -(-(a.prompt + a.steps) // page)                # pages of a request
-    layer = DecoderLayer(cfg, 16, 2, 128, a.batch * each + 1, page, a.cache)
+    layer = DecoderLayer(cfg, 16, 2, 128, a.batch * each, page, a.cache)
+    pool = PagePool.empty(a.batch * each, page, a.batch, each)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
-    table = (torch.randperm(a.batch * each, generator=g, device="cuda") + 1).to(torch.int32)
-    table = table.view(a.batch, each)                      # page 0 is nobody's
 
-    def slots_of(b, token):
-        return table[b, token // page] * page + token % page
+    def differs(o, want):
+        return float((o.double() - want).norm() / want.norm())
 
-    # prompts of several lengths, in one call
-    lengths = torch.tensor([1 + (a.prompt - 1) * i // max(1, a.batch - 1) for i in range(a.batch)],
-                           device="cuda")
-    b = torch.repeat_interleave(torch.arange(a.batch, device="cuda"), lengths)
-    token = torch.cat([torch.arange(n, device="cuda") for n in lengths.tolist()])
-    x = torch.randn((len(b), cfg.D), generator=g, device="cuda").to(torch.bfloat16)
-    positions = token.to(torch.int32).repeat(3, 1)         # text: the axes agree
-    layer.prompt(x, positions, slots_of(b, token).to(torch.int32))
+    # prompts of several lengths, in one call (text: the three axes of positions agree)
+    news = [1 + (a.prompt - 1) * i // max(1, a.batch - 1) for i in range(a.batch)]
+    x = torch.randn((sum(news), cfg.D), generator=g, device="cuda").to(torch.bfloat16)
+    plan = pool.plan(torch.tensor(news, dtype=torch.int32, device="cuda"), sum(news), axes=3)
+    o, q = layer.prompt(x, plan, pool.table)
+    pool.commit(plan)
+    worst = differs(o, dense_attention(layer, q, pool.table, plan.lengths, news))
 
     x = torch.randn((a.batch, cfg.D), generator=g, device="cuda").to(torch.bfloat16)
-    every = torch.arange(a.batch, device="cuda")
-    worst = 0.0
+    one = torch.ones(a.batch, dtype=torch.int32, device="cuda")
     for step in range(a.steps):
-        positions = lengths.to(torch.int32).repeat(3, 1)
-        slots = slots_of(every, lengths).to(torch.int32)
-        lengths = lengths + 1
-        n = lengths.to(torch.int32)
-        out, residual, o, q = layer.step(x, positions, slots, table, n)
-        want = dense_attention(layer, q, table, n)
-        worst = max(worst, float((o.double() - want).norm() / want.norm()))
+        plan = pool.plan(one, a.batch, axes=3)
+        out, residual, o, q = layer.step(x, plan.positions, plan.slots, pool.table, plan.lengths)
+        pool.commit(plan)
+        want = dense_attention(layer, q, pool.table, plan.lengths, [1] * a.batch)
+        worst = max(worst, differs(o, want))
         assert layer.moe.status() == (0, 0)
         x = (out.float() + residual.float()).to(torch.bfloat16)
     assert bool(torch.isfinite(x.float()).all())

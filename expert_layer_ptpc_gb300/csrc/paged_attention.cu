@@ -46,6 +46,9 @@
 // a bf16 cache the operands are bf16, and the weights go in as the sum of two
 // bf16 numbers (16 bits).
 //
+// A cache with one scale a page and head goes the same way: a token's scale is then read from
+// its page's (128 contexts as below 174 us, 6.2 TB/s, for 8 bytes a token less).
+//
 // GB300: 128 contexts of 0 to 16384 tokens, 64 query heads on 4 of 128, e4m3 (1.11 GB):
 // 183 us, 6.1 TB/s of the copy's 6.8; one context of 262143 tokens (277 MB): 54 us, of
 // which 40 are the tiles at the copy's rate and the rest the first loads, the last CTA

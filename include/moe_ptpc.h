@@ -820,6 +820,16 @@ MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int bat
  *   keys and values from the first token on that any of its rows sees must be finite.
  *   ws: device workspace of moe_prompt_attention_workspace_size bytes, as for
  *   moe_paged_attention.
+ *   Sums, maxima and accumulators are fp32; results do not depend on timing. What the
+ *   tensor cores multiply has fewer bits:
+ *   - e4m3 caches: codes in fp16, exactly; a page's scale as a power of two (a code
+ *     times a scale 2^-31 of the largest of its 128 tokens, 64 with head_dim 256, counts as 0), a
+ *     token's scale of a value rounded into it (2^-11). q in fp16, its head's largest
+ *     element scaled into [2^8, 2^9): off by up to 2^-33 of that element. Weights in fp16:
+ *     off by up to 2^-11 of each, or 2^-32 of the row's largest where that is more. Scales
+ *     below 2^-64 count as that.
+ *   - bf16 cache: q, k and v exactly; weights in bf16, off by up to 2^-8 of each.
+ *   Every wait inside is bounded; one that runs out is reported by moe_device_status().
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned pointers, q_heads
  *         not a multiple of heads, bad strides, scale not finite, rows or batch < 0,
  *         max_pages < 0, table_stride < max_pages, window < 0), MOE_ERR_UNSUPPORTED (batch

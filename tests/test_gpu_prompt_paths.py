@@ -252,3 +252,18 @@ def test_tensors_elsewhere_refused():
                 dict(new_tokens=ints([1, 1]).cpu()), dict(rows=-1), dict(axes=0), dict(axes=9)):
         with pytest.raises(ValueError):
             pool.plan(**{**dict(new_tokens=ints([1, 1]), rows=4), **bad})
+
+
+def test_decoder_example_with_page_scales():
+    import importlib.util
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location(
+        "decoder_step", os.path.join(root, "examples", "decoder_step.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    # both sides round to bf16 (half a step is 2^-8 of the value); the contexts
+    # read back are rounded to bf16 too
+    worst = example.main(["--steps", "3", "--batch", "6", "--prompt", "333", "--cache",
+                          "e4m3_page"])
+    assert worst <= 2 * 2.0 ** -8
