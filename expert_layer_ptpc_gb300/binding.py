@@ -947,6 +947,8 @@ def moe_prompt_attention(cache, q, offsets, block_table, lengths, scale, window=
         out_stride = _need_heads(out, hq, d, "out", index)
         if out.shape[0] != rows:
             raise ValueError(f"out must have {rows} tokens, got {out.shape[0]}")
+        if out.data_ptr() == q.data_ptr() and rows:
+            raise ValueError("out must not overlap q")
     if lse is not None:
         _need_on(lse, torch.float32, "lse", index)
         if tuple(lse.shape) != (rows, hq):

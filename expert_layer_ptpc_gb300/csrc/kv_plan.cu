@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
       a.table[b * a.table_stride + have + i] = page_at(first[b] + i);
   }
   // the tokens: the last request that starts at or before one
-  for (int t = blockIdx.x * kThreads + threadIdx.x; t < a.rows; t += gridDim.x * kThreads) {
+  for (int64_t t = blockIdx.x * kThreads + threadIdx.x; t < a.rows; t += gridDim.x * kThreads) {
     int32_t slot = -1;
     int at = 0;
     if (t < total) {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
         const int mid = (lo + hi) >> 1;
         if (start[mid] <= t) lo = mid; else hi = mid;
       }
-      at = held[lo] + (t - start[lo]);
+      at = held[lo] + (int)(t - start[lo]);
       const int64_t have = pages_of(held[lo]), i = at >> a.page_shift;
       const int32_t p = i < have ? a.table[lo * a.table_stride + i] : page_at(first[lo] + i - have);
       slot = valid(p) ? (p << a.page_shift) + (at & (page - 1)) : -1;
@@ -195,7 +195,7 @@ int launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
       cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
           cudaSuccess)
     return -3;
-  const int ctas = std::min(kMaxCtas, std::max(1, (a.rows + kTokens - 1) / kTokens));
+  const int ctas = std::min(kMaxCtas, a.rows / kTokens + 1);
   const cudaError_t e = launch_kernel(true, dim3(ctas), dim3(kThreads), smem, stream,
                                       kv_plan_kernel, a);
   return e == cudaSuccess ? 0 : -3;

@@ -345,7 +345,8 @@ __device__ __forceinline__ Segment segment_of(const Args& a, const Context& c, i
   s.place = c.place;
   s.row0 = item * ROWS;
   s.rows = min(ROWS, c.rows - s.row0);
-  const int64_t room = min((int64_t)a.c.max_pages << a.c.page_shift, (int64_t)INT_MAX);
+  // (a tile behind the last token stays within an int)
+  const int64_t room = min((int64_t)a.c.max_pages << a.c.page_shift, (int64_t)INT_MAX - 255);
   const int first = s.row0 / a.group, last = (s.row0 + s.rows - 1) / a.group;
   s.end = (int)max(min((int64_t)c.place + last + 1, room), (int64_t)0);
   s.begin = a.window > 0 ? (int)max((int64_t)c.place + first + 1 - a.window, (int64_t)0) : 0;
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           const Context c = context(b);
           const Weights w = weights_of<S::kStreams>(a, c);
           const int64_t each = w.before(c.items);
-          const int kv = (int)(past / each);
+          const int kv = (int)min(past / each, (int64_t)a.c.heads - 1);
           const int64_t in = past - kv * each;
           int lo = 0, hi = c.items;     // before(lo) <= in < before(hi)
           while (hi - lo > 1) {
@@ -1324,6 +1325,13 @@ int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_str
                             int q_heads, const int32_t* offsets, const int32_t* lengths, int batch,
                             float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
                             void* ws, cudaStream_t stream) {
+  const int group = q_heads / c.heads;
+  // the weights' sum over all items, times the CTAs, stays within 64 bits (contexts that
+  // overlap, which the contract rules out, could add up to 2^16 times as much)
+  const double items = (double)rows * q_heads / 128 + (double)batch * c.heads;
+  const double room = std::min<double>((double)c.max_pages * (1 << c.page_shift), 0x1p31);
+  if (items * (room * group / 128 + (double)rows * group / 128 + 8.0 * group) > 0x1p46)
+    return -2;
   Args a{};
   a.c = c;
   a.q = q;
@@ -1332,7 +1340,7 @@ int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_str
   a.rows = rows;
   a.q_heads = q_heads;
   a.batch = batch;
-  a.group = q_heads / c.heads;
+  a.group = group;
   a.offsets = offsets;
   a.lengths = lengths;
   a.scale = scale;

@@ -814,8 +814,9 @@ MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int bat
  *   q [rows, q_heads, head_dim] bf16 with q_stride elements between tokens; offsets
  *   [batch + 1] int32, ascending from 0, to at most `rows`; block_table and lengths as
  *   for moe_paged_attention (the new tokens' keys and values are in the cache already
- *   and counted); out like q with out_stride; lse [rows, q_heads] fp32 or NULL. Rows
- *   from offsets[batch] on are left as they are.
+ *   and counted; tokens from 2^31 - 256 on are absent); out like q with out_stride, not
+ *   overlapping q; lse [rows, q_heads] fp32 or NULL. Rows from offsets[batch] on are
+ *   left as they are.
  *   Slots that no context covers have no influence, whatever they hold; a context's
  *   keys and values from the first token on that any of its rows sees must be finite.
  *   ws: device workspace of moe_prompt_attention_workspace_size bytes, as for
@@ -833,8 +834,9 @@ MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int bat
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned pointers, q_heads
  *         not a multiple of heads, bad strides, scale not finite, rows or batch < 0,
  *         max_pages < 0, table_stride < max_pages, window < 0), MOE_ERR_UNSUPPORTED (batch
- *         or q_heads > 65535, rows * q_heads >= 2^31), MOE_ERR_WORKSPACE. rows or batch
- *         == 0 is a no-op.
+ *         or q_heads > 65535, rows * q_heads >= 2^31, or 2^46 or more tiles of 128 tokens
+ *         and 128 rows, times the heads of a kv head, that the rows and the tables' room
+ *         make), MOE_ERR_WORKSPACE. rows or batch == 0 is a no-op.
  */
 MOE_API size_t moe_prompt_attention_workspace_size(const moe_kv_cache* cache, int q_heads);
 MOE_API int moe_prompt_attention(const moe_kv_cache* cache, const uint16_t* q,

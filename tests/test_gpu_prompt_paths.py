@@ -241,7 +241,7 @@ def test_tensors_elsewhere_refused():
     for bad in (dict(q=q.float()), dict(q=q[:, :5]), dict(q=q.cpu()), dict(offsets=o.long()),
                 dict(offsets=o.cpu()), dict(offsets=ints([0, 1, 2])), dict(block_table=t.cpu()),
                 dict(block_table=t.t()), dict(lengths=n.float()), dict(window=2 ** 31),
-                dict(out=q[:5]), dict(out=q.float()), dict(lse=torch.zeros(70, 6)),
+                dict(out=q[:5]), dict(out=q.float()), dict(out=q), dict(lse=torch.zeros(70, 6)),
                 dict(lse=torch.zeros((70, 5), device="cuda"))):
         with pytest.raises((ValueError, binding.MoeError)):
             cache.attend_prompt(**{**good, **bad})

@@ -52,6 +52,8 @@ def prompt(lib, c=None, q=A, qs=1024, rows=4, hq=8, offsets=A, table=A, stride=4
     (dict(ws=None), WORKSPACE), (dict(ws=MIS), WORKSPACE), (dict(ws_bytes=0), WORKSPACE),
     (dict(batch=65536), UNSUPPORTED), (dict(hq=65536, qs=65536 * 128), UNSUPPORTED),
     (dict(rows=1 << 28), UNSUPPORTED),
+    # (a table's room of 2^31 tokens, 2^24 rows of 8 heads on 2)
+    (dict(rows=1 << 24, c=cache(page_size=1024), wide=1 << 21, stride=1 << 21), UNSUPPORTED),
 ])
 def test_prompt_refusals(lib, kw, want):  # noqa: F811
     assert prompt(lib, **kw) == want
