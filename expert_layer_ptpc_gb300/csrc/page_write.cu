@@ -18,10 +18,11 @@
 // code, so the first 4 units of a thread stay in registers between, and the rest are read
 // twice: one warp for pages of up to 16 tokens of 128 elements, four for larger ones. Bound by
 // memory without a rotation: 2 bytes an element in, 1 out; GB300, 12100 tokens of 8 heads of
-// 128 in pages of 16: 21 us, 3.5 TB/s of the copy's 6.8 (with fp32 elements kept instead of what was
-// read, 16 warps an SM and 42 us). Behind a rotation by the angles, which every head
-// works out anew: 6146 tokens of 4 heads 27 us. q is rotated by a launch of its own (28 us of
-// its own with 64 heads), which runs beside this one's last blocks: 53 us together.
+// 128 in pages of 16: 21 us, 3.5 TB/s of the copy's 6.8 (with fp32 elements kept instead of what
+// was read, 16 warps an SM and 42 us). Behind a rotation by the angles: a block works a run's
+// out once for up to four of k's heads. q is rotated by a launch of its own (28 us with 64
+// heads and 6146 tokens), which runs beside this one's last blocks: 49 us together with 4
+// heads of k and v (53 with the angles worked out for each head).
 #include <algorithm>
 
 #include "attention.h"
@@ -38,6 +39,8 @@ namespace {
 constexpr int kWarps = 4;       // of a block
 constexpr int kKept = 4;        // units of a thread in registers
 constexpr int kMostTokens = 64; // of a team's part
+constexpr int kMostHeads = 4;   // of k that a team does one after the other
+constexpr int kTurns = 4096;    // (cos, sin) of a block
 constexpr float kLeastScale = 0x1p-48f;
 
 // 2^e, e the least integer >= -48 with amax <= 448 * 2^e (448 = 1.75 * 2^8).
@@ -71,12 +74,15 @@ __device__ __forceinline__ uint32_t scaled_codes(uint32_t w, float by) {
 
 // TEAM: warps of a team.
 template <int PAIRS, int TEAM>
-__global__ void __launch_bounds__(32 * kWarps, PAIRS == kNoPairs ? 8 : 4) page_write_kernel(const RotaryArgs a, int part) {
-  constexpr int kThreads = 32 * TEAM;
+__global__ void __launch_bounds__(32 * kWarps, PAIRS == kNoPairs ? 8 : 4)
+    page_write_kernel(const RotaryArgs a, int part, int at_once) {
+  constexpr int kThreads = 32 * TEAM, kMine = kTurns / (kWarps / TEAM);
+  // (cos, sin) of a run's tokens, for all of the team's heads
+  __shared__ __align__(16) float2 all_turns[PAIRS == kNoPairs ? 1 : kTurns];
   // of each team: the slots of its part and of the token before it; its warps' findings
   __shared__ int32_t all_slots[kWarps / TEAM][kMostTokens + 1];
   __shared__ int ends[TEAM], begins[TEAM];
-  __shared__ float maxima[TEAM];
+  __shared__ float maxima[2][TEAM];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, team = threadIdx.x / kThreads, me = threadIdx.x % kThreads;
@@ -84,8 +90,13 @@ __global__ void __launch_bounds__(32 * kWarps, PAIRS == kNoPairs ? 8 : 4) page_w
   const int64_t t_begin = ((int64_t)blockIdx.x * (kWarps / TEAM) + team) * part;
   if (TEAM == 1 && t_begin >= a.T) return;
   const int t0 = (int)t_begin, here = min(part, a.T - t0);
-  const bool is_v = (blockIdx.y & 1) != 0;
-  const int head = blockIdx.y >> 1;
+  // k's heads in groups, then v's
+  const int groups = PAIRS == kNoPairs ? a.k_heads : (a.k_heads + at_once - 1) / at_once;
+  const bool is_v = (int)blockIdx.y >= groups;
+  const int head0 = is_v ? (int)blockIdx.y - groups
+                         : (int)blockIdx.y * (PAIRS == kNoPairs ? 1 : at_once);
+  const int head1 = PAIRS == kNoPairs || is_v ? head0 + 1 : min(a.k_heads, head0 + at_once);
+  float2* const turns = all_turns + (PAIRS == kNoPairs ? 0 : team * kMine);
   const int size = 1 << a.page_shift;
   int32_t* const slots = all_slots[team];
   auto sync = [&]() {
@@ -105,24 +116,26 @@ __global__ void __launch_bounds__(32 * kWarps, PAIRS == kNoPairs ? 8 : 4) page_w
   const int from = rotates || rot_units == 0 ? 0 : a.rot;
   const int region = rot_units == 0 ? a.head_dim : rotates ? a.rot : a.head_dim - a.rot;
   const int run0 = from + 8 * (rotates ? u : u - rot_units), run1 = run0 + region / 2;
-  const uint16_t* const src = (is_v ? a.v : a.k) + head * a.head_dim;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   // a unit as it comes, and its elements (rotated)
   struct Raw {
     uint4 a, b;
   };
+  const uint16_t* src = (is_v ? a.v : a.k) + head0 * a.head_dim;   // of the head
   auto ask = [&](int t) -> Raw {
     return {*reinterpret_cast<const uint4*>(src + t * stride + run0),
             *reinterpret_cast<const uint4*>(src + t * stride + run1)};
   };
-  auto elements = [&](const Raw& raw, int t, float* x) {
+  const int pairs = a.rot / 2, room = PAIRS == kNoPairs ? 0 : kMine / pairs;   // tokens
+  auto elements = [&](const Raw& raw, int t, int in_run, float* x) {
     unpack8(raw.a, x);
     unpack8(raw.b, x + 8);
     if (PAIRS != kNoPairs && rotates) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int p = pair_of<PAIRS>(u, j, a.rot);
-        const float2 cs = turn_of(a, t, a.turns[p], a.pair_axis[p]);
+        const float2 cs = in_run < room ? turns[in_run * pairs + p]
+                                        : turn_of(a, t, a.turns[p], a.pair_axis[p]);
         turn_pair(cs, PAIRS == kNeighbours ? x[2 * j] : x[j],
                   PAIRS == kNeighbours ? x[2 * j + 1] : x[8 + j]);
       }
@@ -165,75 +178,87 @@ __global__ void __launch_bounds__(32 * kWarps, PAIRS == kNoPairs ? 8 : 4) page_w
     }
     const int n = end;
     const bool begun = zero < n;
-    const int64_t block = (int64_t)page * a.k_heads + head;
-    float* const scale_at = (is_v ? a.v_scale : a.k_scale) + block;
-    const float was = begun ? 0.f : *scale_at;
-
-    // (rotated units are kept as they are wanted, others as they come)
-    Raw raw[PAIRS == kNoPairs ? kKept : 1];
-    float x[PAIRS == kNoPairs ? 1 : kKept][kUnit], top = 0.f;
-    if (PAIRS == kNoPairs) {
-#pragma unroll
-      for (int k = 0; k < kKept; ++k)
-        if (first + k * step < n) raw[PAIRS == kNoPairs ? k : 0] = ask(t + first + k * step);
-    }
-#pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-      const int j = first + k * step;
-      if (j < n) {
-        float* const y = x[PAIRS == kNoPairs ? 0 : k];
-        elements(PAIRS == kNoPairs ? raw[PAIRS == kNoPairs ? k : 0] : ask(t + j), t + j, y);
-        top = fmaxf(top, largest(y));
-      }
-    }
-    for (int j = first + kKept * step; j < n; j += step) {
-      float y[kUnit];
-      elements(ask(t + j), t + j, y);
-      top = fmaxf(top, largest(y));
-    }
-    top = warp_max(top);
-    if (TEAM > 1) {
-      if (lane == 0) maxima[warp] = top;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < TEAM; ++w) top = fmaxf(top, maxima[w]);
-    }
-    const float scale = fmaxf(was, page_scale(top)), by = __frcp_rn(scale);
-    uint8_t* const out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) +
-                         (block << a.page_shift) * a.head_dim;
-    if (!begun && scale > was) {   // the codes that stay (the run's are written over them)
-      const float down = was * by;
-      for (int c = me; c < size * a.head_dim / 16; c += kThreads) {
-        uint4 w = reinterpret_cast<uint4*>(out)[c];
-        w.x = scaled_codes(w.x, down);
-        w.y = scaled_codes(w.y, down);
-        w.z = scaled_codes(w.z, down);
-        w.w = scaled_codes(w.w, down);
-        reinterpret_cast<uint4*>(out)[c] = w;
+    if (PAIRS != kNoPairs && !is_v) {
+      sync();   // (the last run's have been used)
+      for (int c = me; c < min(n, room) * pairs; c += kThreads) {
+        const int j = c / pairs, p = c - j * pairs;
+        turns[c] = turn_of(a, t + j, a.turns[p], a.pair_axis[p]);
       }
       sync();
     }
-    auto store = [&](int t, const float* x) {
-      uint8_t* const row = out + (a.slots[t] & (size - 1)) * a.head_dim;
-      *reinterpret_cast<uint2*>(row + run0) = codes8(x, by);
-      *reinterpret_cast<uint2*>(row + run1) = codes8(x + 8, by);
-    };
+    for (int head = head0; head < (PAIRS == kNoPairs ? head0 + 1 : head1); ++head) {
+      if (PAIRS != kNoPairs) src = (is_v ? a.v : a.k) + head * a.head_dim;
+      const int64_t block = (int64_t)page * a.k_heads + head;
+      float* const scale_at = (is_v ? a.v_scale : a.k_scale) + block;
+      const float was = begun ? 0.f : *scale_at;
+
+      // (rotated units are kept as they are wanted, others as they come)
+      Raw raw[PAIRS == kNoPairs ? kKept : 1];
+      float x[PAIRS == kNoPairs ? 1 : kKept][kUnit], top = 0.f;
+      if (PAIRS == kNoPairs) {
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-      const int j = first + k * step;
-      if (j < n) {
-        if (PAIRS == kNoPairs) elements(raw[PAIRS == kNoPairs ? k : 0], t + j, x[0]);
-        store(t + j, x[PAIRS == kNoPairs ? 0 : k]);
+        for (int k = 0; k < kKept; ++k)
+          if (first + k * step < n) raw[PAIRS == kNoPairs ? k : 0] = ask(t + first + k * step);
       }
+#pragma unroll
+      for (int k = 0; k < kKept; ++k) {
+        const int j = first + k * step;
+        if (j < n) {
+          float* const y = x[PAIRS == kNoPairs ? 0 : k];
+          elements(PAIRS == kNoPairs ? raw[PAIRS == kNoPairs ? k : 0] : ask(t + j), t + j, j, y);
+          top = fmaxf(top, largest(y));
+        }
+      }
+      for (int j = first + kKept * step; j < n; j += step) {
+        float y[kUnit];
+        elements(ask(t + j), t + j, j, y);
+        top = fmaxf(top, largest(y));
+      }
+      top = warp_max(top);
+      if (TEAM > 1) {
+        float(&of)[TEAM] = maxima[head & 1];   // (the next head's can come before all have read)
+        if (lane == 0) of[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < TEAM; ++w) top = fmaxf(top, of[w]);
+      }
+      const float scale = fmaxf(was, page_scale(top)), by = __frcp_rn(scale);
+      uint8_t* const out = static_cast<uint8_t*>(is_v ? a.cache_v : a.cache_k) +
+                           (block << a.page_shift) * a.head_dim;
+      if (!begun && scale > was) {   // the codes that stay (the run's are written over them)
+        const float down = was * by;
+        for (int c = me; c < size * a.head_dim / 16; c += kThreads) {
+          uint4 w = reinterpret_cast<uint4*>(out)[c];
+          w.x = scaled_codes(w.x, down);
+          w.y = scaled_codes(w.y, down);
+          w.z = scaled_codes(w.z, down);
+          w.w = scaled_codes(w.w, down);
+          reinterpret_cast<uint4*>(out)[c] = w;
+        }
+        sync();
+      }
+      auto store = [&](int t, const float* x) {
+        uint8_t* const row = out + (a.slots[t] & (size - 1)) * a.head_dim;
+        *reinterpret_cast<uint2*>(row + run0) = codes8(x, by);
+        *reinterpret_cast<uint2*>(row + run1) = codes8(x + 8, by);
+      };
+#pragma unroll
+      for (int k = 0; k < kKept; ++k) {
+        const int j = first + k * step;
+        if (j < n) {
+          if (PAIRS == kNoPairs) elements(raw[PAIRS == kNoPairs ? k : 0], t + j, j, x[0]);
+          store(t + j, x[PAIRS == kNoPairs ? 0 : k]);
+        }
+      }
+      for (int j = first + kKept * step; j < n; j += step) {
+        float y[kUnit];
+        elements(ask(t + j), t + j, j, y);
+        store(t + j, y);
+      }
+      // (every lane has read the scale that was)
+      if (TEAM == 1) __syncwarp();
+      if (me == 0) *scale_at = scale;
     }
-    for (int j = first + kKept * step; j < n; j += step) {
-      float y[kUnit];
-      elements(ask(t + j), t + j, y);
-      store(t + j, y);
-    }
-    // (every lane has read the scale that was)
-    if (TEAM == 1) __syncwarp();
-    if (me == 0) *scale_at = scale;
   }
 }
 
@@ -242,12 +267,20 @@ cudaError_t launch(const RotaryArgs& a, bool neighbours, cudaStream_t stream) {
   // tokens of a team: so that there are enough teams to fill the GPU
   const int64_t work = (int64_t)a.T * 2 * a.k_heads, teams = 16384 / TEAM;
   const int part = (int)std::min<int64_t>(kMostTokens, std::max<int64_t>(1, work / teams));
-  void (*kernel)(RotaryArgs, int) = a.rot == 0   ? page_write_kernel<kNoPairs, TEAM>
+  // heads of k that share the angles: as long as the runs of full pages are still one a team
+  // and SM (GB300, 6146 tokens of 4 heads of 128 in pages of 64)
+  const int64_t runs = std::max<int64_t>(1, a.T >> a.page_shift);
+  const int at_once =
+      a.rot == 0 ? 1
+                 : (int)std::min<int64_t>(std::min(kMostHeads, a.k_heads),
+                                          std::max<int64_t>(1, runs * a.k_heads / 152));
+  void (*kernel)(RotaryArgs, int, int) = a.rot == 0   ? page_write_kernel<kNoPairs, TEAM>
                                     : neighbours ? page_write_kernel<kNeighbours, TEAM>
                                                  : page_write_kernel<kHalves, TEAM>;
   const int64_t of_block = (int64_t)part * (kWarps / TEAM);   // tokens
-  return launch_kernel(true, dim3((unsigned)((a.T + of_block - 1) / of_block), 2 * a.k_heads),
-                       dim3(32 * kWarps), 0, stream, kernel, a, part);
+  return launch_kernel(true, dim3((unsigned)((a.T + of_block - 1) / of_block),
+                            (a.k_heads + at_once - 1) / at_once + a.k_heads),
+                       dim3(32 * kWarps), 0, stream, kernel, a, part, at_once);
 }
 
 }  // namespace

@@ -681,8 +681,8 @@ typedef struct moe_kv_cache {
  *                     become e4m3(q * scale / scale'), exact but for codes that are
  *                     subnormal after it.
  * The tokens that a call brings to one page must follow one another in the call
- * (in any order, but without skipped tokens or other pages' between them), as the tokens of a request
- * do; a page that comes twice in one call is outside the contract.
+ * (in any order, but without skipped tokens or other pages' between them), as the
+ * tokens of a request do; a page that comes twice in one call is outside the contract.
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
  *         pointers, bad strides, T < 0). T == 0 is a no-op.
  */

@@ -13,8 +13,8 @@ from tests.test_attention_refusals import (A, BAD_CACHES, INVALID, MIS, P, UNSUP
 PAGE = binding.MOE_DTYPE_E4M3_PAGE
 
 
-def plan(lib, state=A, new=A, batch=4, table=A, stride=8, wide=8, stack=A, pages=32, size=16,  # noqa: F811,E501
-         rows=4, axes=1, offsets=A, slots=A, positions=A, out=A, refused=A):
+def plan(lib, state=A, new=A, batch=4, table=A, stride=8, wide=8, stack=A, pages=32,  # noqa: F811
+         size=16, rows=4, axes=1, offsets=A, slots=A, positions=A, out=A, refused=A):
     return lib.moe_kv_plan(P(state), P(new), batch, P(table), stride, wide, P(stack), pages, size,
                            rows, axes, P(offsets), P(slots), P(positions), P(out), P(refused),
                            None)
@@ -33,8 +33,8 @@ def test_plan_refusals(lib, kw, want):  # noqa: F811
     assert plan(lib, **kw) == want
 
 
-def prompt(lib, c=None, q=A, qs=1024, rows=4, hq=8, offsets=A, table=A, stride=4, wide=4,  # noqa: F811,E501
-           lengths=A, batch=2, scale=1.0, window=0, out=A, outs=1024, lse=None, ws=A,
+def prompt(lib, c=None, q=A, qs=1024, rows=4, hq=8, offsets=A, table=A, stride=4,  # noqa: F811
+           wide=4, lengths=A, batch=2, scale=1.0, window=0, out=A, outs=1024, lse=None, ws=A,
            ws_bytes=1 << 40):
     return lib.moe_prompt_attention(ctypes.byref(c if c is not None else cache()), P(q), qs, rows,
                                     hq, P(offsets), P(table), stride, wide, P(lengths), batch,
