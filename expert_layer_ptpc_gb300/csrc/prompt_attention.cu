@@ -85,6 +85,8 @@ constexpr int kLeastWork = 4;
 constexpr int kLeastExponent = -64;        // scales below 2^-64 count as that (sums end at 2^128)
 
 enum Kind { kPageScales = 0, kTokenScales = 1, kBf16 = 2 };
+enum Mode { kOne = 0, kTilesEach = 1, kRowsEach = 2 };
+constexpr int kLeastTiles = 4;             // of a segment whose halves share its tiles out
 
 struct Args {
   CacheView c;
@@ -574,8 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   auto place = [](uint32_t base, int rows, int r, int u) -> uint32_t {
     return base + (u >> 3) * (rows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
   };
-  // halves of 128 rows that a segment works on together
-  auto streams_of = [&](const Segment& s) { return s.rows > 128 ? 2 : 1; };
+  // How the two halves work on a segment: each on rows of its own; on the same rows and
+  // every other tile (joined like pieces of different CTAs, and therefore only where there are
+  // such); or the first alone.
+  auto mode_of = [&](const Segment& s) -> int {
+    if (S::kStreams == 1) return kOne;
+    if (s.rows > 128) return kRowsEach;
+    return s.whole() || s.u1 - s.u0 < kLeastTiles ? kOne : kTilesEach;
+  };
 
   if (warp < kSoftWarps) {
     // ---------------- softmax ----------------
@@ -589,21 +597,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     bool ok = true;
     // This half's rows of q, a warp the rows of its threads; the factor of each.
     auto load_q = [&](const Segment& s) {
+      const int base = mode_of(s) == kRowsEach ? me * 128 : 0;   // of the item's rows
       constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;   // lanes of a row, rows of a load
       constexpr int kBatch = 8;                              // loads in flight
       const int u = lane % kLanes;
       const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
       const float scale = fabsf(a.scale) * 1.4426950408889634f;
       const int r0 = (warp & 3) * 32 + lane / kLanes;        // of the half
-      int token = (s.row0 + me * 128 + r0) / a.group;
-      int in = s.row0 + me * 128 + r0 - token * a.group;     // head of the group
+      int token = (s.row0 + base + r0) / a.group;
+      int in = s.row0 + base + r0 - token * a.group;         // head of the group
       for (int i0 = 0; i0 < 32; i0 += kBatch * kAtOnce) {
         uint4 raw[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           raw[i] = make_uint4(0u, 0u, 0u, 0u);
           if (i * kAtOnce < 32 - i0) {
-            if (me * 128 + r0 + i0 + i * kAtOnce < s.rows)
+            if (base + r0 + i0 + i * kAtOnce < s.rows)
               raw[i] = *reinterpret_cast<const uint4*>(
                   a.q + (int64_t)(s.token0 + token) * a.q_stride +
                   (int64_t)(s.kv * a.group + in) * D + u * 8);
@@ -643,16 +652,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       fence_proxy_async_smem();
       warp_arrive(&sh.q_full[me]);
     };
-    auto has_q = [&](const Segment& s) { return me < streams_of(s); };
+    auto has_q = [&](const Segment& s) { return me == 0 || mode_of(s) != kOne; };
     int number = 0;
     bool running = me < S::kStreams && take(0);
     if (running && has_q(sh.ring[0])) load_q(sh.ring[0]);
     for (; ok && running; release(number++)) {
       const Segment& seg = sh.ring[number % kRing];
-      const int streams = streams_of(seg), tiles = seg.u1 - seg.u0;
-      const bool mine = me < streams, whole = seg.whole();
-      const int r = seg.row0 + me * 128 + row;          // of the context
-      const bool live = mine && me * 128 + row < seg.rows;
+      const int mode = mode_of(seg), tiles = seg.u1 - seg.u0;
+      const bool mine = me == 0 || mode != kOne, whole = seg.whole();
+      const int base = mode == kRowsEach ? me * 128 : 0;       // of the item's rows
+      const int tile0 = mode == kTilesEach ? me : 0, step = mode == kTilesEach ? 2 : 1;
+      const int r = seg.row0 + base + row;                     // of the context
+      const bool live = mine && base + row < seg.rows;
       const int token = r / a.group, head = seg.kv * a.group + (r - token * a.group);
       // tokens [lo, hi) are seen (rows behind the last take anything; a warp of such rows
       // only keeps step)
@@ -665,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       if (mine) {
         const float factor = sh.row_scale[me * 128 + row];
         const int start = seg.start + seg.u0 * kTile;
-        for (int i = 0; ok && i < tiles; ++i) {
+        for (int i = tile0; ok && i < tiles; i += step) {
           const int turn = S::kSlots == 2 ? i & 1 : 0, slot = me + turn;
           const uint32_t s_at = tmem + lanes + slot * kTile;
           ok = warp_wait(&sh.s_full[slot], (s_phase >> turn) & 1u, sh, a.err,
@@ -676,14 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           // with two, they are waited for before O is touched, and before the barrier can get a
           // phase further.
           auto last_products = [&]() -> bool {
-            return S::kSlots == 1 || i == 0 ||
+            return S::kSlots == 1 || i == tile0 ||
                    warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
           };
           if (!works) {
             ok = last_products();
             if (!ok) break;
             warp_arrive(&sh.p_full[slot]);
-            if (S::kSlots == 2 || i == tiles - 1) o_phase ^= 1u;
+            if (S::kSlots == 2 || i + step >= tiles) o_phase ^= 1u;
             continue;
           }
           tc_fence_after_sync();
@@ -752,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             const float down = top == -INFINITY ? 0.f : exp2_approx(top - next);
             top = next;
             sum *= down;
-            if (i > 0) {
+            if (i > tile0) {
               ok = last_products();
               if (!ok) break;
               waited = true;
@@ -792,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             if (!ok) break;
           }
           warp_arrive(&sh.p_full[slot]);
-          if (S::kSlots == 2 || i == tiles - 1) o_phase ^= 1u;   // (commits on o_full)
+          if (S::kSlots == 2 || i + step >= tiles) o_phase ^= 1u;   // (commits on o_full)
         }
         if (!ok) break;
       }
@@ -836,8 +847,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       tc_fence_before_sync();
       warp_arrive(&sh.o_empty[me]);
       if (live) {
-        if (!whole) a.stats[slot * kRows + me * 128 + row] = make_float2(top, sum);
-        else if (a.lse != nullptr)
+        if (!whole) {
+          a.stats[slot * kRows + me * 128 + row] = make_float2(top, sum);
+          if (S::kStreams == 2 && mode == kOne)   // (the other half's tiles: none)
+            a.stats[slot * kRows + 128 + row] = make_float2(-INFINITY, 0.f);
+        } else if (a.lse != nullptr)
           a.lse[to * a.q_heads + head] =
               sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
       }
@@ -1072,21 +1086,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       bool ok = true;
       constexpr uint32_t kQk = idesc_f16(kIsBf16, kTile, false), kPv = idesc_f16(kIsBf16, D, true);
       for (int number = 0; ok && take(number); ++number) {
-        const int streams = streams_of(sh.ring[number % kRing]);
+        const int mode = mode_of(sh.ring[number % kRing]);
         const int tiles = sh.ring[number % kRing].u1 - sh.ring[number % kRing].u0;
         release(number);
-        // the scores of tile i of a stream
-        auto scores = [&](int stream, int i) -> bool {
-          if (i == 0) {   // the stream's rows of q
+        // Task t: the scores, then the weights' products, of a stream and a tile; two tasks
+        // are under way where there are two tiles of scores for them.
+        const int tasks = mode == kRowsEach ? 2 * tiles : tiles;
+        const int ahead = mode == kOne && S::kSlots == 1 ? 1 : 2;
+        auto stream_of = [&](int t) { return mode == kOne ? 0 : t & 1; };
+        auto slot_of = [&](int t) { return S::kSlots == 2 ? t & 1 : stream_of(t); };
+        auto begins = [&](int t) { return t < (mode == kOne ? 1 : 2); };            // its stream
+        auto ends = [&](int t) { return t >= tasks - (mode == kOne ? 1 : 2); };
+        auto opens = [&](int t) { return mode != kRowsEach || (t & 1) == 0; };       // its tile
+        auto closes = [&](int t) { return mode != kRowsEach || (t & 1) == 1; };
+        auto scores = [&](int t) -> bool {
+          const int stream = stream_of(t), slot = slot_of(t);
+          if (begins(t)) {   // the stream's rows of q
             if (!warp_wait(&sh.q_full[stream], (q_phase >> stream) & 1u, sh, a.err,
                            kErrTimeoutMma))
               return false;
             q_phase ^= 1u << stream;
           }
-          if (stream == 0 && !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
+          if (opens(t) && !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
             return false;
           tc_fence_after_sync();
-          const int slot = stream + (S::kSlots == 2 ? i & 1 : 0);
           const uint32_t d = uniform(tmem + slot * kTile);
           const uint32_t qs = uniform(desc_k(q_at + stream * S::kQBytes));
           const uint32_t ks = uniform(desc_k(k_at + k_stage * S::kTileBytes));
@@ -1096,52 +1119,49 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
               mma_f16_ss(d, qs + ((j >> 2) * (128 * 128) + (j & 3) * 32) / 16,
                          ks + ((j >> 2) * (kTile * 128) + (j & 3) * 32) / 16, kQk, j > 0 ? 1u : 0u);
             mma_commit(smem_u32(&sh.s_full[slot]));
-            if (stream == streams - 1) mma_commit(smem_u32(&sh.k_empty[k_stage]));
+            if (closes(t)) mma_commit(smem_u32(&sh.k_empty[k_stage]));
           }
           __syncwarp();
-          if (stream == streams - 1 && ++k_stage == S::kStages) {
+          if (closes(t) && ++k_stage == S::kStages) {
             k_stage = 0;
             k_phase ^= 1u;
           }
           return true;
         };
-        for (int i = 0; ok && i < min(tiles, S::kSlots); ++i)
-          for (int stream = 0; ok && stream < streams; ++stream) ok = scores(stream, i);
-        for (int i = 0; ok && i < tiles; ++i) {
-          for (int stream = 0; ok && stream < streams; ++stream) {
-            const int turn = S::kSlots == 2 ? i & 1 : 0, slot = stream + turn;
-            if (i == 0) {   // O: the last segment's has been read
-              ok = warp_wait(&sh.o_empty[stream], (oe_phase >> stream) & 1u, sh, a.err,
-                             kErrTimeoutMma);
-              if (!ok) break;
-              oe_phase ^= 1u << stream;
-            }
-            if (stream == 0) {
-              ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a.err, kErrTimeoutMma);
-              if (!ok) break;
-            }
-            ok = warp_wait(&sh.p_full[slot], (p_phase >> slot) & 1u, sh, a.err, kErrTimeoutMma);
+        for (int t = 0; ok && t < min(tasks, ahead); ++t) ok = scores(t);
+        for (int t = 0; ok && t < tasks; ++t) {
+          const int stream = stream_of(t), slot = slot_of(t);
+          if (begins(t)) {   // O: the last segment's has been read
+            ok = warp_wait(&sh.o_empty[stream], (oe_phase >> stream) & 1u, sh, a.err,
+                           kErrTimeoutMma);
             if (!ok) break;
-            p_phase ^= 1u << slot;
-            tc_fence_after_sync();
-            const uint32_t d = uniform(tmem + S::kSOut + stream * D);
-            const uint32_t p = uniform(tmem + slot * kTile + S::kPOut);
-            const uint32_t vs = uniform(desc_mn(v_at + v_stage * S::kTileBytes, kTile * 128));
-            const uint32_t more = uniform(i > 0 ? 1u : 0u);
-            if (elect_one()) {
-#pragma unroll
-              for (int j = 0; j < kTile / 16; ++j)
-                mma_f16_ts(d, p + 8 * j, vs + j * (2048 / 16), kPv, j > 0 ? 1u : more);
-              if (S::kSlots == 2 || i == tiles - 1) mma_commit(smem_u32(&sh.o_full[stream]));
-              if (stream == streams - 1) mma_commit(smem_u32(&sh.v_empty[v_stage]));
-            }
-            __syncwarp();
-            if (stream == streams - 1 && ++v_stage == S::kStages) {
-              v_stage = 0;
-              v_phase ^= 1u;
-            }
-            if (i + S::kSlots < tiles) ok = scores(stream, i + S::kSlots);
+            oe_phase ^= 1u << stream;
           }
+          if (opens(t)) {
+            ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a.err, kErrTimeoutMma);
+            if (!ok) break;
+          }
+          ok = warp_wait(&sh.p_full[slot], (p_phase >> slot) & 1u, sh, a.err, kErrTimeoutMma);
+          if (!ok) break;
+          p_phase ^= 1u << slot;
+          tc_fence_after_sync();
+          const uint32_t d = uniform(tmem + S::kSOut + stream * D);
+          const uint32_t p = uniform(tmem + slot * kTile + S::kPOut);
+          const uint32_t vs = uniform(desc_mn(v_at + v_stage * S::kTileBytes, kTile * 128));
+          const uint32_t more = uniform(begins(t) ? 0u : 1u);
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < kTile / 16; ++j)
+              mma_f16_ts(d, p + 8 * j, vs + j * (2048 / 16), kPv, j > 0 ? 1u : more);
+            if (S::kSlots == 2 || ends(t)) mma_commit(smem_u32(&sh.o_full[stream]));
+            if (closes(t)) mma_commit(smem_u32(&sh.v_empty[v_stage]));
+          }
+          __syncwarp();
+          if (closes(t) && ++v_stage == S::kStages) {
+            v_stage = 0;
+            v_phase ^= 1u;
+          }
+          if (t + ahead < tasks) ok = scores(t + ahead);
         }
       }
       // every product has ended before tensor memory and shared memory are given back
@@ -1207,7 +1227,10 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
   // between them can have got nothing)
   __shared__ int slots[kWorkers];
   __shared__ int count;
-  __shared__ float weight[kWorkers][32];   // of a piece's row, over the joined sum
+  // of a piece's row, over the joined sum; items of up to 128 rows have two pieces a slot,
+  // those of the CTA's halves
+  constexpr int kMostHalves = kRows == 256 ? 2 : 1;
+  __shared__ float weight[kMostHalves * kWorkers][32];
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int n = 1;
@@ -1233,10 +1256,17 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
   }
   __syncthreads();
   const int row = blockIdx.y * 32 + (threadIdx.x & 31);
+  const int halves = kMostHalves == 2 && rec.rows <= 128 ? 2 : 1;
+  const int pieces = count * halves;
+  // row of a piece among all slots' rows
+  auto place = [&](int i) -> int64_t {
+    return (int64_t)slots[i / halves] * kRows + (i % halves) * 128 + row;
+  };
+  if (blockIdx.y * 32 >= rec.rows) return;
   if (threadIdx.x < 32) {
     float top = -INFINITY, sum = 0.f;
-    for (int i = 0; i < count; ++i) {
-      const float2 s = a.stats[slots[i] * kRows + row];
+    for (int i = 0; i < pieces; ++i) {
+      const float2 s = a.stats[place(i)];
       weight[i][threadIdx.x] = s.x;
       const float next = fmaxf(top, s.x);
       if (next != -INFINITY)
@@ -1245,7 +1275,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
       top = next;
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < pieces; ++i) {
       const float m = weight[i][threadIdx.x];
       weight[i][threadIdx.x] = m == -INFINITY ? 0.f : exp2_approx(m - top) * inv;
     }
@@ -1266,13 +1296,14 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
   float4 o[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < count; ++i) {
+  for (int i = 0; i < pieces; ++i) {
     const float by = weight[i][threadIdx.x & 31];
-    const int64_t slot = slots[i];
+    if (by == 0.f) continue;   // (a half without tiles left no rows)
+    const int64_t at = (int64_t)slots[i / halves] * (D / 4) * kRows + (i % halves) * 128 + row;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       const int d = (threadIdx.x >> 5) + k * (kJoinThreads / 32);
-      const float4 v = parts[(slot * (D / 4) + d) * kRows + row];
+      const float4 v = parts[at + (int64_t)d * kRows];
       o[k].x = fmaf(v.x, by, o[k].x);
       o[k].y = fmaf(v.y, by, o[k].y);
       o[k].z = fmaf(v.z, by, o[k].z);

@@ -267,3 +267,21 @@ def test_decoder_example_with_page_scales():
     worst = example.main(["--steps", "3", "--batch", "6", "--prompt", "333", "--cache",
                           "e4m3_page"])
     assert worst <= 2 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,lengths,news,window", [
+    (16, [5000, 700, 0, 3333], [5, 8, 0, 1], 0), (1, [5121], [128], 0), (3, [6000, 64], [43, 1], 0),
+    (64, [4000], [2], 1500), (20, [9000, 2500], [6, 6], 2000),
+])
+def test_few_rows_over_long_contexts(kind, d, group, lengths, news, window):
+    """Items of up to 128 rows that are cut: the halves of a CTA take every other tile, and
+    their pieces are joined; pages absent in the middle and at an end, rows that see nothing."""
+    cache, q, table = prompt_case(group, lengths, news, 2 * group, 2, d, 32, kind)
+    check_prompt(cache, q, table, lengths, news, window=window, kind=kind)
+    table[0, 20:60] = -1
+    table[-1, :9] = cache.pages
+    check_prompt(cache, q, table, lengths, news, window=window, kind=kind)
+    table[0] = -1
+    check_prompt(cache, q, table, lengths, news, window=window, kind=kind)

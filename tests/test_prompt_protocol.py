@@ -1,7 +1,7 @@
 """Host model of the barriers between the roles of a prompt-attention CTA: the warp that
-hands out segments, loading warps of keys and of values, an issuer of products and four
-softmax warps for each half of the rows. The roles run as generators in random order, the
-commits of an issuer's products land late but in its order. Every parity wait
+hands out segments, loading warps of keys and of values, the issuer of the products, and
+two halves of softmax warps. The roles run as generators in random order, the products'
+commits land late but in order. Every parity wait
 names the phase that it means: the model checks that the barrier is in that phase or just past
 it (a parity cannot be mistaken), that nobody waits for ever, and that buffers are written
 only when their readers are done. No GPU involved."""
@@ -35,24 +35,34 @@ class Model:
         self.rng = random.Random(seed)
         ring = range(stages)
         self.k_full, self.v_full = ([Barrier(LOADERS) for _ in ring] for _ in range(2))
-        self.k_empty, self.v_empty = ([Barrier(halves) for _ in ring] for _ in range(2))
+        self.k_empty, self.v_empty = ([Barrier(1) for _ in ring] for _ in range(2))
         self.q_full = [Barrier(4) for _ in range(2)]
         self.s_full, self.p_full = ([Barrier(n) for _ in range(2)] for n in (1, 4))
         self.o_full, self.o_empty = ([Barrier(n) for _ in range(2)] for n in (1, 4))
         self.maxed = [Barrier(LOADERS) for _ in range(2)]
-        readers = 5 * halves + 2 * LOADERS
+        readers = 4 * halves + 2 * LOADERS + 1
         self.seg_full = [Barrier(1) for _ in range(RING)]
         self.seg_empty = [Barrier(readers) for _ in range(RING)]
         self.ring = [None] * RING
-        self.queues = [[], []]          # an issuer's products and commits under way, in order
+        self.queue = []                 # products and commits under way, in order
         self.holds = [[[None] * LOADERS for _ in range(stages)] for _ in range(2)]
         self.q_holds = [[None] * 4 for _ in range(2)]
         self.side = [[None] * LOADERS for _ in range(SIDES)]
         self.s_holds, self.o_holds = [None] * 2, [[], []]
         self.out = []
 
-    def streams(self, rows):
-        return 2 if rows > 128 and self.halves == 2 else 1
+    def mode(self, n):
+        """0: the first half alone; 1: the same rows, every other tile; 2: rows of their own."""
+        rows, tiles = self.segments[n]
+        if self.halves == 1:
+            return 0
+        return 2 if rows > 128 else 1 if rows == 128 and tiles >= 4 else 0
+
+    def tiles_of(self, n, me):
+        mode, tiles = self.mode(n), self.segments[n][1]
+        if mode == 0:
+            return list(range(tiles)) if me == 0 else []
+        return list(range(me, tiles, 2)) if mode == 1 else list(range(tiles))
 
     @staticmethod
     def wait(barrier, phase):
@@ -112,58 +122,71 @@ class Model:
                 stage, use = 0, use + 1
             yield
 
-    def issuer(self, me):
-        queue = self.queues[me]
-        k = v = number = q = oe = 0
-        p = [0, 0]
+    def issuer(self):
+        queue = self.queue
+        k = v = number = 0              # tiles used
+        p, q, oe = [0, 0], [0, 0], [0, 0]
         while (yield from self.take(number)):
             n = number
-            rows, tiles = self.segments[n]
+            mode, tiles = self.mode(n), self.segments[n][1]
             self.release(number)
             number += 1
-            mine = me < self.streams(rows)
+            tasks = 2 * tiles if mode == 2 else tiles
+            each = 1 if mode == 0 else 2        # streams
+            ahead = self.slots if mode == 0 else 2
 
-            def scores(i):
+            def of(t):
+                stream = t % each
+                return stream, (t % 2 if self.slots == 2 else stream), t // 2 if mode == 2 else t
+
+            def closes(t):
+                return mode != 2 or t % 2 == 1
+
+            def opens(t):
+                return mode != 2 or t % 2 == 0
+
+            def scores(t):
                 nonlocal k
-                stage, slot = k % self.stages, me + i % self.slots
-                yield from self.wait(self.k_full[stage], k // self.stages)
-                if mine:
-                    queue.append(("s", slot, (n, i, me), stage))
-                    queue.append(self.s_full[slot])
+                stream, slot, tile = of(t)
+                stage = k % self.stages
+                if t < each:
+                    yield from self.wait(self.q_full[stream], q[stream])
+                    q[stream] += 1
+                if opens(t):
+                    yield from self.wait(self.k_full[stage], k // self.stages)
+                queue.append(("s", slot, (n, tile, stream), stage))
+                queue.append(self.s_full[slot])
+                if closes(t):
                     queue.append(self.k_empty[stage])
-                else:
-                    self.k_empty[stage].arrive()
-                k += 1
+                    k += 1
 
-            if mine:
-                yield from self.wait(self.q_full[me], q)
-                q += 1
-            for i in range(min(tiles, self.slots)):
-                yield from scores(i)
-            for i in range(tiles):
-                stage, slot = v % self.stages, me + i % self.slots
-                if mine and i == 0:
-                    yield from self.wait(self.o_empty[me], oe - 1)
-                    oe += 1
-                yield from self.wait(self.v_full[stage], v // self.stages)
-                if mine:
-                    yield from self.wait(self.p_full[slot], p[i % self.slots])
-                    p[i % self.slots] += 1
-                    queue.append(("o", slot, (n, i, me), stage))
-                    queue.append(self.o_full[me])
+            for t in range(min(tasks, ahead)):
+                yield from scores(t)
+            for t in range(tasks):
+                stream, slot, tile = of(t)
+                stage = v % self.stages
+                if t < each:
+                    yield from self.wait(self.o_empty[stream], oe[stream] - 1)
+                    oe[stream] += 1
+                if opens(t):
+                    yield from self.wait(self.v_full[stage], v // self.stages)
+                yield from self.wait(self.p_full[slot], p[slot])
+                p[slot] += 1
+                queue.append(("o", slot, (n, tile, stream), stage))
+                if self.slots == 2 or t >= tasks - each:
+                    queue.append(self.o_full[stream])
+                if closes(t):
                     queue.append(self.v_empty[stage])
-                else:
-                    self.v_empty[stage].arrive()
-                v += 1
-                if i + self.slots < tiles:
-                    yield from scores(i + self.slots)
+                    v += 1
+                if t + ahead < tasks:
+                    yield from scores(t + ahead)
                 yield
 
     def softmax(self, me, w):
         s, o, tile = [0, 0], 0, 0
 
         def load_q(n):
-            if self.segments[n][1] and me < self.streams(self.segments[n][0]):
+            if self.tiles_of(n, me):
                 self.q_holds[me][w] = n
                 self.q_full[me].arrive()
 
@@ -173,48 +196,46 @@ class Model:
             load_q(0)
         while running:
             n = number
-            rows, tiles = self.segments[n]
-            mine = me < self.streams(rows)
-            if mine:
-                for i in range(tiles):
-                    turn = i % self.slots
-                    slot, waited = me + turn, self.slots == 1
-                    yield from self.wait(self.s_full[slot], s[turn])
-                    s[turn] += 1
-                    assert self.s_holds[slot] == (n, i, me)
-                    yield
-                    if i > 0 and self.rng.random() < 0.5:     # rescales O
-                        if not waited:
-                            yield from self.wait(self.o_full[me], o - 1)
-                            waited = True
-                        assert self.o_holds[me][-1] == (n, i - 1, me)
-                        yield
-                    assert self.s_holds[slot] == (n, i, me)
-                    assert self.side[(tile + i) % SIDES] == [(n, i)] * LOADERS
-                    if i > 0 and not waited:
+            mine = self.tiles_of(n, me)
+            for at, i in enumerate(mine):
+                turn = i % 2 if self.slots == 2 else 0
+                slot, waited = me + turn, self.slots == 1
+                yield from self.wait(self.s_full[slot], s[turn])
+                s[turn] += 1
+                assert self.s_holds[slot] == (n, i, me)
+                yield
+                if at > 0 and self.rng.random() < 0.5:     # rescales O
+                    if not waited:
                         yield from self.wait(self.o_full[me], o - 1)
-                    self.p_full[slot].arrive()
-                    o += 1
+                        waited = True
+                    assert self.o_holds[me][-1] == (n, mine[at - 1], me)
                     yield
+                assert self.s_holds[slot] == (n, i, me)
+                assert self.side[(tile + i) % SIDES] == [(n, i)] * LOADERS
+                if at > 0 and not waited:
+                    yield from self.wait(self.o_full[me], o - 1)
+                self.p_full[slot].arrive()
+                if self.slots == 2 or at == len(mine) - 1:
+                    o += 1
+                yield
             running = yield from self.take(number + 1)
             if running:
                 load_q(number + 1)
-            if mine and tiles:
+            if mine:
                 yield from self.wait(self.o_full[me], o - 1)
-                assert self.o_holds[me] == [(n, i, me) for i in range(tiles)]
-            tile += tiles
+                assert self.o_holds[me] == [(n, i, me) for i in mine]
+            tile += self.segments[n][1]
             if mine:
                 yield
-                if tiles:
-                    assert self.o_holds[me] == [(n, i, me) for i in range(tiles)]
-                    self.o_empty[me].arrive()
+                assert self.o_holds[me] == [(n, i, me) for i in mine]
+                self.o_empty[me].arrive()
                 self.out.append((n, me, w))
             self.release(number)
             number += 1
 
-    def tensor_core(self, queue):
+    def tensor_core(self):
         """One queued product or commit."""
-        x = queue.pop(0)
+        x = self.queue.pop(0)
         if isinstance(x, Barrier):
             x.arrive()
             return
@@ -227,21 +248,20 @@ class Model:
         else:
             assert self.holds[1][stage] == [(n, i)] * LOADERS
             assert self.s_holds[slot] == task
-            if i == 0:
+            if i == self.tiles_of(n, stream)[0]:
                 self.o_holds[stream] = []
             self.o_holds[stream].append(task)
 
     def run(self):
         roles = [self.loader(x, w) for x in range(2) for w in range(LOADERS)]
-        roles += [self.issuer(me) for me in range(self.halves)] + [self.planner()]
+        roles += [self.issuer(), self.planner()]
         roles += [self.softmax(me, w) for me in range(self.halves) for w in range(4)]
         idle = 0
         speed = [self.rng.choice((1, 1, 3, 10, 40)) for _ in roles]
         while roles:
-            before = [len(x) for x in self.queues]
-            queue = self.rng.choice(self.queues)
-            if queue and self.rng.random() < 0.3:
-                self.tensor_core(queue)
+            before = len(self.queue)
+            if self.queue and self.rng.random() < 0.3:
+                self.tensor_core()
                 idle = 0
             i = self.rng.randrange(len(roles))
             if self.rng.randrange(speed[i]) == 0:
@@ -251,11 +271,10 @@ class Model:
                     roles.pop(i)
                     speed.pop(i)
                     idle = 0
-            idle = 0 if [len(x) for x in self.queues] != before else idle + 1
+            idle = 0 if len(self.queue) != before else idle + 1
             assert idle < 20000, "a role waits for ever"
-        for queue in self.queues:
-            while queue:
-                self.tensor_core(queue)
+        while self.queue:
+            self.tensor_core()
 
 
 @pytest.mark.parametrize("halves,stages", [(2, 2), (2, 3), (1, 2)])
@@ -266,6 +285,6 @@ def test_roles_of_a_cta(halves, stages):
                     for _ in range(rng.randint(0, 40))]
         m = Model(segments, stages, halves, trial)
         m.run()
-        want = [(n, me, w) for n, (rows, _) in enumerate(segments)
-                for me in range(m.streams(rows)) for w in range(4)]
+        want = [(n, me, w) for n in range(len(segments))
+                for me in range(halves) if m.tiles_of(n, me) for w in range(4)]
         assert sorted(m.out) == sorted(want)
