@@ -72,6 +72,7 @@ constexpr int kThreads = 32 * (kMmaWarp + 4);
 // Registers of a thread, by role (640 threads are launched with 96 each: 61440).
 constexpr int kSoftRegs = 136, kLoadRegs = 80, kMmaRegs = 48;
 static_assert(256 * kSoftRegs + 256 * kLoadRegs + 128 * kMmaRegs <= 96 * kThreads, "registers");
+constexpr int kAhead = 3;                  // tiles whose rows are on their way to L2
 constexpr int kRing = 16;                  // segments handed out at a time
 constexpr int kSides = 8;                  // tiles whose masks and factors are at hand
 constexpr int kRequests = 256;             // contexts whose places a CTA keeps at hand
@@ -963,9 +964,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
     bool running = asked, ok = true;
     uint32_t now = resolve();               // the lane's row of this tile
     ask();
-    bool follows = asked;
-    uint32_t then = resolve();              // and of the next
-    ask();
+    bool follows[kAhead];                   // and of the next ones
+    uint32_t then[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      follows[i] = asked;
+      then[i] = resolve();
+      ask();
+    }
     if (running && !kIsBf16) {              // (bf16 rows go straight to the stages)
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) reg[i] = fetch(now, i);
@@ -1027,11 +1033,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
 
       const uint32_t to = stages + stage * S::kTileBytes;
       const uint32_t mine = now;
-      running = follows;
-      now = then;
+      running = follows[0];
+      now = then[0];
       if (!kIsBf16) ask_scales(now);
-      follows = asked;
-      then = resolve();
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) {
+        follows[i] = follows[i + 1];
+        then[i] = then[i + 1];
+      }
+      follows[kAhead - 1] = asked;
+      then[kAhead - 1] = resolve();
       ask();
       ok = warp_wait(&empty[stage], phase, sh, a.err, kErrTimeoutProducer);
       if (!ok) break;

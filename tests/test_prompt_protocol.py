@@ -13,6 +13,7 @@ import pytest
 LOADERS = 4
 SIDES = 8
 RING = 16
+AHEAD = 6      # tiles that a loading warp has looked up, the one it lays out included
 
 
 class Barrier:
@@ -97,7 +98,7 @@ class Model:
 
         def ask():
             nonlocal number, more
-            while more and len(tiles) < 4:
+            while more and len(tiles) < AHEAD:
                 more = yield from self.take(number)
                 if more:
                     tiles.extend((number, i) for i in range(self.segments[number][1]))
