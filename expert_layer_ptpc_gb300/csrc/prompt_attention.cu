@@ -27,7 +27,8 @@
 // Roles of a CTA's warps: 0-3 and 4-7 the softmax of 128 rows each, a row a thread, and
 // the rows' q; 8-11 fetch keys from the pages and lay them out for the tensor cores, 12-15
 // values; 16 issues the products, 17 hands out the work. While one half's softmax runs, the
-// other half's products do. Loading warps turn codes into fp16 in registers: a lane asks for
+// other half's products do. (In a cut item of up to 128 rows the halves take every other tile of
+// the same rows.) Loading warps turn codes into fp16 in registers: a lane asks for
 // a piece of the next tile as it lays the last one's out, and the rows of the tile after
 // that are on their way to L2. (Copies straight into shared memory, with the codes turned
 // there, would pass 32 KB a tile more through it, which the products' operands already fill
@@ -39,8 +40,9 @@
 // which a second kernel joins.
 //
 // GB300, 64 heads on 4 of 128 elements, a scale a page: a prompt of 8192 tokens 1015 us, 1.08
-// PFLOP/s of cuBLAS's 1.95; 2048 tokens over 40001 with a scale a token 2.76 ms, 0.95 PFLOP/s;
-// 5 tokens of each of 32 requests over up to 16384 (272 MB) 124 us, 2.2 TB/s. The tensor
+// PFLOP/s of cuBLAS's 1.95; 2048 tokens over 40001 with a scale a token 2.75 ms, 0.95 PFLOP/s;
+// 5 tokens of each of 32 requests over up to 16384 (272 MB) 120 us, 2.3 TB/s, which the loading
+// warps bound (2800 cycles a tile). The tensor
 // pipe is 47% busy; what bounds it is the turn of a half: its softmax (about 2500 cycles a
 // tile, of 512 that the exponentials take: loads from TMEM and issue slots shared with the
 // loading warps) and then its two products, which one thread issues in some 1100. Tried
