@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       tile += tiles;
       if (!mine) continue;
       const int64_t slot = 2 * worker + (seg.u0 == 0 ? 1 : 0);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;   // (0: nothing seen; NaN stays)
       const int64_t to = (int64_t)(seg.token0 + token);
       uint16_t* const out = a.out + to * a.out_stride + (int64_t)head * D;
       float4* const part = reinterpret_cast<float4*>(a.parts) +
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
             a.stats[slot * kRows + 128 + row] = make_float2(-INFINITY, 0.f);
         } else if (a.lse != nullptr)
           a.lse[to * a.q_heads + head] =
-              sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+              sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       }
       if (threadIdx.x == 0) {
         Record& rec = a.records[worker];
@@ -1281,22 +1281,24 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
     for (int i = 0; i < pieces; ++i) {
       const float2 s = a.stats[place(i)];
       weight[i][threadIdx.x] = s.x;
+      // (a sum is NaN where a score was, and stays so, whatever the maxima)
       const float next = fmaxf(top, s.x);
-      if (next != -INFINITY)
-        sum = sum * (top == -INFINITY ? 0.f : exp2_approx(top - next)) +
-              (s.x == -INFINITY ? 0.f : s.y * exp2_approx(s.x - next));
+      sum = sum * (top == -INFINITY ? 0.f : exp2_approx(top - next)) +
+            s.y * (s.x == -INFINITY ? 0.f : exp2_approx(s.x - next));
       top = next;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     for (int i = 0; i < pieces; ++i) {
       const float m = weight[i][threadIdx.x];
-      weight[i][threadIdx.x] = m == -INFINITY ? 0.f : exp2_approx(m - top) * inv;
+      weight[i][threadIdx.x] = sum != sum        ? sum
+                               : m == -INFINITY ? -1.f   // nothing seen, or no tiles: no rows
+                                                : exp2_approx(m - top) * inv;
     }
     if (row < rec.rows && a.lse != nullptr) {
       const int r = rec.row0 + row, token = r / a.group;
       const int head = rec.tail.y * a.group + (r - token * a.group);
       a.lse[(int64_t)(rec.token0 + token) * a.q_heads + head] =
-          sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
   __syncthreads();
@@ -1311,7 +1313,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
   for (int k = 0; k < kSteps; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < pieces; ++i) {
     const float by = weight[i][threadIdx.x & 31];
-    if (by == 0.f) continue;   // (a half without tiles left no rows)
+    if (by < 0.f) continue;
     const int64_t at = (int64_t)slots[i / halves] * (D / 4) * kRows + (i % halves) * 128 + row;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {

@@ -819,6 +819,8 @@ MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int bat
  *   left as they are.
  *   Slots that no context covers have no influence, whatever they hold; a context's
  *   keys and values from the first token on that any of its rows sees must be finite.
+ *   (A NaN there, or in a row of q, shows as NaN in the rows that it reaches, and never as
+ *   a row that sees nothing.)
  *   ws: device workspace of moe_prompt_attention_workspace_size bytes, as for
  *   moe_paged_attention.
  *   Sums, maxima and accumulators are fp32; results do not depend on timing. What the

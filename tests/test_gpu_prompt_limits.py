@@ -1,0 +1,88 @@
+"""Attention of many new tokens at the ends of its range: NaN, scales of every size, long
+segments of work, and rows of padding."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from expert_layer_ptpc_gb300 import attention, binding
+from tests.gpu_helpers import U32, ensure_library, require_gpu
+from tests.test_gpu_attention import HALF_BF16, host, values
+from tests.test_gpu_prompt_attention import KINDS, check_prompt, ints, prompt_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    require_gpu()
+    ensure_library()
+    yield
+    assert binding.moe_device_status() == (0, 0)     # no wait of any test ran out
+
+
+# ---------------------------------------------------------------------------
+# NaN stays in the rows that it reaches, whole items and cut ones alike
+# ---------------------------------------------------------------------------
+LONG_AND_SHORT = ([9000, 60, 300], [40, 60, 2])     # cut over many CTAs, and whole
+
+
+class WithNan:
+    """A cache whose attend_prompt gets NaN in some rows of q, and gives back what those
+    rows are without."""
+
+    def __init__(self, cache, hurt):
+        self.cache, self.hurt = cache, hurt
+        self.k, self.v, self.k_scale, self.v_scale = cache.k, cache.v, cache.k_scale, cache.v_scale
+
+    def attend_prompt(self, q, *call, out, lse, **kw):
+        clean = self.cache.attend_prompt(q, *call, return_lse=True, **kw)
+        q = q.clone()
+        q[self.hurt] = float("nan")
+        self.cache.attend_prompt(q, *call, out=out, lse=lse, **kw)
+        assert torch.isnan(out[self.hurt].float()).all() and torch.isnan(lse[self.hurt]).all()
+        out[self.hurt], lse[self.hurt] = clean[0][self.hurt], clean[1][self.hurt]
+        return out, lse
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group", [2, 5])           # items of up to 128 rows, and of more
+def test_nan_of_q_stays_in_its_rows(kind, d, group):
+    """(A row's neighbours need not be the same bit for bit: the 32 rows of a warp move the
+    bounds of their weights together, by what is no power of two, and a row of NaN moves none.)"""
+    lengths, news = LONG_AND_SHORT
+    cache, q, table = prompt_case(d, lengths, news, 2 * group, 2, d, 32, kind)
+    hurt = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    for row, head in ((0, 0), (17, group), (39, 2 * group - 1), (40, 1), (77, group), (101, 0)):
+        hurt[row, head] = True
+    check_prompt(WithNan(cache, hurt), q, table, lengths, news, kind=kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_nan_of_the_cache_reaches_every_row_that_sees_it(kind, which):
+    """A NaN in a token that all rows of a context see, and in no other context."""
+    lengths, news = LONG_AND_SHORT
+    cache, q, table = prompt_case(3, lengths, news, 6, 2, 128, 32, kind)
+    call = ints(np.concatenate([[0], np.cumsum(news)]).tolist()), torch.from_numpy(table).cuda(), \
+        ints(lengths)
+    clean = cache.attend_prompt(q, *call, return_lse=True)
+    for context, rows in ((0, slice(0, 40)), (2, slice(100, 102))):
+        t = getattr(cache, which)
+        page, offset = int(table[context, 5]), 3
+        kept = t[page, :, offset].clone()
+        t[page, :, offset, 9] = float("nan") if kind == "bf16" else 0x7f
+        out, lse = cache.attend_prompt(q, *call, return_lse=True)
+        t[page, :, offset] = kept
+        seen = out[rows] if which == "k" else out[rows][..., 9]
+        assert torch.isnan(seen.float()).all()
+        if which == "k":
+            assert torch.isnan(lse[rows]).all()
+        else:
+            assert torch.equal(lse[rows], clean[1][rows])
+        others = torch.ones(102, dtype=torch.bool, device="cuda")
+        others[rows] = False
+        assert torch.equal(out[others], clean[0][others])
+        assert torch.equal(lse[others], clean[1][others])
