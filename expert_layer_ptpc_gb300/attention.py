@@ -100,8 +100,8 @@ _kept = threading.local()   # workspaces: this host thread's, by GPU and stream
 class PagedKVCache:
     """Pages of keys and values, [pages, heads, page_size, head_dim] each, as
     e4m3 codes with one fp32 scale per token and head (scales [pages, heads,
-    page_size]) or per page and head (a power of two, scales [pages, heads]), or in
-    bf16."""
+    page_size]) or per page and head (scales [pages, heads]: powers of two as the writes
+    make them; attend_prompt rounds others to 11 bits), or in bf16."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:

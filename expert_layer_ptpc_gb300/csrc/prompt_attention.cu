@@ -15,9 +15,10 @@
 // rarely rescaled. A weight is off by up to 2^-11 of it in fp16, or 2^-32 of the largest
 // where that is more.
 //
-// What the tensor cores multiply: e4m3 codes in fp16, which holds them; a page's scale, a
-// power of two, goes into them as a power of two relative to the tile's largest (exact;
-// what is 2^-31 of the tile's largest becomes 0), a token's scale into the score's column
+// What the tensor cores multiply: e4m3 codes in fp16, which holds them; a page's scale goes
+// into them, relative to the tile's largest (exact where it is a power of two, as the
+// framework's writes make it, else a rounding to 11 bits of the scale and one of the
+// product; what is 2^-31 of the tile's largest becomes 0), a token's scale into the score's column
 // (keys) or, rounded to fp16, into the value. q in fp16, scaled by a power of two that
 // brings its head's largest element into [2^8, 2^9): exact down to 2^-25 of that, below
 // that off by up to 2^-33. A bf16 cache: q, k and v as they are, the weights rounded to
@@ -85,7 +86,7 @@ constexpr float kNewWeight = 7.0f;         // and of a tile's largest when M is 
 constexpr int kItemCost = 4;
 constexpr int kLeastWork = 4;
 
-constexpr int kLeastExponent = -64;        // scales below 2^-64 count as that (sums end at 2^128)
+constexpr int kLeastExponent = -64;        // E and F as of scales of 2^-64 at least (sums end at 2^128)
 
 enum Kind { kPageScales = 0, kTokenScales = 1, kBf16 = 2 };
 enum Mode { kOne = 0, kTilesEach = 1, kRowsEach = 2 };
@@ -1008,17 +1009,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         // the largest codes (448) times what is left of the scales: below 2^15, or 2^16
         e = e == none || KIND == kTokenScales ? 0 : e - 6;
         f = f == none ? 0 : f - 6;
-        auto pair = [](int x) -> uint32_t {   // 2^x as an fp16 pair (0 below fp16)
-          if (x < -24) return 0u;
-          const __half h = __float2half_rn(power(x));
-          return (uint32_t)*reinterpret_cast<const uint16_t*>(&h) * 0x10001u;
-        };
-        if (KIND == kTokenScales)
-          factor = __float_as_uint(keys ? 1.f : ve == none ? 0.f : vs * power(-f));
-        else if (keys)
-          factor = ke == none ? 0u : pair(ke - e);
-        else
-          factor = ve == none ? 0u : pair(ve - f);
+        // (a scale of 0 and one of NaN stay what they are)
+        const float x = keys ? (KIND == kTokenScales ? 1.f : ks * power(-e)) : vs * power(-f);
+        const __half h = __float2half_rn(x);
+        factor = KIND == kTokenScales
+                     ? __float_as_uint(x)
+                     : (uint32_t)*reinterpret_cast<const uint16_t*>(&h) * 0x10001u;
       }
       if (keys) {
         Side& side = sh.side[tile & (kSides - 1)];

@@ -86,3 +86,50 @@ def test_nan_of_the_cache_reaches_every_row_that_sees_it(kind, which):
         others[rows] = False
         assert torch.equal(out[others], clean[0][others])
         assert torch.equal(lse[others], clean[1][others])
+
+
+# ---------------------------------------------------------------------------
+# page scales that are no powers of two
+# ---------------------------------------------------------------------------
+def bounds(cache, q, table, lengths, news, score=0.0, value=0.0, weight=2.0 ** -11, window=0):
+    """The oracle's out and lse, with what attention of many tokens may be off from them
+    over an e4m3 cache: as in test_gpu_prompt_attention, with every product of q and a key off by
+    `score` of it more, and every value by `value` of it."""
+    offsets = np.concatenate([[0], np.cumsum(news)])
+    kc, vc, ks, vs = host(cache)
+    d, n = cache.head_dim, max(max(lengths), 1)
+    ref, lse, spread, reach, mass = oracle.prompt_attention_ref(
+        values(q), kc, vc, ks, vs, table, lengths, offsets,
+        np.float32(d ** -0.5).astype(np.float64), window)
+    e = ((2 * (d + 8) + 4) * U32 + 2.0 ** -18 + score) * reach
+    rel = np.expm1(2 * e) + 2 * n * U32 + weight + value
+    tol = HALF_BF16 * np.abs(ref) + rel[..., None] * spread + 2.0 ** -32 * mass
+    lse_tol = e + 2 * n * U32 + 4 * U32 * (1 + np.abs(np.where(np.isneginf(lse), 0, lse)))
+    return ref, lse, tol, lse_tol
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_page_scales_that_are_no_powers_of_two(d):
+    """A caller's own scales: every operator takes them as they are. In the prompt's attention a
+    scale is rounded to fp16 and its product with a code once more: 2^-11 twice."""
+    lengths, news = [300, 70, 2000], [120, 70, 9]
+    cache, q, table = prompt_case(d, lengths, news, 6, 2, d, 32, "e4m3_page")
+    for s in (cache.k_scale, cache.v_scale):
+        s *= 1 + torch.rand(s.shape, device="cuda")
+    t, n = torch.from_numpy(table).cuda(), ints(lengths)
+    ends = np.concatenate([[0], np.cumsum(news)])
+    out, lse = cache.attend_prompt(q, ints(ends.tolist()), t, n, return_lse=True)
+    twice = 2.0 ** -10 + 2.0 ** -22
+    ref, ref_lse, tol, lse_tol = bounds(cache, q, table, lengths, news, twice, twice)
+    assert np.all(np.abs(values(out) - ref) <= tol)
+    assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= lse_tol)
+    # one token a request: the last row of each
+    last = torch.from_numpy(ends[1:] - 1).cuda()
+    one, one_lse = cache.attend(q[last], t, n, return_lse=True)
+    at = ends[1:] - 1
+    assert np.all(np.abs(values(one) - ref[at]) <= tol[at])
+    assert np.all(np.abs(one_lse.cpu().numpy() - ref_lse[at]) <= lse_tol[at])
+    k, _ = cache.read(t, ints([0, 300, 370, 2370]), 2370)
+    kc, _, ks, _ = host(cache)
+    want, _ = oracle.cache_rows_ref(kc, ks, table[0], range(300))
+    assert np.array_equal(values(k)[:300], oracle.bf16_round(want))
