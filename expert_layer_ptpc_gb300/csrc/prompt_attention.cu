@@ -18,8 +18,8 @@
 // What the tensor cores multiply: e4m3 codes in fp16, which holds them; a page's scale goes
 // into them, relative to the tile's largest (exact where it is a power of two, as the
 // framework's writes make it, else a rounding to 11 bits of the scale and one of the
-// product; what is 2^-31 of the tile's largest becomes 0), a token's scale into the score's column
-// (keys) or, rounded to fp16, into the value. q in fp16, scaled by a power of two that
+// product; what is 2^-31 of the tile's largest becomes 0), a token's scale, relative to the
+// largest too, into the score's column (keys) or, rounded to fp16, into the value. q in fp16, scaled by a power of two that
 // brings its head's largest element into [2^8, 2^9): exact down to 2^-25 of that, below
 // that off by up to 2^-33. A bf16 cache: q, k and v as they are, the weights rounded to
 // bf16 (8 bits): the values' own products have no more, and a second product for the
@@ -172,7 +172,7 @@ struct Shared {
   uint32_t tmem;
   int abort;
   Side side[kSides];
-  alignas(16) float key_scale[kSides][128];   // token scales, read as float4
+  alignas(16) float key_scale[kSides][128];   // token scales times 2^-E, read as float4
   float row_scale[256];
   int maxima[2][2][kLoadWarps][2];   // of keys' loaders and values'
   int2 request[kRequests + 1];       // (first row, length)
@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           f = max(f, maxima[i][1]);
         }
         // the largest codes (448) times what is left of the scales: below 2^15, or 2^16
-        e = e == none || KIND == kTokenScales ? 0 : e - 6;
+        e = e == none ? 0 : e - 6;
         f = f == none ? 0 : f - 6;
         // (a scale of 0 and one of NaN stay what they are)
         const float x = keys ? (KIND == kTokenScales ? 1.f : ks * power(-e)) : vs * power(-f);
@@ -1026,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           }
         }
         if (KIND == kTokenScales && lane < kMine)
-          sh.key_scale[tile & (kSides - 1)][w * kMine + lane] = ks;
+          sh.key_scale[tile & (kSides - 1)][w * kMine + lane] = ks * power(-e);
       }
 
       const uint32_t to = stages + stage * S::kTileBytes;

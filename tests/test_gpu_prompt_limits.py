@@ -133,3 +133,21 @@ def test_page_scales_that_are_no_powers_of_two(d):
     kc, _, ks, _ = host(cache)
     want, _ = oracle.cache_rows_ref(kc, ks, table[0], range(300))
     assert np.array_equal(values(k)[:300], oracle.bf16_round(want))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_large_keys_and_small_queries(kind):
+    """Keys near the end of bf16's range, and queries as far below one: scores like any others."""
+    lengths, news, d, size = [300, 40], [90, 40], 128, 16
+    cache, q, table = prompt_case(8, lengths, news, 4, 2, d, size, "bf16")
+    far = 2.0 ** 112
+    cache.k *= far
+    assert torch.isfinite(cache.k.float()).all()
+    q /= far
+    if kind != "bf16":
+        coded = attention.PagedKVCache.empty(cache.pages, 2, size, d, dtype=kind)
+        coded.write(cache.k.transpose(1, 2).reshape(-1, 2, d),
+                    cache.v.transpose(1, 2).reshape(-1, 2, d),
+                    torch.arange(cache.pages * size, dtype=torch.int32, device="cuda"))
+        cache = coded
+    check_prompt(cache, q, table, lengths, news, kind=kind)
