@@ -833,86 +833,6 @@ MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int bat
  *     [2^8, 2^9): off by up to 2^-33 of that element. Weights in fp16: off by up to 2^-11
  *     of each, or 2^-32 of the row's largest where that is more. Scales below 2^-85 lose
  *     bits.
- *   - bf16 cache: q, k and v exactly; each weight as the sum of two bf16 numbers
- *     (16 bits).
- * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned
- *         pointers, q_heads not a multiple of heads, scale not finite, batch
- *         < 0, max_pages < 0, table_stride < max_pages, window < 0),
- *         MOE_ERR_UNSUPPORTED (batch > 65535, q_heads > 65535, or tables of
- *         more than about 2^31 units of 64 tokens and 16 to 32 query heads in
- *         all), MOE_ERR_WORKSPACE. batch == 0 is a no-op.
- */
-MOE_API size_t moe_paged_attention_workspace_size(const moe_kv_cache* cache, int batch,
-                                                  int q_heads);
-MOE_API int moe_paged_attention(const moe_kv_cache* cache, const uint16_t* q,
-                                int64_t q_stride, int batch, int q_heads,
-                                const int32_t* block_table, int64_t table_stride,
-                                int max_pages, const int32_t* lengths, float scale,
-                                int window, uint16_t* out, float* lse, void* ws,
-                                size_t ws_bytes, moe_stream_t stream);
-
-/*
- * moe_kv_plan - the block tables and slot maps of a step, from how many tokens the
- * requests hold and get. Pages come from a stack of free ones and go back to it, all
- * on the device.
- *   state [batch + 1]: the tokens h_b that request b holds, then the number of
- *   pages on the stack; new_tokens [batch]: n_b more tokens, or a negative number
- *   for a request that leaves; block_table [batch, max_pages] with table_stride
- *   entries between rows; stack [pages], the next page to be taken last.
- *   1. The pages of the requests that leave (entries of their ceil(h_b / page_size)
- *      first that lie in [0, pages)) go onto the stack, in order of request and
- *      entry. F pages are then free.
- *   2. Request b needs ceil((h_b + n_b) / page_size) - ceil(h_b / page_size) pages. It is
- *      served when n_b >= 0, its tokens fit max_pages pages and an int32, and the pages
- *      and the tokens of all such requests up to it are at most F and `rows`.
- *   3. The k-th page that the served requests take, in order, is stack[F - 1 - k];
- *      it becomes the next entry of its request's table.
- *   offsets [batch + 1]: the rows of each request in the step; slots [rows] and positions
- *   [axes, rows]: of each row's token (its place in the context on every axis); -1 and
- *   0 for rows from offsets[batch] on. state_out [batch + 1]: h_b + n_b of a served
- *   request, 0 of one that leaves, else h_b, then the free pages left. refused [1]:
- *   requests with n_b > 0 that were not served. All int32.
- *   block_table (entries of pages taken) and stack (from its end on) are written in
- *   place, state is not: the call can be repeated. The outputs must not overlap the
- *   inputs. Entries outside [0, pages) on the stack give slots of -1.
- * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, batch, pages, page_size or
- *         max_pages < 1, table_stride < max_pages, rows < 0, axes outside 1..8),
- *         MOE_ERR_UNSUPPORTED (batch > 4096, page_size not a power of two <= 1024, 2^31
- *         or more slots).
- */
-MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int batch,
-                        int32_t* block_table, int64_t table_stride, int max_pages,
-                        int32_t* stack, int pages, int page_size, int rows, int axes,
-                        int32_t* offsets, int32_t* slots, int32_t* positions,
-                        int32_t* state_out, int32_t* refused, moe_stream_t stream);
-
-/*
- * moe_prompt_attention - attention of many new tokens per context over its cached keys
- * and values. Row r of context b (offsets[b] <= r < offsets[b + 1]) is token
- *   i = lengths[b] - (offsets[b + 1] - r)
- * of that context, and out and lse of its heads are those of moe_paged_attention for a
- * context of i + 1 tokens: it sees its own token and those before it, with window > 0 the
- * last `window` of them. A row with i < 0 sees nothing.
- *   q [rows, q_heads, head_dim] bf16 with q_stride elements between tokens; offsets
- *   [batch + 1] int32, ascending from 0, to at most `rows`; block_table and lengths as
- *   for moe_paged_attention (the new tokens' keys and values are in the cache already
- *   and counted; tokens from 2^31 - 256 on are absent); out like q with out_stride, not
- *   overlapping q; lse [rows, q_heads] fp32 or NULL. Rows from offsets[batch] on are
- *   left as they are.
- *   Slots that no context covers have no influence, whatever they hold; a context's
- *   keys and values from the first token on that any of its rows sees must be finite.
- *   (A NaN there, or in a row of q, shows as NaN in the rows that it reaches, and never as
- *   a row that sees nothing.)
- *   ws: device workspace of moe_prompt_attention_workspace_size bytes, as for
- *   moe_paged_attention.
- *   Sums, maxima and accumulators are fp32; results do not depend on timing. What the
- *   tensor cores multiply has fewer bits:
- *   - e4m3 caches: codes in fp16, exactly; a page's scale as a power of two (a code
- *     times a scale 2^-31 of the largest of its 128 tokens, 64 with head_dim 256, counts as 0), a
- *     token's scale of a value rounded into it (2^-11). q in fp16, its head's largest
- *     element scaled into [2^8, 2^9): off by up to 2^-33 of that element. Weights in fp16:
- *     off by up to 2^-11 of each, or 2^-32 of the row's largest where that is more. Scales
- *     below 2^-64 count as that.
  *   - bf16 cache: q, k and v exactly; weights in bf16, off by up to 2^-8 of each.
  *   Every wait inside is bounded; one that runs out is reported by moe_device_status().
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned pointers, q_heads
