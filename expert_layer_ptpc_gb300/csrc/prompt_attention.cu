@@ -85,6 +85,10 @@ constexpr float kNewWeight = 7.0f;         // and of a tile's largest when M is 
 // CTA is given.
 constexpr int kItemCost = 4;
 constexpr int kLeastWork = 4;
+// What a wait is given, beside kWaitLimitNs, for each 128 tokens of the longest run that a
+// CTA can have: its halves can be a ring of segments apart, so that one waits for most of the
+// run (2 to 3 us each).
+constexpr double kWaitNsOfTile = 20000.0;
 
 constexpr int kLeastExponent = -64;        // E and F as of scales of 2^-64 at least (sums end at 2^128)
 
@@ -106,6 +110,7 @@ struct Args {
   float2* stats;            // [2 kWorkers][rows of an item] (M, l)
   float* parts;             // [2 kWorkers][D / 4][rows of an item][4]
   unsigned* err;
+  unsigned long long wait_ns;   // after which a wait has run out
 };
 
 // What a CTA left of items that it shares with others: of its first one, begun by an
@@ -402,7 +407,7 @@ __device__ __forceinline__ bool next_of(const Args& a, const Shared& sh, Walk& w
 
 // Bounded wait of a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared& sh,
-                                          unsigned* err, unsigned code) {
+                                          const Args& a, unsigned code) {
   const uint32_t at = smem_u32(bar);
   if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
   const unsigned long long t0 = global_timer_ns();
@@ -410,9 +415,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared
     if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
     if ((spin & 63u) == 63u) {
       bool bail = *reinterpret_cast<volatile int*>(&sh.abort) != 0;
-      if (!bail && global_timer_ns() - t0 > kWaitLimitNs) {
+      if (!bail && global_timer_ns() - t0 > a.wait_ns) {
         *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-        atomicOr(err, code);
+        atomicOr(a.err, code);
         bail = true;
       }
       if (__any_sync(0xffffffffu, bail)) return false;
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
   // The segments, from the warp that hands them out: number n is there (false: the run has
   // ended, or a wait has run out) and, when a role is done with it, free.
   auto take = [&](int n) -> bool {
-    return warp_wait(&sh.seg_full[n % kRing], (n / kRing) & 1, sh, a.err, kErrTimeoutSched) &&
+    return warp_wait(&sh.seg_full[n % kRing], (n / kRing) & 1, sh, a, kErrTimeoutSched) &&
            sh.ring[n % kRing].units >= 0;
   };
   auto release = [&](int n) { warp_arrive(&sh.seg_empty[n % kRing]); };
@@ -683,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         for (int i = tile0; ok && i < tiles; i += step) {
           const int turn = S::kSlots == 2 ? i & 1 : 0, slot = me + turn;
           const uint32_t s_at = tmem + lanes + slot * kTile;
-          ok = warp_wait(&sh.s_full[slot], (s_phase >> turn) & 1u, sh, a.err,
+          ok = warp_wait(&sh.s_full[slot], (s_phase >> turn) & 1u, sh, a,
                          kErrTimeoutEpilogue);
           if (!ok) break;
           s_phase ^= 1u << turn;
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           // phase further.
           auto last_products = [&]() -> bool {
             return S::kSlots == 1 || i == tile0 ||
-                   warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
+                   warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a, kErrTimeoutEpilogue);
           };
           if (!works) {
             ok = last_products();
@@ -816,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       if (running && has_q(sh.ring[(number + 1) % kRing])) load_q(sh.ring[(number + 1) % kRing]);
       if (mine) {
         // the last products (o_phase has moved past them)
-        ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a.err, kErrTimeoutEpilogue);
+        ok = warp_wait(&sh.o_full[me], o_phase ^ 1u, sh, a, kErrTimeoutEpilogue);
         if (!ok) break;
         tc_fence_after_sync();
       }
@@ -998,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         }
         uint64_t* const maxed = &sh.maxed[keys ? 0 : 1];
         warp_arrive(maxed);
-        ok = warp_wait(maxed, tile & 1, sh, a.err, kErrTimeoutProducer);
+        ok = warp_wait(maxed, tile & 1, sh, a, kErrTimeoutProducer);
         if (!ok) break;
         e = f = none;
 #pragma unroll
@@ -1042,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
       follows[kAhead - 1] = asked;
       then[kAhead - 1] = resolve();
       ask();
-      ok = warp_wait(&empty[stage], phase, sh, a.err, kErrTimeoutProducer);
+      ok = warp_wait(&empty[stage], phase, sh, a, kErrTimeoutProducer);
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -1111,12 +1116,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         auto scores = [&](int t) -> bool {
           const int stream = stream_of(t), slot = slot_of(t);
           if (begins(t)) {   // the stream's rows of q
-            if (!warp_wait(&sh.q_full[stream], (q_phase >> stream) & 1u, sh, a.err,
+            if (!warp_wait(&sh.q_full[stream], (q_phase >> stream) & 1u, sh, a,
                            kErrTimeoutMma))
               return false;
             q_phase ^= 1u << stream;
           }
-          if (opens(t) && !warp_wait(&sh.k_full[k_stage], k_phase, sh, a.err, kErrTimeoutMma))
+          if (opens(t) && !warp_wait(&sh.k_full[k_stage], k_phase, sh, a, kErrTimeoutMma))
             return false;
           tc_fence_after_sync();
           const uint32_t d = uniform(tmem + slot * kTile);
@@ -1141,16 +1146,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
         for (int t = 0; ok && t < tasks; ++t) {
           const int stream = stream_of(t), slot = slot_of(t);
           if (begins(t)) {   // O: the last segment's has been read
-            ok = warp_wait(&sh.o_empty[stream], (oe_phase >> stream) & 1u, sh, a.err,
+            ok = warp_wait(&sh.o_empty[stream], (oe_phase >> stream) & 1u, sh, a,
                            kErrTimeoutMma);
             if (!ok) break;
             oe_phase ^= 1u << stream;
           }
           if (opens(t)) {
-            ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a.err, kErrTimeoutMma);
+            ok = warp_wait(&sh.v_full[v_stage], v_phase, sh, a, kErrTimeoutMma);
             if (!ok) break;
           }
-          ok = warp_wait(&sh.p_full[slot], (p_phase >> slot) & 1u, sh, a.err, kErrTimeoutMma);
+          ok = warp_wait(&sh.p_full[slot], (p_phase >> slot) & 1u, sh, a, kErrTimeoutMma);
           if (!ok) break;
           p_phase ^= 1u << slot;
           tc_fence_after_sync();
@@ -1206,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
           }
         }
         if (!more) s.units = -1;
-        if (!warp_wait(&sh.seg_empty[n % kRing], ((n / kRing) & 1) ^ 1, sh, a.err,
+        if (!warp_wait(&sh.seg_empty[n % kRing], ((n / kRing) & 1) ^ 1, sh, a,
                        kErrTimeoutSched))
           break;
         if (lane == 0) sh.ring[n % kRing] = s;
@@ -1372,9 +1377,10 @@ int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_str
   // overlap, which the contract rules out, could add up to 2^16 times as much)
   const double items = (double)rows * q_heads / 128 + (double)batch * c.heads;
   const double room = std::min<double>((double)c.max_pages * (1 << c.page_shift), 0x1p31);
-  if (items * (room * group / 128 + (double)rows * group / 128 + 8.0 * group) > 0x1p46)
-    return -2;
+  const double work = items * (room * group / 128 + (double)rows * group / 128 + 8.0 * group);
+  if (work > 0x1p46) return -2;
   Args a{};
+  a.wait_ns = kWaitLimitNs + (unsigned long long)(work / group / kWorkers * kWaitNsOfTile);
   a.c = c;
   a.q = q;
   a.q_stride = q_stride;

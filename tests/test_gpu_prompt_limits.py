@@ -151,3 +151,54 @@ def test_large_keys_and_small_queries(kind):
                     torch.arange(cache.pages * size, dtype=torch.int32, device="cuda"))
         cache = coded
     check_prompt(cache, q, table, lengths, news, kind=kind)
+
+
+# ---------------------------------------------------------------------------
+# segments that take long
+# ---------------------------------------------------------------------------
+def test_a_role_waits_as_long_as_the_others_work():
+    """Items of one row over 20 million tokens each, and behind eight of them on every CTA items of
+    more than 128 rows: the second half of the softmax warps waits for those from the start on, for
+    over a second."""
+    ctas, heads, d, size, pages = 152, 8, 64, 1024, 20000
+    lengths, news = [pages * size, 129] * ctas, [1, 129] * ctas
+    cache, q, _ = prompt_case(4, [2 * size], news, heads, heads, d, size, "e4m3_page")
+    table = torch.zeros((2 * ctas, pages), dtype=torch.int32, device="cuda")
+    offsets = ints(np.concatenate([[0], np.cumsum(news)]).tolist())
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    cache.attend_prompt(q, offsets, table, ints(lengths), out=out, lse=lse)
+    end.record()
+    assert binding.moe_device_status() == (0, 0)
+    assert start.elapsed_time(end) > 1100
+    # every page is the same one: the attention over it, and its sum that many times
+    first = offsets[:-1].long()[::2]
+    once, once_lse = cache.attend(q[first], table[::2, :1].contiguous(), ints([size] * ctas),
+                                  return_lse=True)
+    tiles = pages * size // 128
+    # fp32 sums of a tile at a time, and of 16 tokens at a time (truncated): 2 u a step
+    assert np.all(np.abs((lse[first] - once_lse).cpu().numpy() - np.log(pages)) <=
+                  4 * tiles * U32 + 1e-4)
+    kc, vc, ks, vs = host(cache)
+    spread = np.abs(oracle.e4m3_decode(vc[0])).max(1) * vs[0][:, None]
+    assert np.all(np.abs(values(out[first]) - values(once)) <=
+                  (2 * 8 * tiles * U32 + 2.0 ** -10) * spread + 2 * HALF_BF16 * np.abs(values(once)))
+    for b in range(0, ctas, 37):
+        at = slice(int(offsets[2 * b + 1]), int(offsets[2 * b + 2]))
+        check_prompt(Given(cache, out[at], lse[at]), q[at], np.zeros((1, 1), np.int32), [129], [129],
+                     kind="e4m3_page")
+
+
+class Given:
+    """A cache with results that are there already."""
+
+    def __init__(self, cache, out, lse):
+        self.k, self.v, self.k_scale, self.v_scale = cache.k, cache.v, cache.k_scale, cache.v_scale
+        self.out, self.lse = out, lse
+
+    def attend_prompt(self, q, *call, out, lse, **kw):
+        out.copy_(self.out)
+        lse.copy_(self.lse)
+        return out, lse
