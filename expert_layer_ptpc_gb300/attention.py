@@ -230,7 +230,8 @@ class PagedKVCache:
         context b's in rows offsets[b] .. offsets[b + 1], which are the last of its
         lengths[b] tokens (keys and values already written). Each sees the tokens
         of its context up to its own (the last `window` of them when window > 0). Rows
-        from offsets[-1] on are left as they are. scale: default 1 / sqrt(head_dim).
+        from offsets[-1] on are left as they are in `out` and `lse`, and are 0 and -inf in
+        tensors that the call makes. scale: default 1 / sqrt(head_dim).
         Returns out, or (out, lse) with `return_lse` or `lse`."""
         if scale is None:
             scale = self._scale

@@ -112,6 +112,8 @@ _SIGNATURES = {
     "moe_prompt_attention_workspace_size": (_SZ, [_P, _I]),
     "moe_prompt_attention": (_I, [_P, _P, _I64, _I, _I, _P, _P, _I64, _I, _P, _I, ctypes.c_float,
                                   _I, _P, _I64, _P, _P, _SZ, _P]),
+    "moe_prompt_attention_padded": (_I, [_P, _P, _I64, _I, _I, _P, _P, _I64, _I, _P, _I,
+                                         ctypes.c_float, _I, _P, _I64, _P, _P, _SZ, _P]),
 }
 
 MOE_SCALE_PTPC, MOE_SCALE_SUB512, MOE_SCALE_BLOCK128 = 0, 1, 2
@@ -682,6 +684,15 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _fill(t, value, stream):
+    """Fill t on the stream the kernel will run on."""
+    if stream is None:
+        t.fill_(value)
+        return
+    with torch.cuda.stream(stream):
+        t.fill_(value)
+
+
 def _need_heads(t, heads, head_dim, name, index):
     """A [T, heads, head_dim] bf16 tensor whose tokens may be strided (a slice
     of a wider projection) on GPU `index`; returns the token stride."""
@@ -927,9 +938,9 @@ def moe_prompt_attention(cache, q, offsets, block_table, lengths, scale, window=
     """Attention of the new tokens of each context: q [rows, q_heads, head_dim] bf16,
     rows offsets[b]..offsets[b + 1] the last tokens of context b; returns out, of q's
     shape, or (out, lse) with return_lse. `lse`: optional [rows, q_heads] fp32 tensor
-    that receives the log of the sums. Rows from offsets[-1] on are left as they are.
-    ws: a contiguous tensor of at least moe_prompt_attention_workspace_size bytes
-    (None: a new one)."""
+    that receives the log of the sums. Rows from offsets[-1] on are left as they are in
+    the caller's tensors, and are 0 in a new out and -inf in a new lse. ws: a contiguous
+    tensor of at least moe_prompt_attention_workspace_size bytes (None: a new one)."""
     rows, hq, d = q.shape
     if not -_INT_MAX <= window <= _INT_MAX:
         raise ValueError(f"window must be at most {_INT_MAX}, got {window}")
@@ -941,8 +952,14 @@ def moe_prompt_attention(cache, q, offsets, block_table, lengths, scale, window=
     stride, pages = _need_table(block_table, batch, index)
     if offsets.numel() != batch + 1:
         raise ValueError(f"offsets must have {batch + 1} entries, got {offsets.numel()}")
-    if out is None:
+    lib, new_out = _lib or load_library(), out is None
+    entry = lib.moe_prompt_attention
+    if new_out:
         out, out_stride = _empty((rows, hq, d), torch.bfloat16, q.device, stream), hq * d
+        if lse is None:      # all outputs are new: the kernels see to the padding
+            entry = lib.moe_prompt_attention_padded
+        else:
+            _fill(out, 0.0, stream)
     else:
         out_stride = _need_heads(out, hq, d, "out", index)
         if out.shape[0] != rows:
@@ -955,12 +972,14 @@ def moe_prompt_attention(cache, q, offsets, block_table, lengths, scale, window=
             raise ValueError(f"lse must be {(rows, hq)}, got {tuple(lse.shape)}")
     elif return_lse:
         lse = _empty((rows, hq), torch.float32, q.device, stream)
+        if not new_out:
+            _fill(lse, float("-inf"), stream)
     if ws is None:
         need = moe_prompt_attention_workspace_size(cache, hq)
         ws = _empty(max(need, 1), torch.uint8, q.device, stream)
     elif ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous CUDA tensor on GPU {index}")
-    status = (_lib or load_library()).moe_prompt_attention(
+    status = entry(
         ctypes.byref(cache), q.data_ptr(), q_stride, rows, hq, offsets.data_ptr(),
         block_table.data_ptr(), stride, pages, lengths.data_ptr(), batch, scale, window,
         out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), ws.data_ptr(),

@@ -110,6 +110,32 @@ void set_plan(RotaryArgs* a, const moe_rotary_plan& p, const int32_t* positions)
 
 constexpr int kMaxTokenElements = 65536;
 
+// `pad`: whether rows from offsets[batch] on are made those that see nothing.
+int prompt_attention(bool pad, const moe_kv_cache* cache, const uint16_t* q, int64_t q_stride,
+                     int rows, int q_heads, const int32_t* offsets, const int32_t* block_table,
+                     int64_t table_stride, int max_pages, const int32_t* lengths, int batch,
+                     float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
+                     void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (rows < 0 || batch < 0 || q_heads < 1 || window < 0 || !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (const int st = check_cache(cache)) return st;
+  if (q_heads % cache->heads != 0) return MOE_ERR_INVALID_ARG;
+  if (batch > 65535 || q_heads > 65535 || (int64_t)rows * q_heads >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (rows == 0 || (batch == 0 && !pad)) return MOE_OK;
+  if (batch == 0) max_pages = 0;   // all rows are padding
+  if (const int st = check_table(block_table, table_stride, max_pages)) return st;
+  if (!good_heads(q, q_stride, q_heads, cache->head_dim) || !good4(offsets) ||
+      (batch > 0 && !good4(lengths)) || !good_heads(out, out_stride, q_heads, cache->head_dim) ||
+      (lse != nullptr && !good4(lse)))
+    return MOE_ERR_INVALID_ARG;
+  if (!good16(ws) || ws_bytes < prompt_attention_ws_bytes(cache->heads, cache->head_dim, q_heads))
+    return MOE_ERR_WORKSPACE;
+  return launch_prompt_attention(view_of(*cache, block_table, table_stride, max_pages), q, q_stride,
+                                 rows, q_heads, offsets, lengths, batch, scale, window, out,
+                                 out_stride, lse, pad, ws, stream);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -297,22 +323,20 @@ int moe_prompt_attention(const moe_kv_cache* cache, const uint16_t* q, int64_t q
                          int64_t table_stride, int max_pages, const int32_t* lengths, int batch,
                          float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
                          void* ws, size_t ws_bytes, moe_stream_t stream) {
-  if (rows < 0 || batch < 0 || q_heads < 1 || window < 0 || !std::isfinite(scale))
-    return MOE_ERR_INVALID_ARG;
-  if (const int st = check_cache(cache)) return st;
-  if (q_heads % cache->heads != 0) return MOE_ERR_INVALID_ARG;
-  if (batch > 65535 || q_heads > 65535 || (int64_t)rows * q_heads >= (int64_t(1) << 31))
-    return MOE_ERR_UNSUPPORTED;
-  if (rows == 0 || batch == 0) return MOE_OK;
-  if (const int st = check_table(block_table, table_stride, max_pages)) return st;
-  if (!good_heads(q, q_stride, q_heads, cache->head_dim) || !good4(offsets) || !good4(lengths) ||
-      !good_heads(out, out_stride, q_heads, cache->head_dim) || (lse != nullptr && !good4(lse)))
-    return MOE_ERR_INVALID_ARG;
-  if (!good16(ws) || ws_bytes < prompt_attention_ws_bytes(cache->heads, cache->head_dim, q_heads))
-    return MOE_ERR_WORKSPACE;
-  return launch_prompt_attention(view_of(*cache, block_table, table_stride, max_pages), q, q_stride,
-                                 rows, q_heads, offsets, lengths, batch, scale, window, out,
-                                 out_stride, lse, ws, stream);
+  return prompt_attention(false, cache, q, q_stride, rows, q_heads, offsets, block_table,
+                          table_stride, max_pages, lengths, batch, scale, window, out, out_stride,
+                          lse, ws, ws_bytes, stream);
+}
+
+int moe_prompt_attention_padded(const moe_kv_cache* cache, const uint16_t* q, int64_t q_stride,
+                                int rows, int q_heads, const int32_t* offsets,
+                                const int32_t* block_table, int64_t table_stride, int max_pages,
+                                const int32_t* lengths, int batch, float scale, int window,
+                                uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                size_t ws_bytes, moe_stream_t stream) {
+  return prompt_attention(true, cache, q, q_stride, rows, q_heads, offsets, block_table,
+                          table_stride, max_pages, lengths, batch, scale, window, out, out_stride,
+                          lse, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -69,6 +69,6 @@ size_t prompt_attention_ws_bytes(int heads, int head_dim, int q_heads);
 int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int rows,
                             int q_heads, const int32_t* offsets, const int32_t* lengths, int batch,
                             float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
-                            void* ws, cudaStream_t stream);
+                            bool pad, void* ws, cudaStream_t stream);
 
 }  // namespace moe

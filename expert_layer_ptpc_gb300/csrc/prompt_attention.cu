@@ -1227,13 +1227,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const Arg
 }
 
 // Joins the pieces of the items that several CTAs share: the one that CTA blockIdx.x
-// began, 32 of its rows a block, four elements of a row a thread at a time.
+// began, 32 of its rows a block, four elements of a row a thread at a time. PAD: before that, all
+// threads together make the rows behind the last context's those that see nothing.
 constexpr int kJoinThreads = 256;
 
-template <int KIND, int D>
+template <int KIND, int D, bool PAD>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a, int workers) {
   constexpr int kRows = Shape<KIND, D>::kRows;
   pdl_wait();
+  if (PAD) {
+    const int from = min(max(a.offsets[a.batch], 0), a.rows);
+    const int per = a.q_heads * (D / 8);   // 16-byte units of a token
+    const int64_t me = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * kJoinThreads + threadIdx.x;
+    const int64_t all = (int64_t)gridDim.x * gridDim.y * kJoinThreads;
+    for (int64_t i = me; i < (int64_t)(a.rows - from) * per; i += all)
+      *reinterpret_cast<uint4*>(a.out + (from + i / per) * a.out_stride + (i % per) * 8) =
+          make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse != nullptr)
+      for (int64_t i = (int64_t)from * a.q_heads + me; i < (int64_t)a.rows * a.q_heads; i += all)
+        a.lse[i] = -INFINITY;
+  }
   const int w = blockIdx.x;
   const Record rec = a.records[w];
   if (rec.tail.x < 0) return;
@@ -1335,7 +1348,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const Args a,
 }
 
 template <int KIND, int D>
-int launch(const Args& a, cudaStream_t stream) {
+int launch(const Args& a, bool pad, cudaStream_t stream) {
   using S = Shape<KIND, D>;
   // the opt-in to more than 48 KB of shared memory, once per device
   static std::atomic<uint64_t> opted{0};
@@ -1353,7 +1366,8 @@ int launch(const Args& a, cudaStream_t stream) {
                                 prompt_attention_kernel<KIND, D>, a);
   if (e != cudaSuccess) return -3;
   e = launch_kernel(true, dim3(kWorkers, S::kRows / 32), dim3(kJoinThreads), 0, stream,
-                    prompt_join_kernel<KIND, D>, a, kWorkers);
+                    pad ? prompt_join_kernel<KIND, D, true> : prompt_join_kernel<KIND, D, false>, a,
+                    kWorkers);
   return e == cudaSuccess ? 0 : -3;
 }
 
@@ -1371,7 +1385,7 @@ size_t prompt_attention_ws_bytes(int, int head_dim, int) {
 int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_stride, int rows,
                             int q_heads, const int32_t* offsets, const int32_t* lengths, int batch,
                             float scale, int window, uint16_t* out, int64_t out_stride, float* lse,
-                            void* ws, cudaStream_t stream) {
+                            bool pad, void* ws, cudaStream_t stream) {
   const int group = q_heads / c.heads;
   // the weights' sum over all items, times the CTAs, stays within 64 bits (contexts that
   // overlap, which the contract rules out, could add up to 2^16 times as much)
@@ -1405,16 +1419,16 @@ int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_str
   if (a.err == nullptr) return -3;
   const int kind = !c.e4m3 ? kBf16 : c.scale_shift > 0 ? kPageScales : kTokenScales;
   if (c.head_dim == 64)
-    return kind == kBf16         ? launch<kBf16, 64>(a, stream)
-           : kind == kPageScales ? launch<kPageScales, 64>(a, stream)
-                                 : launch<kTokenScales, 64>(a, stream);
+    return kind == kBf16         ? launch<kBf16, 64>(a, pad, stream)
+           : kind == kPageScales ? launch<kPageScales, 64>(a, pad, stream)
+                                 : launch<kTokenScales, 64>(a, pad, stream);
   if (c.head_dim == 128)
-    return kind == kBf16         ? launch<kBf16, 128>(a, stream)
-           : kind == kPageScales ? launch<kPageScales, 128>(a, stream)
-                                 : launch<kTokenScales, 128>(a, stream);
-  return kind == kBf16         ? launch<kBf16, 256>(a, stream)
-         : kind == kPageScales ? launch<kPageScales, 256>(a, stream)
-                               : launch<kTokenScales, 256>(a, stream);
+    return kind == kBf16         ? launch<kBf16, 128>(a, pad, stream)
+           : kind == kPageScales ? launch<kPageScales, 128>(a, pad, stream)
+                                 : launch<kTokenScales, 128>(a, pad, stream);
+  return kind == kBf16         ? launch<kBf16, 256>(a, pad, stream)
+         : kind == kPageScales ? launch<kPageScales, 256>(a, pad, stream)
+                               : launch<kTokenScales, 256>(a, pad, stream);
 }
 
 }  // namespace moe

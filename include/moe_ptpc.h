@@ -853,6 +853,19 @@ MOE_API int moe_prompt_attention(const moe_kv_cache* cache, const uint16_t* q,
                                  uint16_t* out, int64_t out_stride, float* lse, void* ws,
                                  size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * moe_prompt_attention_padded - the same, and rows from offsets[batch] on (all of them with
+ * batch == 0) become those that see nothing, 0 in out and -inf in lse, for outputs whose
+ * every row is read afterwards.
+ */
+MOE_API int moe_prompt_attention_padded(const moe_kv_cache* cache, const uint16_t* q,
+                                        int64_t q_stride, int rows, int q_heads,
+                                        const int32_t* offsets, const int32_t* block_table,
+                                        int64_t table_stride, int max_pages,
+                                        const int32_t* lengths, int batch, float scale, int window,
+                                        uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                        size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

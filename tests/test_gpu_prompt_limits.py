@@ -1,6 +1,8 @@
 """Attention of many new tokens at the ends of its range: NaN, scales of every size, long
 segments of work, and rows of padding."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -202,3 +204,99 @@ class Given:
         out.copy_(self.out)
         lse.copy_(self.lse)
         return out, lse
+
+
+# ---------------------------------------------------------------------------
+# rows of padding
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("streamed", [False, True])
+def test_padding_of_new_outputs(kind, d, streamed):
+    """Rows behind the last context's are zeros, with log-sums of -inf, in tensors that the call
+    makes, whatever their memory held; in the caller's they stay."""
+    lengths, news, pad = [4000, 60, 300], [70, 60, 2], 200
+    cache, q, table = prompt_case(d, lengths, news, 6, 2, d, 32, kind, pad=pad)
+    call = ints([0, 70, 130, 132]), torch.from_numpy(table).cuda(), ints(lengths)
+    rows = len(q)
+    out, lse = check_prompt(cache, q, table, lengths, news, kind=kind)
+    stream = torch.cuda.Stream() if streamed else None
+    torch.cuda.synchronize()
+
+    def poison():       # what the next new tensors of these sizes are made of
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                held = [torch.full((rows, 6, d), float("nan"), dtype=torch.bfloat16,
+                                   device="cuda"),
+                        torch.full((rows, 6), float("nan"), device="cuda")]
+                del held
+
+    def check(new, of, want, behind):
+        torch.cuda.synchronize()
+        if new:
+            assert torch.equal(of[:132], want[:132]) and torch.all(of[132:] == behind)
+        else:
+            assert torch.equal(of, want)
+
+    zero, none = 0.0, float("-inf")
+    poison()
+    check(True, cache.attend_prompt(q, *call, stream=stream), out, zero)
+    poison()
+    got = cache.attend_prompt(q, *call, return_lse=True, stream=stream)
+    check(True, got[0], out, zero)
+    check(True, got[1], lse, none)
+    poison()
+    given = torch.full_like(lse, 7.0)
+    torch.cuda.synchronize()
+    got = cache.attend_prompt(q, *call, lse=given, stream=stream)
+    check(True, got[0], out, zero)
+    check(False, got[1], lse, none)
+    poison()
+    given = torch.full_like(out, 7.0)
+    torch.cuda.synchronize()
+    got = cache.attend_prompt(q, *call, out=given, return_lse=True, stream=stream)
+    check(False, got[0], out, zero)
+    check(True, got[1], lse, none)
+
+
+def test_padding_alone_and_wrong_ends():
+    cache, q, table = prompt_case(2, [40], [40], 4, 2, 64, 16, "bf16")
+    t, n = torch.from_numpy(table).cuda(), ints([40])
+    out, lse = cache.attend_prompt(q, ints([0]), t[:0], ints([]), return_lse=True)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    wide = torch.full((3, 40, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    need = binding.moe_prompt_attention_workspace_size(cache.struct, 4)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for end in (2 ** 31 - 1, -2 ** 31, -1, 41, 40, 0):
+        wide.fill_(3.0)
+        offsets = ints([0, end])
+        assert binding.load_library().moe_prompt_attention_padded(
+            ctypes.byref(cache.struct), q.data_ptr(), 256, 40, 4, offsets.data_ptr(), t.data_ptr(),
+            t.shape[1], t.shape[1], n.data_ptr(), 1, 0.125, 0, wide[1].data_ptr(), 256, None,
+            ws.data_ptr(), need, None) == 0
+        torch.cuda.synchronize()
+        assert torch.all(wide[0] == 3.0) and torch.all(wide[2] == 3.0)
+        if end <= 0:
+            assert torch.all(wide[1] == 0)
+        if end > 40:
+            assert torch.all(wide[1] == 3.0)
+
+
+def test_padding_follows_the_lengths_of_a_captured_step():
+    """A step of fixed size without outputs of the caller's, replayed with other lengths."""
+    cache, q, table = prompt_case(6, [200, 300], [24, 40], 4, 2, 128, 16, "e4m3_page")
+    t, n, o = torch.from_numpy(table).cuda(), ints([200, 300]), ints([0, 24, 64])
+    cache.attend_prompt(q, o, t, n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = cache.attend_prompt(q, o, t, n, return_lse=True)
+    for news, lengths in (([24, 40], [200, 300]), ([1, 1], [9, 300]), ([0, 0], [9, 0]),
+                          ([5, 0], [5, 77]), ([30, 34], [200, 34])):
+        o.copy_(ints([0, news[0], sum(news)]))
+        n.copy_(ints(lengths))
+        graph.replay()
+        end = sum(news)
+        want = [torch.zeros_like(out), torch.full_like(lse, float("-inf"))]
+        cache.attend_prompt(q, o, t, n, out=want[0], lse=want[1])
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        assert torch.all(out[end:] == 0) and torch.all(torch.isneginf(lse[end:]))
