@@ -215,8 +215,11 @@ class PagedKVCache:
                return_lse=False, ws=None, stream=None):
         """Attention of one new token per context: q [batch, q_heads, head_dim]
         bf16 over the first lengths[b] tokens of block_table[b] (the last
-        `window` of them when window > 0). scale: default 1 / sqrt(head_dim).
-        Returns out, or (out, lse) with `return_lse` or `lse`."""
+        `window` of them when window > 0). Row b is context b's, whatever it gets: the
+        rows of a StepPlan are those only where every request got one token, as
+        requests without new tokens have no rows there (attend_prompt takes its offsets).
+        scale: default 1 / sqrt(head_dim). Returns out, or (out, lse) with `return_lse` or
+        `lse`."""
         if scale is None:
             scale = self._scale
         if ws is None:
@@ -244,7 +247,8 @@ class PagedKVCache:
 
 class StepPlan:
     """What one step needs to know, all int32 on the GPU: `offsets` [batch + 1] of the
-    requests' rows, `lengths` [batch] of their contexts with the new tokens, `slots`
+    requests' rows (none for a request that leaves, waits or has no new tokens: the rows of
+    those behind it move up), `lengths` [batch] of their contexts with the new tokens, `slots`
     [rows] and `positions` [axes, rows] of the rows (-1 and 0 for rows behind the
     last), `refused` [1], the number of requests that wait for pages or rows, and
     `state`, the pool's after the step."""
