@@ -269,7 +269,16 @@ class PagePool:
     pages in order; `stack` [pages] int32, the free pages, the next to be handed out
     last; `state` [batch + 1] int32: the tokens that each request holds, then the
     number of free pages. All of it lives on the GPU, and so a captured step can go
-    on handing out pages."""
+    on handing out pages.
+
+    A page has one owner: the stack, or one entry of one request's ceil(tokens / page_size)
+    first. A page in two of them (a prefix that requests share) would come back twice, and
+    then have two owners; such pages belong to the caller, in tables of its own. Pages come
+    back when their request leaves. A caller who gives some back before (those behind a
+    window, or of drafted tokens that are rejected) changes all three tensors together: the
+    page goes to stack[state[-1]], state[-1] grows by one, and the entry becomes -1, or lies
+    behind the tokens that are left in state[b]. Lowering state[b] alone loses the pages
+    behind."""
 
     def __init__(self, table, stack, state, page_size):
         if table.dim() != 2 or stack.dim() != 1 or state.dim() != 1:

@@ -794,6 +794,10 @@ MOE_API int moe_paged_attention(const moe_kv_cache* cache, const uint16_t* q,
  *   block_table (entries of pages taken) and stack (from its end on) are written in
  *   place, state is not: the call can be repeated. The outputs must not overlap the
  *   inputs. Entries outside [0, pages) on the stack give slots of -1.
+ *   A page has one owner: the stack, or one of the ceil(h_b / page_size) first entries of
+ *   one request. Pages that requests share must stay out of these tables, as each of
+ *   them would give them back. Pages given back by the caller go to stack[state[batch]], with
+ *   state[batch] grown and their entries made -1 or left behind a smaller h_b.
  * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, batch, pages, page_size or
  *         max_pages < 1, table_stride < max_pages, rows < 0, axes outside 1..8),
  *         MOE_ERR_UNSUPPORTED (batch > 4096, page_size not a power of two <= 1024, 2^31
