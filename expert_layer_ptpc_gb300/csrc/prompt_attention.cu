@@ -16,9 +16,11 @@
 // where that is more.
 //
 // What the tensor cores multiply: e4m3 codes in fp16, which holds them; a page's scale goes
-// into them, relative to the tile's largest (exact where it is a power of two, as the
-// framework's writes make it, else a rounding to 11 bits of the scale and one of the
-// product; what is 2^-31 of the tile's largest becomes 0), a token's scale, relative to the
+// into them, relative to the tile's largest, brought to 2^6 (exact where it is a power of two,
+// as the framework's writes make it, else a rounding to 11 bits of the scale and one of the
+// product; codes go down to 2^-9 and fp16 to 2^-24, so that all is exact down to 2^-21 of
+// the largest, off by up to 2^-31 of it below, and 0 from 2^-31 on; the largest is over all
+// tokens that the item loads, whether a row sees them or not), a token's scale, relative to the
 // largest too, into the score's column (keys) or, rounded to fp16, into the value. q in fp16, scaled by a power of two that
 // brings its head's largest element into [2^8, 2^9): exact down to 2^-25 of that, below
 // that off by up to 2^-33. A bf16 cache: q, k and v as they are, the weights rounded to

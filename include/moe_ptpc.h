@@ -830,13 +830,17 @@ MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int bat
  *   moe_paged_attention.
  *   Sums, maxima and accumulators are fp32; results do not depend on timing. What the
  *   tensor cores multiply has fewer bits:
- *   - e4m3 caches: codes in fp16, exactly; a page's scale in them (exactly for a power of
- *     two, else off by 2^-11 and the product by 2^-11; a code times a scale 2^-31 of the
- *     largest of its 128 tokens, 64 with head_dim 256, counts as 0), a token's scale of a
- *     value rounded into it (2^-11). q in fp16, its head's largest element scaled into
- *     [2^8, 2^9): off by up to 2^-33 of that element. Weights in fp16: off by up to 2^-11
- *     of each, or 2^-32 of the row's largest where that is more. Scales below 2^-85 lose
- *     bits.
+ *   - e4m3 caches: a code and a page's scale as one fp16 number, exactly for a power of two,
+ *     else the scale off by 2^-11 and the product by 2^-11; a code of a value and its token's
+ *     scale as well, off by 2^-11 (a key's token scale goes to the score in fp32). These
+ *     numbers are relative to the largest scale of 128 tokens (64 with head_dim 256), from a
+ *     multiple of 128 on: they are exact down to scales of 2^-21 of it, off by up to 2^-31 of
+ *     it below, and pages' scales from 2^-31 of it on count as 0. It is the largest of all
+ *     tokens that any of up to 256 rows (new tokens x heads) of the context sees, also
+ *     where a row does not see them itself (later new tokens, or tokens before its window).
+ *     Scales below 2^-85 lose bits too. q in fp16, its head's largest element scaled into
+ *     [2^8, 2^9): off by up to 2^-33 of that element. Weights in fp16: off by up to 2^-11 of
+ *     each, or 2^-32 of the row's largest where that is more.
  *   - bf16 cache: q, k and v exactly; weights in bf16, off by up to 2^-8 of each.
  *   Every wait inside is bounded (1 s, and 20 us for every 128 tokens that one of 152 CTAs
  *   can have to go through, with contexts as long as the tables' room); one that runs out

@@ -93,18 +93,19 @@ def test_nan_of_the_cache_reaches_every_row_that_sees_it(kind, which):
 # ---------------------------------------------------------------------------
 # page scales that are no powers of two
 # ---------------------------------------------------------------------------
-def bounds(cache, q, table, lengths, news, score=0.0, value=0.0, weight=2.0 ** -11, window=0):
+def bounds(cache, q, table, lengths, news, score=0.0, value=0.0, weight=2.0 ** -11, window=0,
+           more=0.0):
     """The oracle's out and lse, with what attention of many tokens may be off from them
     over an e4m3 cache: as in test_gpu_prompt_attention, with every product of q and a key off by
-    `score` of it more, and every value by `value` of it."""
+    `score` of it more and every score by `more`, and every value by `value` of it."""
     offsets = np.concatenate([[0], np.cumsum(news)])
     kc, vc, ks, vs = host(cache)
     d, n = cache.head_dim, max(max(lengths), 1)
     ref, lse, spread, reach, mass = oracle.prompt_attention_ref(
         values(q), kc, vc, ks, vs, table, lengths, offsets,
         np.float32(d ** -0.5).astype(np.float64), window)
-    e = ((2 * (d + 8) + 4) * U32 + 2.0 ** -18 + score) * reach
-    rel = np.expm1(2 * e) + 2 * n * U32 + weight + value
+    e = ((2 * (d + 8) + 4) * U32 + 2.0 ** -18 + score) * reach + more
+    rel = np.expm1(np.minimum(2 * e, 50.0)) + 2 * n * U32 + weight + value
     tol = HALF_BF16 * np.abs(ref) + rel[..., None] * spread + 2.0 ** -32 * mass
     lse_tol = e + 2 * n * U32 + 4 * U32 * (1 + np.abs(np.where(np.isneginf(lse), 0, lse)))
     return ref, lse, tol, lse_tol
@@ -300,3 +301,35 @@ def test_padding_follows_the_lengths_of_a_captured_step():
         cache.attend_prompt(q, o, t, n, out=want[0], lse=want[1])
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
         assert torch.all(out[end:] == 0) and torch.all(torch.isneginf(lse[end:]))
+
+
+# ---------------------------------------------------------------------------
+# scales far above a row's own, in tokens that it does not see
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("window", [0, 12])
+@pytest.mark.parametrize("gap", [10, 21, 22, 24, 27, 30, 31, 34])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scales_far_above_a_rows_own(d, gap, window):
+    """Tokens from the 48th on (without a window: later ones; with one: the rows behind come to see
+    them alone) with page scales 2^gap above those before, in one tile: rows that see the small
+    ones only are within what the header states, exact up to 2^21, and see zeros from 2^31 on."""
+    lengths, news, size = [60], [60], 16
+    cache, q, table = prompt_case(gap, lengths, news, 4, 2, d, size, "e4m3_page", spread=0.0)
+    for s in (cache.k_scale, cache.v_scale):
+        s.fill_(2.0 ** -6)
+        s[torch.from_numpy(table[0, 3:]).long().cuda()] = 2.0 ** (gap - 6)
+    out, lse = cache.attend_prompt(q, ints([0, 60]), torch.from_numpy(table).cuda(), ints(lengths),
+                                   window=window, return_lse=True)
+    # a rounding of fp16 numbers down to 2^-24 that stand for scales 2^-6 of theirs
+    off = 2.0 ** -25 * 2.0 ** (gap - 6 - 6) if gap > 21 else 0.0
+    # (elements of 2^-31 of the largest scale and below: codes up to 448 times that)
+    off = 448 * 2.0 ** -6 if gap >= 31 else off
+    most = np.abs(values(q)).sum(-1) * d ** -0.5 * off
+    ref, ref_lse, tol, lse_tol = bounds(cache, q, table, lengths, news, window=window, more=most)
+    small = np.arange(60) < 48
+    y, z = values(out)[small], lse.cpu().numpy()[small]
+    if gap >= 31:
+        assert np.all(y == 0)
+        return
+    assert np.all(np.abs(y - ref[small]) <= tol[small] + 1.01 * off)
+    assert np.all(np.abs(z - ref_lse[small]) <= lse_tol[small])
