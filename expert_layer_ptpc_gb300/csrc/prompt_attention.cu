@@ -417,7 +417,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared
     if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
     if ((spin & 63u) == 63u) {
       bool bail = *reinterpret_cast<volatile int*>(&sh.abort) != 0;
-      if (!bail && global_timer_ns() - t0 > a.wait_ns) {
+      if (lane_id() == 0 && !bail && global_timer_ns() - t0 > a.wait_ns) {   // (one tells all)
         *reinterpret_cast<volatile int*>(&sh.abort) = 1;
         atomicOr(a.err, code);
         bail = true;
