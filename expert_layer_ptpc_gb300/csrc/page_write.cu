@@ -22,7 +22,7 @@
 // was read, 16 warps an SM and 42 us). Behind a rotation by the angles: a block works a run's
 // out once for up to four of k's heads. q is rotated by a launch of its own (28 us with 64
 // heads and 6146 tokens), which runs beside this one's last blocks: 49 us together with 4
-// heads of k and v (53 with the angles worked out for each head).
+// heads of k and v (59 one after the other; 53 with the angles worked out for each head).
 #include <algorithm>
 
 #include "attention.h"
@@ -268,7 +268,9 @@ cudaError_t launch(const RotaryArgs& a, bool neighbours, cudaStream_t stream) {
   const int64_t work = (int64_t)a.T * 2 * a.k_heads, teams = 16384 / TEAM;
   const int part = (int)std::min<int64_t>(kMostTokens, std::max<int64_t>(1, work / teams));
   // heads of k that share the angles: as long as the runs of full pages are still one a team
-  // and SM (GB300, 6146 tokens of 4 heads of 128 in pages of 64)
+  // and SM (GB300, pages of 64 tokens of 128 elements, all heads at once against one: 4 heads of
+  // 900 tokens 34 and 23 us, of 9216 69 and 80; 8 heads of 2997 47 and 41 (37 by this rule), of
+  // 23998 220 and 278)
   const int64_t runs = std::max<int64_t>(1, a.T >> a.page_shift);
   const int at_once =
       a.rot == 0 ? 1

@@ -21,9 +21,9 @@
 // product; codes go down to 2^-9 and fp16 to 2^-24, so that all is exact down to 2^-21 of
 // the largest, off by up to 2^-31 of it below, and 0 from 2^-31 on; the largest is over all
 // tokens that the item loads, whether a row sees them or not), a token's scale, relative to the
-// largest too, into the score's column (keys) or, rounded to fp16, into the value. q in fp16, scaled by a power of two that
-// brings its head's largest element into [2^8, 2^9): exact down to 2^-25 of that, below
-// that off by up to 2^-33. A bf16 cache: q, k and v as they are, the weights rounded to
+// largest too, into the score's column (keys) or, rounded to fp16, into the value. q in fp16,
+// scaled by a power of two that brings its head's largest element into [2^8, 2^9): exact down
+// to 2^-25 of that, below that off by up to 2^-33. A bf16 cache: q, k and v as they are, the weights rounded to
 // bf16 (8 bits): the values' own products have no more, and a second product for the
 // rest of a weight would cost half as much again.
 //
@@ -32,7 +32,7 @@
 // values; 16 issues the products, 17 hands out the work. While one half's softmax runs, the
 // other half's products do. (In a cut item of up to 128 rows the halves take every other tile of
 // the same rows.) Loading warps turn codes into fp16 in registers: a lane asks for
-// a piece of the next tile as it lays the last one's out, and the rows of the tile after
+// a piece of the next tile as it lays the last one's out, and the rows of the three tiles after
 // that are on their way to L2. (Copies straight into shared memory, with the codes turned
 // there, would pass 32 KB a tile more through it, which the products' operands already fill
 // three quarters of the time that the products take.)
@@ -44,7 +44,7 @@
 //
 // GB300, 64 heads on 4 of 128 elements, a scale a page: a prompt of 8192 tokens 1015 us, 1.08
 // PFLOP/s of cuBLAS's 1.95; 2048 tokens over 40001 with a scale a token 2.75 ms, 0.95 PFLOP/s;
-// 5 tokens of each of 32 requests over up to 16384 (272 MB) 120 us, 2.3 TB/s, which the loading
+// 5 tokens of each of 32 requests over up to 16384 (272 MB) 122 us, 2.2 TB/s, which the loading
 // warps bound (2800 cycles a tile). The tensor
 // pipe is 47% busy; what bounds it is the turn of a half: its softmax (about 2500 cycles a
 // tile, of 512 that the exponentials take: loads from TMEM and issue slots shared with the
@@ -83,20 +83,26 @@ constexpr int kSides = 8;                  // tiles whose masks and factors are 
 constexpr int kRequests = 256;             // contexts whose places a CTA keeps at hand
 constexpr float kMostWeight = 15.0f;       // log2 of the largest weight let stand,
 constexpr float kNewWeight = 7.0f;         // and of a tile's largest when M is set by it
-// What an item costs beside its tiles, in tiles of 128 tokens, and the least that a
-// CTA is given.
+// What an item costs beside its tiles, in tiles of 128 tokens: 48 short items of a window (the
+// packed prompts) take 164 us with 2, 168 with 4 and 176 with 8, drafts 147, 121 and 117, 32 ragged
+// chunks of up to 100 tokens 211, 164 and 162. And the least that a CTA is given: 4 tokens over
+// 16384 take 67 us with 2, 68 with 4 and 50 with 8 (fewer pieces to join), four chunks of 40
+// tokens 34, 39 and 47, nine short prompts 40, 39 and 48.
 constexpr int kItemCost = 4;
 constexpr int kLeastWork = 4;
 // What a wait is given, beside kWaitLimitNs, for each 128 tokens of the longest run that a
 // CTA can have: its halves can be a ring of segments apart, so that one waits for most of the
 // run (2 to 3 us each).
 constexpr double kWaitNsOfTile = 20000.0;
+constexpr double kMostWaitNs = 1e11;
 
 constexpr int kLeastExponent = -64;        // E and F as of scales of 2^-64 at least (sums end at 2^128)
 
 enum Kind { kPageScales = 0, kTokenScales = 1, kBf16 = 2 };
 enum Mode { kOne = 0, kTilesEach = 1, kRowsEach = 2 };
-constexpr int kLeastTiles = 4;             // of a segment whose halves share its tiles out
+// Tiles of a segment whose halves share them out: drafts take 121 us with 2 and 4 and 125 with 8,
+// 4 tokens over 16384 68, 68 and 58, four chunks of 40 tokens 40, 39 and 37.
+constexpr int kLeastTiles = 4;
 
 struct Args {
   CacheView c;
@@ -1396,7 +1402,8 @@ int launch_prompt_attention(const CacheView& c, const uint16_t* q, int64_t q_str
   const double work = items * (room * group / 128 + (double)rows * group / 128 + 8.0 * group);
   if (work > 0x1p46) return -2;
   Args a{};
-  a.wait_ns = kWaitLimitNs + (unsigned long long)(work / group / kWorkers * kWaitNsOfTile);
+  a.wait_ns = kWaitLimitNs +
+              (unsigned long long)std::min(work / group / kWorkers * kWaitNsOfTile, kMostWaitNs);
   a.c = c;
   a.q = q;
   a.q_stride = q_stride;

@@ -843,8 +843,8 @@ MOE_API int moe_kv_plan(const int32_t* state, const int32_t* new_tokens, int bat
  *     each, or 2^-32 of the row's largest where that is more.
  *   - bf16 cache: q, k and v exactly; weights in bf16, off by up to 2^-8 of each.
  *   Every wait inside is bounded (1 s, and 20 us for every 128 tokens that one of 152 CTAs
- *   can have to go through, with contexts as long as the tables' room); one that runs out
- *   is reported by moe_device_status().
+ *   can have to go through, with contexts as long as the tables' room, up to 100 s); one that
+ *   runs out is reported by moe_device_status().
  * Errors: those of the cache; MOE_ERR_INVALID_ARG (null or misaligned pointers, q_heads
  *         not a multiple of heads, bad strides, scale not finite, rows or batch < 0,
  *         max_pages < 0, table_stride < max_pages, window < 0), MOE_ERR_UNSUPPORTED (batch
