@@ -713,6 +713,23 @@ def _need_heads(t, heads, head_dim, name, index):
     return stride if n > 1 else h * d
 
 
+def _tokens_overlap(a, a_stride, b, b_stride, rows, width):
+    """Whether two bf16 tensors of `rows` tokens of `width` elements share any, from their
+    addresses and strides. (Of different strides, only ranges that meet by the first or last
+    token are found out: tokens between them may lie side by side.)"""
+    if rows == 0:
+        return False
+    if a > b:
+        a, a_stride, b, b_stride = b, b_stride, a, a_stride
+    ahead, width, stride = b - a, 2 * width, 2 * a_stride
+    if ahead >= (rows - 1) * stride + width:
+        return False
+    past = ahead % stride if rows > 1 else ahead
+    if a_stride != b_stride:
+        return past < width
+    return past < width or (stride - past < width and ahead // stride + 1 < rows)
+
+
 def _need_slots(slots, T, index):
     _need_on(slots, torch.int32, "slots", index)
     if slots.numel() != T:
@@ -964,7 +981,7 @@ def moe_prompt_attention(cache, q, offsets, block_table, lengths, scale, window=
         out_stride = _need_heads(out, hq, d, "out", index)
         if out.shape[0] != rows:
             raise ValueError(f"out must have {rows} tokens, got {out.shape[0]}")
-        if out.data_ptr() == q.data_ptr() and rows:
+        if _tokens_overlap(q.data_ptr(), q_stride, out.data_ptr(), out_stride, rows, hq * d):
             raise ValueError("out must not overlap q")
     if lse is not None:
         _need_on(lse, torch.float32, "lse", index)
